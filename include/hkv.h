@@ -374,6 +374,90 @@ hkv_status hkv_move_chunks_noalloc(const hkv_layout* layout, int32_t op, void* p
                                    const hkv_chunk_batch* batch, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The decode step over the pool: operators that read and update the pages
+ * in place, for one new token per sequence.
+ *
+ * Unlike the copies above, their block tables, block ids and lengths are
+ * DEVICE arrays, as a decode loop keeps them, so a captured call follows them
+ * from replay to replay.  Their contents therefore cannot be checked on the
+ * host: a kernel never reads or writes through an id outside the pool or past
+ * a table's end, and each call says what becomes of a sequence with such a
+ * value.  Everything else is checked on the host before anything is enqueued.
+ * The calls allocate nothing, synchronise nothing, enqueue only kernel
+ * launches on the caller's stream and may all be captured into a HIP graph.
+ * A workspace may be shared by calls and by captured graphs that the stream
+ * runs one after another, not by ones that may run at once; nothing in it
+ * has to be kept or cleared between calls.
+ * ------------------------------------------------------------------------ */
+
+#define HKV_BF16 0
+#define HKV_FP16 1
+#define HKV_FP32 2
+#define HKV_E4M3 3 /* OCP fp8 e4m3 (no infinities) */
+
+/* MLA attention of one new token per sequence over one layer's paged latent
+ * cache.  A cached row k_t has mla_width values of which the first
+ * value_width are also its value v_t (an MLA layer caches the latent and the
+ * rotary part as one row: vLLM hybrid KV-cache blog, section 4.2, the
+ * (num_blocks, N, 576) view); the query is already multiplied into the
+ * latent space, so every head reads the same rows:
+ *   s_ht = scale x cache_scale x sum_w q_hw k_tw          (fp32)
+ *   lse_h = ln sum_t exp(s_ht),  p_ht = exp(s_ht - lse_h)
+ *   out_hv = cache_scale x sum_t p_ht k_tv, v < value_width
+ * over the tokens t < seq_lens[s] whose block is not HKV_NULL_BLOCK.  Token t
+ * is row t % N of block block_table[s][t / N].  The new token's own row must
+ * be in the cache already (seq_lens counts it).
+ * A sequence with no such token gets zeros and lse = -infinity. */
+typedef struct hkv_mla_attend_args {
+  int32_t layer;             /* an MLA layer */
+  int32_t n_seqs;            /* 0..65535; 0 is a no-op */
+  int32_t n_heads;           /* 1..128 query heads */
+  int32_t value_width;       /* a multiple of 16, at most 512 and at most mla_width */
+  int32_t dtype;             /* of q and out: HKV_BF16 or HKV_FP16 */
+  int32_t cache_dtype;       /* mla_bytes = 2: the same as dtype; 1: HKV_E4M3 */
+  int32_t max_blocks;        /* entries of a block_table row, >= 1 */
+  float scale;               /* softmax scale */
+  float cache_scale;         /* what a cached 1.0 stands for (1 unless e4m3) */
+  const void* q;             /* DEVICE [n_seqs][n_heads][mla_width] */
+  int64_t q_seq_stride;      /* elements; multiples of 8, >= 0 */
+  int64_t q_head_stride;
+  const int32_t* block_table; /* DEVICE [n_seqs][max_blocks] block ids of the layer's KV
+                                group, or HKV_NULL_BLOCK; entries past a sequence's end are
+                                not read.  A block may appear in several sequences */
+  int64_t table_stride;      /* elements between its rows, >= 0 */
+  const int32_t* seq_lens;   /* DEVICE [n_seqs] tokens, 0..max_blocks x N */
+  void* out;                 /* DEVICE [n_seqs][n_heads][value_width]; rows must not overlap */
+  int64_t out_seq_stride;    /* elements; multiples of 8 */
+  int64_t out_head_stride;
+  float* lse;                /* DEVICE [n_seqs][n_heads], or NULL */
+  float* weights;            /* DEVICE [n_seqs][weights_stride], or NULL: weights[s][t] +=
+                                sum_h p_ht for t < seq_lens[s] (what hkv_mla_evict reads);
+                                other entries are left as they were */
+  int64_t weights_stride;    /* elements, >= max_blocks x N */
+} hkv_mla_attend_args;
+
+/* Device workspace bytes of a call with these shapes (n_seqs, n_heads,
+ * value_width, max_blocks and whether weights is given; pointers are not
+ * read).  With weights it holds one fp32 per head and token of the table.
+ * Errors: HKV_E_ARG. */
+hkv_status hkv_mla_attend_workspace(const hkv_layout* layout, const hkv_mla_attend_args* args,
+                                    size_t* bytes);
+
+/* Enqueues the attention (see above).  pool: DEVICE as for hkv_store_chunks,
+ * only read.  Needs mla_width a multiple of 32 of at most 576 and mla_bytes 1
+ * or 2.  q, out and the workspace are 16-byte aligned, the other arrays by
+ * their element; out, lse, weights and the workspace must not overlap any
+ * other buffer of the call.  The result of a call depends on its inputs alone
+ * (no atomics).  A sequence that names a live block id outside [0,
+ * num_blocks) gets NaN in out, lse and its weights; one whose length is
+ * outside [0, max_blocks x N] gets NaN in out and lse, and its weights are
+ * left as they were.
+ * Errors: HKV_E_ARG, HKV_E_ALIAS, HKV_E_ALIGN, HKV_E_WORKSPACE, HKV_E_HIP. */
+hkv_status hkv_mla_attend(const hkv_layout* layout, const void* pool,
+                          const hkv_mla_attend_args* args, void* workspace, size_t ws_bytes,
+                          void* stream);
+
+/* ------------------------------------------------------------------------
  * Object identity.  Cached pages are byte-opaque, so an entry must never be
  * read back by an engine whose object format differs: other attention
  * backends or kernel block sizes ("Kimi-Linear", "Kimi K3" recipes and

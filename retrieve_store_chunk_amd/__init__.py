@@ -81,6 +81,24 @@ HKV_OP_STORE = 0
 HKV_OP_RETRIEVE = 1
 
 
+HKV_BF16 = 0
+HKV_FP16 = 1
+HKV_FP32 = 2
+HKV_E4M3 = 3
+
+f32 = ctypes.c_float
+
+
+class hkv_mla_attend_args(ctypes.Structure):
+    """Pointers are integer device addresses (0 = NULL)."""
+    _fields_ = [("layer", i32), ("n_seqs", i32), ("n_heads", i32), ("value_width", i32),
+                ("dtype", i32), ("cache_dtype", i32), ("max_blocks", i32), ("scale", f32),
+                ("cache_scale", f32), ("q", vp), ("q_seq_stride", i64), ("q_head_stride", i64),
+                ("block_table", vp), ("table_stride", i64), ("seq_lens", vp), ("out", vp),
+                ("out_seq_stride", i64), ("out_head_stride", i64), ("lse", vp),
+                ("weights", vp), ("weights_stride", i64)]
+
+
 def one_hip_runtime() -> None:
     """A process must hold one HIP runtime.  PyTorch-ROCm ships its own copy,
     which its libraries load by file name; if libhkv.so were loaded first it
@@ -126,6 +144,12 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.hkv_chunk_keys.argtypes = [vp, ctypes.POINTER(i32), i64, i32, u64, u64,
                                  ctypes.POINTER(u64), ctypes.POINTER(u64), i32,
                                  ctypes.POINTER(i64)]
+    L.hkv_mla_attend_workspace.restype = i32
+    L.hkv_mla_attend_workspace.argtypes = [vp, ctypes.POINTER(hkv_mla_attend_args),
+                                           ctypes.POINTER(ctypes.c_size_t)]
+    L.hkv_mla_attend.restype = i32
+    L.hkv_mla_attend.argtypes = [vp, vp, ctypes.POINTER(hkv_mla_attend_args), vp,
+                                 ctypes.c_size_t, vp]
     L.hkv_last_error.restype = ctypes.c_char_p
     L.hkv_last_error.argtypes = []
     return L
@@ -303,6 +327,19 @@ def hkv_move_chunks_noalloc(handle: int, op: int, pool_ptr: int, block_ids, obje
     del keep
 
 
+def hkv_mla_attend_workspace(handle: int, args: hkv_mla_attend_args) -> int:
+    out = ctypes.c_size_t()
+    _check(lib.hkv_mla_attend_workspace(handle, ctypes.byref(args), ctypes.byref(out)),
+           "hkv_mla_attend_workspace")
+    return out.value
+
+
+def hkv_mla_attend(handle: int, pool_ptr: int, args: hkv_mla_attend_args, workspace_ptr: int,
+                   ws_bytes: int, stream: int = 0) -> None:
+    _check(lib.hkv_mla_attend(handle, pool_ptr, ctypes.byref(args), workspace_ptr, ws_bytes,
+                              stream), "hkv_mla_attend")
+
+
 def status_of(fn, *args) -> int:
     """Calls one of the wrappers above and returns its status instead of
     raising (for tests of error paths)."""
@@ -363,3 +400,9 @@ class Layout:
     def move_noalloc(self, op, pool_ptr, block_ids, objects, stream=0, chunk_tokens=None):
         hkv_move_chunks_noalloc(self.handle, op, pool_ptr, block_ids, objects, stream,
                                 info=self.info, chunk_tokens=chunk_tokens)
+
+    def mla_attend_workspace(self, args: hkv_mla_attend_args) -> int:
+        return hkv_mla_attend_workspace(self.handle, args)
+
+    def mla_attend(self, pool_ptr, args: hkv_mla_attend_args, ws_ptr, ws_bytes, stream=0):
+        hkv_mla_attend(self.handle, pool_ptr, args, ws_ptr, ws_bytes, stream)

@@ -28,28 +28,23 @@
 #include "hkv.h"
 #include "hkv_device_tables.hpp"
 #include "hkv_groups.hpp"
+#include "hkv_handle.hpp"
 #include "hkv_launch.hpp"
 #include "hkv_plan.hpp"
 #include "hkv_scratch.hpp"
 
-struct hkv_layout {
-  hkv::Plan plan;
-  // The plan's constant tables as the kernels read them: layer placements
-  // (padded to 256 bytes), then the per-chunk work items.
-  std::vector<uint8_t> table_image;
-  // Never reused by another layout of the process: names the tables that the
-  // static scratch of hkv_move_chunks_noalloc holds.
-  uint64_t serial = 0;
-  // The constant tables in the memory of each device the layout has been
-  // used on, uploaded by the first call there and freed with the layout.
-  mutable std::mutex mu;
-  mutable std::map<int, void*> dev_tables;
-  ~hkv_layout();
-};
+using hkv::aligned16;
+using hkv::DeviceScope;
+using hkv::hip_error;
+using hkv::set_error;
+using hkv::stream_device;
+using hkv::trace_on;
 
 namespace {
-
 thread_local std::string t_last_error;
+}  // namespace
+
+namespace hkv {
 
 hkv_status set_error(hkv_status st, const std::string& msg) {
   t_last_error = msg;
@@ -61,10 +56,6 @@ hkv_status hip_error(hipError_t e, const char* what) {
                                   hipGetErrorString(e) + ")");
 }
 
-// HKV_TRACE=1 in the environment: one line on stderr per layout and per
-// call (the layout's N, chunk size and placements; a call's chunks, launches,
-// work items and bytes), like the engine's own log line naming the block size
-// it settled on.
 bool trace_on() {
   static const bool on = [] {
     const char* v = std::getenv("HKV_TRACE");
@@ -72,6 +63,15 @@ bool trace_on() {
   }();
   return on;
 }
+
+hkv_status stream_device(hipStream_t stream, int* dev) {
+  const hipError_t e = stream ? hipStreamGetDevice(stream, dev) : hipGetDevice(dev);
+  return e == hipSuccess ? HKV_OK : hip_error(e, "finding the stream's device");
+}
+
+}  // namespace hkv
+
+namespace {
 
 // ---------------------------------------------------------------- staging
 // A few pinned host buffers per device, used round-robin.  Each remembers
@@ -100,27 +100,6 @@ Ring* ring_for(int dev) {
   auto& r = (*g_rings)[dev];
   if (!r) r.reset(new Ring());
   return r.get();
-}
-
-// Makes `dev` current for the scope, restoring the previous device after.
-struct DeviceScope {
-  int prev = -1;
-  hipError_t err = hipSuccess;
-  explicit DeviceScope(int dev) {
-    err = hipGetDevice(&prev);
-    if (err == hipSuccess && prev != dev) err = hipSetDevice(dev);
-  }
-  ~DeviceScope() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
-
-// The device a call's work goes to: the stream's, or the current one for
-// the default stream.
-hkv_status stream_device(hipStream_t stream, int* dev) {
-  const hipError_t e = stream ? hipStreamGetDevice(stream, dev) : hipGetDevice(dev);
-  return e == hipSuccess ? HKV_OK : hip_error(e, "finding the stream's device");
 }
 
 // Copies `bytes` bytes of `fill`-written staging into `dst` on `stream`
@@ -169,8 +148,6 @@ hkv_status upload(int dev, void* dst, size_t bytes, hipStream_t stream, Fill fil
 }
 
 // ---------------------------------------------------------------- validation
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 struct Span {
   uintptr_t lo, hi;
   const char* what;

@@ -1,0 +1,277 @@
+// C ABI of the operators that read and update the pool in place (declared in
+// include/hkv.h): MLA attention.  Every call checks its arguments on the
+// host, then enqueues kernel launches on the caller's stream; none allocates
+// or synchronises.
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <exception>
+#include <string>
+
+#include "hkv.h"
+#include "hkv_handle.hpp"
+#include "hkv_ops.hpp"
+
+using hkv::aligned16;
+using hkv::DeviceScope;
+using hkv::hip_error;
+using hkv::set_error;
+using hkv::stream_device;
+using hkv::trace_on;
+
+namespace {
+
+// Nothing may leave a C entry point but a status.
+template <class F>
+hkv_status guarded(F f) {
+  try {
+    return f();
+  } catch (const std::exception&) {
+    return HKV_E_ARG;  // out of host memory while a message was put together
+  }
+}
+
+// A buffer of the call: [lo, lo + bytes).  `written`: it must not overlap any
+// other.
+struct Buffer {
+  const void* p;
+  uint64_t bytes;
+  bool written;
+  const char* what;
+};
+
+template <size_t N>
+hkv_status check_overlap(const Buffer (&b)[N]) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = i + 1; j < N; ++j) {
+      if (!b[i].p || !b[j].p || !b[i].bytes || !b[j].bytes) continue;
+      if (!b[i].written && !b[j].written) continue;
+      const uintptr_t x = reinterpret_cast<uintptr_t>(b[i].p);
+      const uintptr_t y = reinterpret_cast<uintptr_t>(b[j].p);
+      if (x < y + b[j].bytes && y < x + b[i].bytes)
+        return set_error(HKV_E_ALIAS, std::string(b[i].what) + " overlaps " + b[j].what);
+    }
+  return HKV_OK;
+}
+
+// Elements from a strided array's first to its last, plus one; -1 if that
+// overflows.  Strides are >= 0, counts >= 1.
+int64_t extent(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t inner) {
+  int64_t a = 0, b = 0, r = 0;
+  if (__builtin_mul_overflow(n0 - 1, s0, &a) || __builtin_mul_overflow(n1 - 1, s1, &b) ||
+      __builtin_add_overflow(a, b, &r) || __builtin_add_overflow(r, inner, &r) ||
+      r > (int64_t(1) << 58))
+    return -1;
+  return r;
+}
+
+// Whether rows of `inner` elements at i0 * s0 + i1 * s1 are disjoint: the
+// smaller stride steps over a row, the larger over all rows of the smaller.
+bool rows_disjoint(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t inner) {
+  if (n0 <= 1 && n1 <= 1) return true;
+  if (n0 <= 1) return s1 >= inner;
+  if (n1 <= 1) return s0 >= inner;
+  if (s0 > s1) {
+    std::swap(s0, s1);
+    std::swap(n0, n1);
+  }
+  return s0 >= inner && s1 >= extent(n0, s0, 1, 0, inner);
+}
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+hkv_status layer_of(const hkv::Plan& p, int32_t layer, bool mla, const hkv::LayerPlacement** out) {
+  if (layer < 0 || layer >= (int32_t)p.layers.size())
+    return set_error(HKV_E_ARG, "layer index out of range");
+  if ((p.layers[layer].is_mla != 0) != mla)
+    return set_error(HKV_E_ARG, std::string("layer ") + std::to_string(layer) + " is not " +
+                                    (mla ? "an MLA" : "a KDA") + " layer");
+  *out = &p.layers[layer];
+  return HKV_OK;
+}
+
+// The block table's shape and the pool's row geometry, as every MLA operator
+// needs them.
+hkv_status check_table(const hkv::Plan& p, int32_t n_seqs, int32_t max_blocks,
+                       int64_t table_stride) {
+  if (n_seqs < 0 || n_seqs > 65535) return set_error(HKV_E_ARG, "n_seqs must be in [0, 65535]");
+  if (max_blocks < 1) return set_error(HKV_E_ARG, "max_blocks must be >= 1");
+  if ((uint64_t)max_blocks * (uint64_t)p.block_size > 0x7FFFFFFFull)
+    return set_error(HKV_E_ARG, "max_blocks x N exceeds 2^31 - 1 tokens");
+  if (table_stride < 0) return set_error(HKV_E_ARG, "table_stride must be >= 0");
+  return HKV_OK;
+}
+
+// ---------------------------------------------------------------- attention
+// Two workgroups of the 16- and 32-head kernels fit a CU (their LDS), one of
+// the 64-head kernel.  Both head tiles of a batch of more than 64 heads run at
+// once, on the same XCD (a multiple of 8 apart), so that the second reads the
+// rows from L2.
+constexpr uint32_t kCus = 256;
+
+hkv_status plan_attend(const hkv_layout* layout, const hkv_mla_attend_args* a, bool weights,
+                       hkv::AttendArgs* k, hkv::AttendWorkspace* ws) {
+  const hkv::Plan& p = layout->plan;
+  const int64_t width = p.shapes[6], bytes = p.shapes[7];
+  if (bytes != 1 && bytes != 2)
+    return set_error(HKV_E_ARG, "attention needs mla_bytes 1 (e4m3) or 2 (bf16, fp16)");
+  if (width % 32 != 0 || width > hkv::kAttendMaxWidth)
+    return set_error(HKV_E_ARG, "attention needs an mla_width that is a multiple of 32 and at "
+                                "most " + std::to_string(hkv::kAttendMaxWidth));
+  hkv_status st = check_table(p, a->n_seqs, a->max_blocks, a->table_stride);
+  if (st != HKV_OK) return st;
+  if (a->n_heads < 1 || a->n_heads > 128)
+    return set_error(HKV_E_ARG, "n_heads must be in [1, 128]");
+  if (a->value_width < 16 || a->value_width % 16 != 0 ||
+      a->value_width > (int32_t)hkv::kAttendMaxValues || a->value_width > width)
+    return set_error(HKV_E_ARG, "value_width must be a multiple of 16, at most 512 and at most "
+                                "mla_width");
+  *k = hkv::AttendArgs{};
+  k->num_blocks = (uint32_t)p.num_blocks;
+  k->block_tokens = (uint32_t)p.block_size;
+  k->row_bytes = (uint32_t)(width * bytes);
+  k->width = (uint32_t)width;
+  k->values = (uint32_t)a->value_width;
+  k->n_seqs = (uint32_t)a->n_seqs;
+  k->n_heads = (uint32_t)a->n_heads;
+  k->head_tile = hkv::attend_head_tile(k->n_heads);
+  k->head_tiles = (k->n_heads + k->head_tile - 1) / k->head_tile;
+  k->max_blocks = (uint32_t)a->max_blocks;
+  const uint64_t tokens = (uint64_t)a->max_blocks * (uint64_t)p.block_size;
+  k->max_tiles = (uint32_t)((tokens + hkv::kAttendTile - 1) / hkv::kAttendTile);
+  const uint64_t tiles = (uint64_t)k->n_seqs * k->max_tiles;
+  if (tiles > 0x7FFFFFFFull)
+    return set_error(HKV_E_ARG, "n_seqs x max_blocks x N exceeds 2^36 tokens; split the batch");
+  const uint64_t fit = (k->head_tile == 64 ? 1 : 2) * kCus / k->head_tiles;
+  const uint64_t useful = (tiles + hkv::kAttendMinTiles - 1) / hkv::kAttendMinTiles;
+  k->workers = (uint32_t)std::max<uint64_t>(1, std::min(fit, useful));
+  *ws = hkv::attend_workspace(k->workers, k->head_tiles, k->head_tile, k->values, k->n_seqs,
+                              k->n_heads, k->max_tiles, weights);
+  return HKV_OK;
+}
+
+hkv_status attend(const hkv_layout* layout, const void* pool, const hkv_mla_attend_args* a,
+                  void* ws, size_t ws_bytes, void* stream) {
+  if (!layout || !a) return set_error(HKV_E_ARG, "layout and args must not be NULL");
+  const hkv::Plan& p = layout->plan;
+  const hkv::LayerPlacement* L = nullptr;
+  hkv_status st = layer_of(p, a->layer, true, &L);
+  if (st != HKV_OK) return st;
+  hkv::AttendArgs k;
+  hkv::AttendWorkspace w;
+  st = plan_attend(layout, a, a->weights != nullptr, &k, &w);
+  if (st != HKV_OK) return st;
+  const int64_t width = p.shapes[6], bytes = p.shapes[7];
+  if (a->dtype != HKV_BF16 && a->dtype != HKV_FP16)
+    return set_error(HKV_E_ARG, "dtype must be HKV_BF16 or HKV_FP16");
+  if (a->cache_dtype != (bytes == 1 ? HKV_E4M3 : a->dtype))
+    return set_error(HKV_E_ARG, bytes == 1 ? "a cache of 1-byte values must be HKV_E4M3"
+                                           : "a cache of 2-byte values must be of q's type");
+  if (!std::isfinite(a->scale) || !std::isfinite(a->cache_scale))
+    return set_error(HKV_E_ARG, "scale and cache_scale must be finite");
+  if (a->n_seqs == 0) return HKV_OK;
+  if (!pool || !a->q || !a->block_table || !a->seq_lens || !a->out)
+    return set_error(HKV_E_ARG, "pool, q, block_table, seq_lens and out must not be NULL");
+  if (a->q_seq_stride < 0 || a->q_head_stride < 0 || a->out_seq_stride < 0 ||
+      a->out_head_stride < 0)
+    return set_error(HKV_E_ARG, "strides must be >= 0");
+  const int64_t n = a->n_seqs, H = a->n_heads;
+  if (!rows_disjoint(n, a->out_seq_stride, H, a->out_head_stride, a->value_width))
+    return set_error(HKV_E_ALIAS, "the strides make rows of out overlap");
+  const int64_t tokens = (int64_t)a->max_blocks * p.block_size;
+  if (a->weights && a->weights_stride < tokens)
+    return set_error(HKV_E_ARG, "weights_stride must be >= max_blocks x N");
+  const int64_t q_ext = extent(n, a->q_seq_stride, H, a->q_head_stride, width);
+  const int64_t o_ext = extent(n, a->out_seq_stride, H, a->out_head_stride, a->value_width);
+  const int64_t t_ext = extent(n, a->table_stride, 1, 0, a->max_blocks);
+  const int64_t w_ext = extent(n, a->weights_stride, 1, 0, tokens);
+  if (q_ext < 0 || o_ext < 0 || t_ext < 0 || (a->weights && w_ext < 0))
+    return set_error(HKV_E_ARG, "strides are too large");
+  if (!ws || ws_bytes < w.total)
+    return set_error(HKV_E_WORKSPACE, "workspace needs " + std::to_string(w.total) + " bytes");
+  if (!aligned16(pool) || !aligned16(a->q) || !aligned16(a->out) || !aligned16(ws))
+    return set_error(HKV_E_ALIGN, "pool, q, out and workspace must be 16-byte aligned");
+  if ((a->q_seq_stride | a->q_head_stride | a->out_seq_stride | a->out_head_stride) % 8 != 0)
+    return set_error(HKV_E_ALIGN, "strides of q and out must be multiples of 8 elements");
+  if (L->pool_offset % 16 != 0 || L->stride % 16 != 0)
+    return set_error(HKV_E_ALIGN, "the layer's pages are not 16-byte aligned in this layout");
+  if (!aligned_to(a->block_table, 4) || !aligned_to(a->seq_lens, 4) || !aligned_to(a->lse, 4) ||
+      !aligned_to(a->weights, 4))
+    return set_error(HKV_E_ALIGN, "block_table, seq_lens, lse and weights must be 4-byte aligned");
+  const Buffer buffers[] = {
+      {pool, p.pool_used, false, "the pool"},
+      {a->q, (uint64_t)q_ext * 2, false, "q"},
+      {a->block_table, (uint64_t)t_ext * 4, false, "block_table"},
+      {a->seq_lens, (uint64_t)n * 4, false, "seq_lens"},
+      {a->out, (uint64_t)o_ext * 2, true, "out"},
+      {a->lse, (uint64_t)(n * H) * 4, true, "lse"},
+      {a->weights, a->weights ? (uint64_t)w_ext * 4 : 0, true, "weights"},
+      {ws, w.total, true, "the workspace"},
+  };
+  st = check_overlap(buffers);
+  if (st != HKV_OK) return st;
+
+  k.pages = static_cast<const uint8_t*>(pool) + L->pool_offset;
+  k.stride = L->stride;
+  k.q = a->q;
+  k.q_seq_stride = a->q_seq_stride;
+  k.q_head_stride = a->q_head_stride;
+  k.table = a->block_table;
+  k.table_stride = a->table_stride;
+  k.lens = a->seq_lens;
+  k.out = a->out;
+  k.out_seq_stride = a->out_seq_stride;
+  k.out_head_stride = a->out_head_stride;
+  k.lse = a->lse;
+  k.weights = a->weights;
+  k.weights_stride = a->weights_stride;
+  k.scale = a->scale * a->cache_scale;
+  k.cache_scale = a->cache_scale;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  k.part_o = reinterpret_cast<float*>(wsb + w.part_o);
+  k.part_ml = reinterpret_cast<float*>(wsb + w.part_ml);
+  k.spans = reinterpret_cast<int32_t*>(wsb + w.spans);
+  if (a->weights) {
+    k.norm = reinterpret_cast<float*>(wsb + w.norm);
+    k.logits = reinterpret_cast<float*>(wsb + w.logits);
+  }
+  int dev = 0;
+  st = stream_device(reinterpret_cast<hipStream_t>(stream), &dev);
+  if (st != HKV_OK) return st;
+  DeviceScope scope(dev);
+  if (scope.err != hipSuccess) return hip_error(scope.err, "selecting the stream's device");
+  const int e = hkv::launch_attend(k, a->dtype, a->cache_dtype, stream);
+  if (e != 0) return hip_error((hipError_t)e, "launching the attention kernels");
+  if (trace_on())
+    std::fprintf(stderr, "[hkv] hkv_mla_attend: layer %d, %d sequences of up to %lld tokens, "
+                 "%d heads, %u workers\n", a->layer, a->n_seqs, (long long)tokens, a->n_heads,
+                 k.workers);
+  return HKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+hkv_status hkv_mla_attend_workspace(const hkv_layout* layout, const hkv_mla_attend_args* args,
+                                    size_t* bytes) {
+  return guarded([&]() -> hkv_status {
+    if (!layout || !args || !bytes)
+      return set_error(HKV_E_ARG, "layout, args and bytes must not be NULL");
+    hkv::AttendArgs k;
+    hkv::AttendWorkspace w;
+    const hkv_status st = plan_attend(layout, args, args->weights != nullptr, &k, &w);
+    if (st == HKV_OK) *bytes = (size_t)w.total;
+    return st;
+  });
+}
+
+hkv_status hkv_mla_attend(const hkv_layout* layout, const void* pool,
+                          const hkv_mla_attend_args* args, void* workspace, size_t ws_bytes,
+                          void* stream) {
+  return guarded([&] { return attend(layout, pool, args, workspace, ws_bytes, stream); });
+}
+
+}  // extern "C"

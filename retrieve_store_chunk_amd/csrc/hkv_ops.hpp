@@ -1,0 +1,84 @@
+// Kernel argument blocks and host-side launches of the operators that read
+// and update the pool in place (MLA attention, eviction, the KDA step).
+// Shared by the host checks (hkv_ops.cpp) and the kernels (plain structs, no
+// HIP types).
+#pragma once
+
+#include <cstdint>
+
+#include "hkv_device_tables.hpp"
+
+namespace hkv {
+
+// ---------------------------------------------------------------- attention
+constexpr uint32_t kAttendTile = 32;        // cached tokens per step of a workgroup
+constexpr uint32_t kAttendMaxWidth = 576;   // values per cached row
+constexpr uint32_t kAttendMaxValues = 512;  // of them, values that are summed
+constexpr uint32_t kAttendMinTiles = 4;     // fewest tiles worth a worker of their own
+
+// One call's geometry as the host plans it and the kernels follow it.
+struct AttendArgs {
+  const uint8_t* pages;  // the layer's page of block 0
+  uint64_t stride;       // bytes between block ids
+  const void* q;         // [n_seqs][n_heads][width]
+  int64_t q_seq_stride, q_head_stride;  // elements
+  const int32_t* table;  // [n_seqs][max_blocks]
+  int64_t table_stride;
+  const int32_t* lens;   // [n_seqs]
+  void* out;             // [n_seqs][n_heads][values]
+  int64_t out_seq_stride, out_head_stride;
+  float* lse;            // [n_seqs][n_heads], natural log, or nullptr
+  float* weights;        // [n_seqs][weights_stride], or nullptr
+  int64_t weights_stride;
+  // workspace
+  float* part_o;         // [workers][head tiles][2][head tile][values]
+  float* part_ml;        // [workers][head tiles][2][head tile][2]: maximum, sum
+  int32_t* spans;        // [n_seqs][4]: first worker, last worker, slot of the first
+  float* norm;           // [n_seqs][n_heads] the lse that weights subtract (weights only)
+  float* logits;         // [n_seqs][max_tiles][n_heads][kAttendTile] (weights only)
+  float scale;           // softmax scale x cache scale
+  float cache_scale;
+  uint32_t num_blocks, block_tokens, row_bytes, width, values;
+  uint32_t n_seqs, n_heads, head_tile, head_tiles, max_blocks, workers;
+  uint32_t max_tiles;    // tiles of the longest sequence the table can hold
+};
+
+// Heads one workgroup takes: 16, 32 or 64, the least that holds all of them
+// (a wider tile reads the cache fewer times; a narrower one wastes less of
+// the matrix instructions' 16-head columns).
+inline constexpr uint32_t attend_head_tile(uint32_t n_heads) {
+  return n_heads <= 16 ? 16u : n_heads <= 32 ? 32u : 64u;
+}
+
+// Tiles per worker: an even share of all tiles, but no fewer than
+// kAttendMinTiles, so that short batches are not cut into more partial
+// results than their keys are worth.
+inline constexpr uint64_t attend_share(uint64_t tiles, uint64_t workers) {
+  const uint64_t s = (tiles + workers - 1) / workers;
+  return s < kAttendMinTiles ? kAttendMinTiles : s;
+}
+
+// Workspace sections, each on a 256-byte boundary.
+struct AttendWorkspace {
+  uint64_t part_o, part_ml, spans, norm, logits, total;
+};
+inline AttendWorkspace attend_workspace(uint64_t workers, uint64_t head_tiles, uint64_t head_tile,
+                                        uint64_t values, uint64_t n_seqs, uint64_t n_heads,
+                                        uint64_t max_tiles, bool weights) {
+  AttendWorkspace w{};
+  const uint64_t slots = workers * head_tiles * 2 * head_tile;
+  w.part_o = 0;
+  w.part_ml = w.part_o + align256(slots * values * sizeof(float));
+  w.spans = w.part_ml + align256(slots * 2 * sizeof(float));
+  w.norm = w.spans + align256(n_seqs * 4 * sizeof(int32_t));
+  w.logits = w.norm + (weights ? align256(n_seqs * n_heads * sizeof(float)) : 0);
+  w.total = w.logits +
+            (weights ? align256(n_seqs * max_tiles * n_heads * kAttendTile * sizeof(float)) : 0);
+  return w;
+}
+
+// Enqueues the attention of one call on `stream` (a hipStream_t).  dtype and
+// cache_dtype: HKV_BF16, HKV_FP16, HKV_E4M3.  Returns the hipError_t.
+int launch_attend(const AttendArgs& a, int32_t dtype, int32_t cache_dtype, void* stream);
+
+}  // namespace hkv
