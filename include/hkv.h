@@ -457,6 +457,114 @@ hkv_status hkv_mla_attend(const hkv_layout* layout, const void* pool,
                           const hkv_mla_attend_args* args, void* workspace, size_t ws_bytes,
                           void* stream);
 
+/* Eviction from the MLA cache by accumulated attention weight: cuts every
+ * sequence longer than `budget` down to `budget` tokens, in each of the given
+ * layers by that layer's own weights, and closes the gaps in place, so that
+ * the sequence's first ceil(budget / N) blocks hold what is kept and its other
+ * blocks are free.
+ * Per layer i and sequence s, of the slots t < seq_lens[s]:
+ *   kept:  slots whose position is below `sinks` or at least
+ *          next_positions[s] - recent, then those of the largest weights
+ *          (NaN counts as the least, below -infinity); ties go to the lowest
+ *          slot;
+ *   moved: the kept slots t >= budget, in order, into the dropped slots
+ *          t < budget, in order: row, weight and position.  No other row
+ *          moves, so after a first eviction slots are not ordered by
+ *          position; the attention does not depend on the order of its rows.
+ * weights_out and positions_out get the kept slots' values for t < budget, and
+ * 0 and -1 for budget <= t < seq_lens[s] (a token that is appended there later
+ * starts with no weight); shorter sequences' are copied.  Entries past
+ * seq_lens[s] are left as they were.  The arrays may be the inputs themselves;
+ * where they are not, the same call can be repeated: it finds its inputs
+ * unchanged and moves the same rows to the same places. */
+typedef struct hkv_mla_evict_args {
+  int32_t n_layers;          /* 1..64 */
+  const int32_t* layers;     /* HOST [n_layers] distinct MLA layers of one KV group (they
+                                share the block table) */
+  int32_t n_seqs;            /* 0..65535; 0 is a no-op */
+  int32_t max_blocks;        /* entries of a block_table row, >= 1 */
+  int32_t budget;            /* tokens to keep, >= 1 */
+  int32_t sinks;             /* >= 0, sinks + recent <= budget */
+  int32_t recent;            /* >= 0 */
+  const int32_t* block_table; /* DEVICE [n_seqs][max_blocks], as for hkv_mla_attend; the
+                                blocks of a sequence belong to it alone */
+  int64_t table_stride;      /* elements, >= 0 */
+  const int32_t* seq_lens;   /* DEVICE [n_seqs] tokens in the cache, 0..max_blocks x N */
+  const int32_t* next_positions; /* DEVICE [n_seqs] position the sequence's next token gets */
+  const float* weights;      /* DEVICE [n_layers][n_seqs][max_blocks x N] accumulated weights */
+  const int32_t* positions;  /* DEVICE, same shape: the position each slot's token had */
+  float* weights_out;        /* DEVICE, same shape and strides: == weights, or disjoint */
+  int32_t* positions_out;    /* DEVICE, same shape and strides: == positions, or disjoint */
+  int64_t layer_stride;      /* elements between layers and sequences of these four; rows */
+  int64_t seq_stride;        /*   must not overlap */
+  int32_t* new_lens;         /* DEVICE [n_seqs] or NULL: min(seq_lens[s], budget), or -1 for
+                                a sequence that was left as it was (below) */
+} hkv_mla_evict_args;
+
+/* Device workspace bytes of a call with these shapes (n_layers, n_seqs,
+ * max_blocks, budget; pointers are not read).  Errors: HKV_E_ARG. */
+hkv_status hkv_mla_evict_workspace(const hkv_layout* layout, const hkv_mla_evict_args* args,
+                                   size_t* bytes);
+
+/* Enqueues the eviction (see above).  Works on rows of any width as opaque
+ * bytes.  pool: DEVICE as for hkv_store_chunks; pool and workspace 16-byte
+ * aligned.  A sequence whose length is outside [0, max_blocks x N], or whose
+ * table holds HKV_NULL_BLOCK, an id outside [0, num_blocks) or a block that
+ * the call's tables name twice before its end, keeps its rows where they are:
+ * its weights and positions are copied unchanged (as far as its length is
+ * valid) and its new_lens entry is -1.
+ * Errors: HKV_E_ARG, HKV_E_ALIAS, HKV_E_ALIGN, HKV_E_WORKSPACE, HKV_E_HIP. */
+hkv_status hkv_mla_evict(const hkv_layout* layout, void* pool, const hkv_mla_evict_args* args,
+                         void* workspace, size_t ws_bytes, void* stream);
+
+/* One token's step of a KDA layer, from the state page of block src_blocks[s]
+ * to that of dst_blocks[s] (vLLM hybrid KV-cache blog, section 5.3: the
+ * retrieved state is the initial state; at a block boundary the next state
+ * goes to a new block, so the finished block's page stays as a snapshot).  A
+ * page is the conv state (conv_dim, kernel-1), oldest tap first, then the
+ * fp32 recurrent state S (heads, d, d), rows = key channels.  conv_dim is
+ * 3 x heads x d: the q, k and v channels of every head, in this order.
+ *   y      = silu(sum_j conv_weight_cj tap_cj + conv_weight_c,kernel-1 x_c)
+ *   q, k   = y's q and k parts over sqrt(sum of squares + eps) per head; q x scale
+ *   S'     = diag(exp(log_decay)) S
+ *   u      = beta (v - S'^T k)
+ *   S      = S' + k u^T,  out = S^T q
+ * in fp32; x becomes the conv state's newest tap.
+ * A source of HKV_NULL_BLOCK is a state of zeros (a request without a cached
+ * prefix); a destination of HKV_NULL_BLOCK is not written.  Source and
+ * destination may be the same block. */
+typedef struct hkv_kda_step_args {
+  int32_t layer;             /* a KDA layer */
+  int32_t n_seqs;            /* 0..4096; 0 is a no-op */
+  int32_t dtype;             /* of x, conv_weight and out, and the conv state's type:
+                                HKV_BF16 or HKV_FP16 (conv_bytes 2), HKV_FP32 (conv_bytes 4) */
+  float scale;               /* of q, e.g. d^-1/2 */
+  float eps;                 /* >= 0 */
+  const void* x;             /* DEVICE [n_seqs][conv_dim] */
+  int64_t x_stride;          /* elements, >= 0 */
+  const void* conv_weight;   /* DEVICE [conv_dim][conv_kernel] */
+  const float* log_decay;    /* DEVICE [n_seqs][heads x d] natural logs (<= 0 to decay) */
+  int64_t decay_stride;      /* elements, >= 0 */
+  const float* beta;         /* DEVICE [n_seqs][heads] */
+  int64_t beta_stride;       /* elements, >= 0 */
+  const int32_t* src_blocks; /* DEVICE [n_seqs] */
+  const int32_t* dst_blocks; /* DEVICE [n_seqs], may be src_blocks */
+  void* out;                 /* DEVICE [n_seqs][heads x d] */
+  int64_t out_stride;        /* elements, a multiple of 4, >= heads x d */
+} hkv_kda_step_args;
+
+/* Enqueues the step as one kernel, without a workspace (see above).  Needs
+ * kda_state_bytes 4, kda_head_dim 16, 32, 64, 128 or 256, conv_kernel 1..8,
+ * conv_dim = 3 x heads x d and a conv state of whole 16-byte units (the pages
+ * hold plain fp32 states in the pool whether or not kda_codec is set).  pool
+ * and out are 16-byte aligned, the other arrays by their element.
+ * A sequence with a block id that is neither HKV_NULL_BLOCK nor in [0,
+ * num_blocks), or whose destination another sequence of the call reads or
+ * writes, gets NaN in out and writes no page.
+ * Errors: HKV_E_ARG, HKV_E_ALIAS, HKV_E_ALIGN, HKV_E_HIP. */
+hkv_status hkv_kda_step(const hkv_layout* layout, void* pool, const hkv_kda_step_args* args,
+                        void* stream);
+
 /* ------------------------------------------------------------------------
  * Object identity.  Cached pages are byte-opaque, so an entry must never be
  * read back by an engine whose object format differs: other attention

@@ -99,6 +99,29 @@ class hkv_mla_attend_args(ctypes.Structure):
                 ("weights", vp), ("weights_stride", i64)]
 
 
+class hkv_mla_evict_args(ctypes.Structure):
+    """Pointers are integer device addresses (0 = NULL), but `layers`: set it
+    with set_layers, which keeps the host array alive."""
+    _fields_ = [("n_layers", i32), ("layers", ctypes.POINTER(i32)), ("n_seqs", i32),
+                ("max_blocks", i32), ("budget", i32), ("sinks", i32), ("recent", i32),
+                ("block_table", vp), ("table_stride", i64), ("seq_lens", vp),
+                ("next_positions", vp), ("weights", vp), ("positions", vp),
+                ("weights_out", vp), ("positions_out", vp), ("layer_stride", i64),
+                ("seq_stride", i64), ("new_lens", vp)]
+
+    def set_layers(self, layers) -> None:
+        self.n_layers = len(layers)
+        self.layers = (i32 * max(1, len(layers)))(*layers)
+
+
+class hkv_kda_step_args(ctypes.Structure):
+    """Pointers are integer device addresses (0 = NULL)."""
+    _fields_ = [("layer", i32), ("n_seqs", i32), ("dtype", i32), ("scale", f32), ("eps", f32),
+                ("x", vp), ("x_stride", i64), ("conv_weight", vp), ("log_decay", vp),
+                ("decay_stride", i64), ("beta", vp), ("beta_stride", i64), ("src_blocks", vp),
+                ("dst_blocks", vp), ("out", vp), ("out_stride", i64)]
+
+
 def one_hip_runtime() -> None:
     """A process must hold one HIP runtime.  PyTorch-ROCm ships its own copy,
     which its libraries load by file name; if libhkv.so were loaded first it
@@ -150,6 +173,14 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.hkv_mla_attend.restype = i32
     L.hkv_mla_attend.argtypes = [vp, vp, ctypes.POINTER(hkv_mla_attend_args), vp,
                                  ctypes.c_size_t, vp]
+    L.hkv_mla_evict_workspace.restype = i32
+    L.hkv_mla_evict_workspace.argtypes = [vp, ctypes.POINTER(hkv_mla_evict_args),
+                                          ctypes.POINTER(ctypes.c_size_t)]
+    L.hkv_mla_evict.restype = i32
+    L.hkv_mla_evict.argtypes = [vp, vp, ctypes.POINTER(hkv_mla_evict_args), vp,
+                                ctypes.c_size_t, vp]
+    L.hkv_kda_step.restype = i32
+    L.hkv_kda_step.argtypes = [vp, vp, ctypes.POINTER(hkv_kda_step_args), vp]
     L.hkv_last_error.restype = ctypes.c_char_p
     L.hkv_last_error.argtypes = []
     return L
@@ -340,6 +371,23 @@ def hkv_mla_attend(handle: int, pool_ptr: int, args: hkv_mla_attend_args, worksp
                               stream), "hkv_mla_attend")
 
 
+def hkv_mla_evict_workspace(handle: int, args: hkv_mla_evict_args) -> int:
+    out = ctypes.c_size_t()
+    _check(lib.hkv_mla_evict_workspace(handle, ctypes.byref(args), ctypes.byref(out)),
+           "hkv_mla_evict_workspace")
+    return out.value
+
+
+def hkv_mla_evict(handle: int, pool_ptr: int, args: hkv_mla_evict_args, workspace_ptr: int,
+                  ws_bytes: int, stream: int = 0) -> None:
+    _check(lib.hkv_mla_evict(handle, pool_ptr, ctypes.byref(args), workspace_ptr, ws_bytes,
+                             stream), "hkv_mla_evict")
+
+
+def hkv_kda_step(handle: int, pool_ptr: int, args: hkv_kda_step_args, stream: int = 0) -> None:
+    _check(lib.hkv_kda_step(handle, pool_ptr, ctypes.byref(args), stream), "hkv_kda_step")
+
+
 def status_of(fn, *args) -> int:
     """Calls one of the wrappers above and returns its status instead of
     raising (for tests of error paths)."""
@@ -406,3 +454,12 @@ class Layout:
 
     def mla_attend(self, pool_ptr, args: hkv_mla_attend_args, ws_ptr, ws_bytes, stream=0):
         hkv_mla_attend(self.handle, pool_ptr, args, ws_ptr, ws_bytes, stream)
+
+    def mla_evict_workspace(self, args: hkv_mla_evict_args) -> int:
+        return hkv_mla_evict_workspace(self.handle, args)
+
+    def mla_evict(self, pool_ptr, args: hkv_mla_evict_args, ws_ptr, ws_bytes, stream=0):
+        hkv_mla_evict(self.handle, pool_ptr, args, ws_ptr, ws_bytes, stream)
+
+    def kda_step(self, pool_ptr, args: hkv_kda_step_args, stream=0):
+        hkv_kda_step(self.handle, pool_ptr, args, stream)

@@ -81,4 +81,72 @@ inline AttendWorkspace attend_workspace(uint64_t workers, uint64_t head_tiles, u
 // cache_dtype: HKV_BF16, HKV_FP16, HKV_E4M3.  Returns the hipError_t.
 int launch_attend(const AttendArgs& a, int32_t dtype, int32_t cache_dtype, void* stream);
 
+// ---------------------------------------------------------------- eviction
+constexpr uint32_t kEvictMaxLayers = 64;
+
+struct EvictArgs {
+  uint8_t* pool;
+  uint64_t page_of[kEvictMaxLayers];  // each layer's page of block 0, from the pool's start
+  uint64_t stride;       // bytes between block ids
+  const int32_t* table;  // [n_seqs][max_blocks]
+  int64_t table_stride;
+  const int32_t* lens;   // [n_seqs]
+  const int32_t* next;   // [n_seqs]
+  const float* weights;  // [n_layers][n_seqs][slots], these four
+  const int32_t* positions;
+  float* weights_out;
+  int32_t* positions_out;
+  int64_t layer_stride, seq_stride;  // elements
+  int32_t* new_lens;     // [n_seqs] or nullptr
+  // workspace
+  int32_t* claims;       // [num_blocks] uses of a block by the call's sequences
+  int32_t* ok;           // [n_seqs] 1: the sequence can be evicted from
+  uint32_t* moves;       // [rows]: slots that move
+  uint32_t* lists;       // [rows][2 * max_moves]: freed slots, then the slots that fill them
+  uint32_t num_blocks, block_tokens, row_bytes;
+  uint32_t n_layers, n_seqs, max_blocks, budget, sinks, recent;
+  uint32_t max_moves;    // min(budget, max_blocks * block_tokens - budget)
+};
+
+struct EvictWorkspace {
+  uint64_t claims, ok, moves, lists, total;
+};
+inline EvictWorkspace evict_workspace(uint64_t num_blocks, uint64_t n_seqs, uint64_t rows,
+                                      uint64_t max_moves) {
+  EvictWorkspace w{};
+  w.claims = 0;
+  w.ok = w.claims + align256(num_blocks * 4);
+  w.moves = w.ok + align256(n_seqs * 4);
+  w.lists = w.moves + align256(rows * 4);
+  w.total = w.lists + align256(rows * 2 * max_moves * 4);
+  return w;
+}
+
+int launch_evict(const EvictArgs& a, void* stream);
+
+// ---------------------------------------------------------------- KDA step
+constexpr uint32_t kKdaMaxKernel = 8;   // conv taps
+constexpr uint32_t kKdaMaxSeqs = 4096;  // every workgroup looks through the call's block ids
+
+struct KdaArgs {
+  uint8_t* pages;        // the layer's page of block 0
+  uint64_t stride;       // bytes between block ids
+  uint64_t conv_bytes;   // the recurrent state's offset in a page
+  const void* x;         // [n_seqs][conv_dim]
+  int64_t x_stride;      // elements, as the other strides
+  const void* conv_weight;  // [conv_dim][taps]
+  const float* log_decay;   // [n_seqs][heads * d]
+  int64_t decay_stride;
+  const float* beta;        // [n_seqs][heads]
+  int64_t beta_stride;
+  const int32_t* src;       // [n_seqs]
+  const int32_t* dst;
+  void* out;                // [n_seqs][heads * d]
+  int64_t out_stride;
+  float scale, eps;
+  uint32_t num_blocks, n_seqs, heads, head_dim, taps;
+};
+
+int launch_kda(const KdaArgs& a, int32_t dtype, void* stream);
+
 }  // namespace hkv
