@@ -37,6 +37,7 @@
 
 #define HKV_GLOBAL __attribute__((address_space(1)))
 #define HKV_LDS __attribute__((address_space(3)))
+#define HKV_CONST __attribute__((address_space(4)))
 
 namespace {
 
@@ -52,7 +53,7 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 constexpr uint32_t kTile = hkv::kAttendTile;
 constexpr uint32_t kWidthSteps = hkv::kAttendMaxWidth / 32;   // k steps of S
 constexpr uint32_t kValueTiles = hkv::kAttendMaxValues / 16;  // 16-column tiles of O
-constexpr uint32_t kPitchMax = hkv::kAttendMaxWidth * 2 + 32;
+constexpr uint32_t kPitch = hkv::kAttendMaxWidth * 2 + 32;  // bytes of a row in LDS
 constexpr uint32_t kPPitch = kTile * 2 + 16;  // bytes of a P row (padded: 16-byte reads of
                                               // eight rows fall into different banks)
 constexpr float kLn2 = 0.693147180559945309f;
@@ -115,6 +116,14 @@ __device__ __forceinline__ float lane_xor(float x, int mask) {
   return __shfl_xor(x, mask, 64);
 }
 
+// The same value, but unknown to the compiler: what is computed from it inside
+// a loop stays there.  Used for addresses that a sequence needs once, which
+// would otherwise be kept in registers throughout the loop over the tiles.
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // Orders LDS accesses across the workgroup; global loads may stay in flight.
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -140,89 +149,162 @@ __device__ __forceinline__ uint32_t served_len(const hkv::AttendArgs& a, uint32_
 
 __device__ __forceinline__ uint32_t tiles_of(uint32_t len) { return (len + kTile - 1) / kTile; }
 
-// The block of 16 rows starting at a 16-aligned token lies in one page (a
-// block is a multiple of 16 tokens), so a tile has two row groups, each with
-// one address.  State: 0 present, 1 absent (null block or past the end), 2 a
-// block id outside the pool.
-struct RowGroup {
-  const uint8_t* base;
-  uint32_t state;
+// A tile has two groups of 16 rows.  A block is a multiple of 16 tokens, so a
+// group lies in one page.
+enum RowState : uint32_t {
+  kPresent = 0,
+  kAbsent = 1,  // a null block, or past the sequence's end
+  kBad = 2      // a block id outside the pool
 };
 
-template <class T, bool kFp8, uint32_t kHeads, uint32_t kWaves>
-struct Attend {
-  static constexpr uint32_t kThreads = kWaves * 64;
-  static constexpr uint32_t kHeadTiles = kHeads / 16;
-  static constexpr uint32_t kSTiles = kHeadTiles * (kTile / 16);  // 16x16 tiles of S
-  static_assert(kSTiles <= kWaves, "one S tile per wave");
-  static constexpr uint32_t kRowThreads = kThreads / kTile;       // threads that load a row
-  static constexpr uint32_t kRowChunks = hkv::kAttendMaxWidth * (kFp8 ? 1 : 2) / 16;
-  static constexpr uint32_t kLoads = (kRowChunks + kRowThreads - 1) / kRowThreads;
-  static constexpr uint32_t kOTiles = kValueTiles / kWaves;       // O column tiles per wave
+// Where the two row groups of a tile are: their entries of the block table,
+// their first token's place in the block, and the blocks' ids (asked for a
+// tile early).
+struct Cursor {
+  uint32_t j[2], off[2];
+  int32_t id[2];
+};
 
-  struct Lds {
-    uint8_t k[2][kTile * kPitchMax];
-    uint8_t p_hi[kHeads * kPPitch];
-    uint8_t p_lo[kHeads * kPPitch];
-    float top[kTile / 16][kHeads];  // a tile's maximum per head and 16 tokens; later the sums
-    float alpha[kHeads];
-    float m[kHeads];
-    uint32_t sums[kWaves];
-    uint32_t start[2];
+// Largest value over the lanes that hold one column of a 16x16 result (lane,
+// lane ^ 16, lane ^ 32, lane ^ 48), and their sum.
+__device__ __forceinline__ float column_max(float m) {
+  m = fmaxf(m, __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(  // lane ^ 16
+                                             __builtin_bit_cast(int, m), 0x401F)));
+  return fmaxf(m, lane_xor(m, 32));
+}
+__device__ __forceinline__ float column_sum(float m) {
+  m += lane_xor(m, 16);
+  return m + lane_xor(m, 32);
+}
+
+// The waves' roles: kLoaders bring rows into LDS, one wave per 16 heads takes
+// their logits and probabilities, kSummers add up the values.
+constexpr uint32_t kLoaders = 4, kSummers = 4;
+constexpr uint32_t attend_threads(uint32_t heads) {
+  return (kLoaders + heads / 16 + kSummers) * 64;
+}
+
+template <class T, bool kFp8, uint32_t kHeads>
+struct Attend {
+  static constexpr uint32_t kHeadTiles = kHeads / 16;
+  static constexpr uint32_t kScorers = kHeadTiles;
+  static constexpr uint32_t kWaves = kLoaders + kScorers + kSummers;
+  static constexpr uint32_t kThreads = attend_threads(kHeads);
+  static_assert(kThreads == kWaves * 64, "the launch has a wave for every role");
+  static constexpr uint32_t kOTiles = kValueTiles / kSummers;  // column tiles per summer
+  // A loader has 8 of a tile's rows, 8 lanes to a row, 16 bytes to a lane.
+  static constexpr uint32_t kLoads = (hkv::kAttendMaxWidth * (kFp8 ? 1 : 2) / 16 + 7) / 8;
+  static_assert(kLoaders * 8 == kTile, "8 rows to a loader");
+  static constexpr uint32_t kBatch = 3;    // k steps a scorer reads ahead
+  static constexpr uint32_t kBuffers = 3;  // a tile is loaded, scored and summed in turn
+
+  // A tile on its way: this lane's pieces, which tile, its groups' states.
+  struct Stage {
+    v4u x[kLoads];
+    uint32_t t, st[2];
   };
 
-  // The block id of a row group, asked for a tile before group_of needs it.
-  static __device__ __forceinline__ int32_t id_at(const hkv::AttendArgs& a, const int32_t* table,
-                                                  uint32_t tok, uint32_t len) {
-    return tok < len ? table[tok / a.block_tokens] : HKV_NULL_BLOCK;
-  }
-  static __device__ __forceinline__ RowGroup group_of(const hkv::AttendArgs& a, int32_t raw,
-                                                      uint32_t tok) {
-    const int32_t id = __builtin_amdgcn_readfirstlane(raw);
-    RowGroup g{a.pages, id == HKV_NULL_BLOCK ? 1u : 2u};
-    if (id >= 0 && (uint32_t)id < a.num_blocks) {
-      g.state = 0;
-      g.base = a.pages + (uint64_t)id * a.stride + (uint64_t)(tok % a.block_tokens) * a.row_bytes;
-    }
-    return g;
-  }
+  // The small arrays come first: the LDS instructions' 16-bit offsets reach
+  // them, and the first row buffer, from one register.
+  struct Lds {
+    uint8_t p_hi[2][kHeads * kPPitch];
+    uint8_t p_lo[2][kHeads * kPPitch];
+    float alpha[2][kHeads];
+    float m[kHeads], l[kHeads];
+    uint32_t tile[kBuffers][4];  // which tile a buffer holds, its groups' states
+    uint32_t sums[kWaves];
+    uint32_t start[2];
+    __align__(16) uint8_t k[kBuffers][kTile * kPitch];
+  };
 
-  // This thread's part of a tile's rows (zeros where a row is absent, so that
-  // 0 x anything the memory holds never reaches a sum).
-  static __device__ __forceinline__ void load_tile(const hkv::AttendArgs& a, const RowGroup* g,
-                                                   uint32_t tok, uint32_t len, v4u* stage) {
-    const uint32_t row = threadIdx.x / kRowThreads, c = threadIdx.x % kRowThreads;
-    const RowGroup& mine = row < 16 ? g[0] : g[1];
-    const bool live = mine.state == 0 && tok + row < len;
-    const HKV_GLOBAL v4u* p =
-        (const HKV_GLOBAL v4u*)(mine.base + (uint64_t)(row & 15) * a.row_bytes) + c;
-    const uint32_t chunks = a.row_bytes / 16;
+  // Asks for the ids of a tile's blocks (scalar loads: they are not in the
+  // way of the row loads, which are waited for in order).
+  static __device__ __forceinline__ void fetch_ids(const HKV_CONST int32_t* table, uint32_t t,
+                                                   uint32_t end, Cursor* c) {
 #pragma unroll
-    for (uint32_t i = 0; i < kLoads; ++i) {
-      v4u v = {0u, 0u, 0u, 0u};
-      if (live && c + i * kRowThreads < chunks) v = p[i * kRowThreads];
-      stage[i] = v;
+    for (uint32_t i = 0; i < 2; ++i)
+      c->id[i] = table[t * kTile + i * 16 < end ? c->j[i] : 0];
+  }
+  static __device__ __forceinline__ void place(const hkv::AttendArgs& a, uint32_t t, Cursor* c) {
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i) {
+      c->j[i] = (t * kTile + i * 16) / a.block_tokens;
+      c->off[i] = (t * kTile + i * 16) - c->j[i] * a.block_tokens;
     }
   }
+  // The state of tile t's groups.
+  static __device__ __forceinline__ void states(const hkv::AttendArgs& a, uint32_t t,
+                                                uint32_t end, const Cursor& c, uint32_t* st) {
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i) {
+      const uint32_t id = (uint32_t)c.id[i];
+      st[i] = t * kTile + i * 16 >= end || id == (uint32_t)HKV_NULL_BLOCK ? kAbsent
+              : id < a.num_blocks                                         ? kPresent
+                                                                          : kBad;
+    }
+  }
+  // From tile t (its ids fetched) to the first tile that holds anything, or to
+  // t1: a null block costs one look at the table, not a tile's work for each
+  // of its tiles.
+  static __device__ __forceinline__ uint32_t find_tile(const hkv::AttendArgs& a,
+                                                       const HKV_CONST int32_t* table,
+                                                       uint32_t t, uint32_t t1, uint32_t end,
+                                                       Cursor* c, uint32_t* st) {
+    states(a, t, end, *c, st);
+    while (st[0] == kAbsent && st[1] == kAbsent && t < t1) {
+      const uint64_t next = (uint64_t)(c->j[1] + 1) * a.block_tokens / kTile;
+      t = next < t1 ? (uint32_t)next : t1;
+      place(a, t, c);
+      fetch_ids(table, t, end, c);
+      states(a, t, end, *c, st);
+    }
+    return t;
+  }
 
-  static __device__ __forceinline__ void stage_tile(const hkv::AttendArgs& a, uint32_t pitch,
-                                                    const v4u* stage, HKV_LDS uint8_t* lds) {
-    const uint32_t row = threadIdx.x / kRowThreads, c = threadIdx.x % kRowThreads;
-    const uint32_t chunks = a.row_bytes / 16;
-    HKV_LDS uint8_t* d = lds + row * pitch + c * (kFp8 ? 32 : 16);
+  // Starts this lane's loads of its row of tile x->t.  What is absent loads the
+  // pool's first bytes instead and is put to zero in stage_tile, so that the
+  // loads need no branch and 0 x anything the memory holds never reaches a sum.
+  static __device__ __forceinline__ void load_tile(const hkv::AttendArgs& a, const Cursor& c,
+                                                   uint32_t loader, uint32_t lane, Stage* x) {
+    const uint32_t g = loader >> 1, row = (loader & 1) * 8 + lane / 8;
+    const uint32_t id = (uint32_t)(g ? c.id[1] : c.id[0]);
+    const uint32_t off = g ? c.off[1] : c.off[0];
+    const bool present = (g ? x->st[1] : x->st[0]) == kPresent;
+    const uint8_t* base = a.pages;
+    if (present) base += (uint64_t)id * a.stride + (uint64_t)off * a.row_bytes;
+    const uint32_t pieces = a.row_bytes / 16;
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; ++i) {
-      if (c + i * kRowThreads >= chunks) continue;
+      const uint32_t k = i * 8 + (lane & 7);
+      x->x[i] = *(const HKV_GLOBAL v4u*)((const HKV_GLOBAL uint8_t*)base +
+                                         (k < pieces ? row * a.row_bytes + k * 16 : 0));
+    }
+  }
+
+  // Writes the loaded pieces to LDS, widening e4m3.
+  static __device__ __forceinline__ void stage_tile(const hkv::AttendArgs& a, uint32_t end,
+                                                    uint32_t loader, uint32_t lane,
+                                                    const Stage& x, HKV_LDS uint8_t* lds) {
+    const uint32_t row = loader * 8 + lane / 8, pieces = a.row_bytes / 16;
+    const bool live = (loader >> 1 ? x.st[1] : x.st[0]) == kPresent && x.t * kTile + row < end;
+    HKV_LDS uint8_t* d = lds + row * kPitch;
+#pragma unroll
+    for (uint32_t i = 0; i < kLoads; ++i) {
+      const uint32_t k = i * 8 + (lane & 7);
+      v4u v = x.x[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = live ? v[e] : 0u;
+      if (k >= pieces) continue;
       if constexpr (kFp8) {
-        const v4u lo = {T::template widen<false>(stage[i][0]), T::template widen<true>(stage[i][0]),
-                        T::template widen<false>(stage[i][1]), T::template widen<true>(stage[i][1])};
-        const v4u hi = {T::template widen<false>(stage[i][2]), T::template widen<true>(stage[i][2]),
-                        T::template widen<false>(stage[i][3]), T::template widen<true>(stage[i][3])};
-        HKV_LDS v4u* to = (HKV_LDS v4u*)(d + i * kRowThreads * 32);
+        const v4u lo = {T::template widen<false>(v[0]), T::template widen<true>(v[0]),
+                        T::template widen<false>(v[1]), T::template widen<true>(v[1])};
+        const v4u hi = {T::template widen<false>(v[2]), T::template widen<true>(v[2]),
+                        T::template widen<false>(v[3]), T::template widen<true>(v[3])};
+        HKV_LDS v4u* to = (HKV_LDS v4u*)(d + k * 32);
         to[0] = lo;
         to[1] = hi;
       } else {
-        *(HKV_LDS v4u*)(d + i * kRowThreads * 16) = stage[i];
+        *(HKV_LDS v4u*)(d + k * 16) = v;
       }
     }
   }
@@ -268,19 +350,219 @@ struct Attend {
     *seq_start = uniform(lds.start[1]);
   }
 
+  // The roles' parts of one run of tiles [t0, t1) of a sequence.  Round i (the
+  // time between two barriers): the loaders write tile i + 1 to its buffer, the
+  // scorers make P of tile i, the summers add tile i - 1.  "Tile i" counts
+  // tiles that hold anything; the loaders say in lds.tile which one it is, and
+  // every role stops after the same round.
+  static __device__ __forceinline__ void load(const hkv::AttendArgs& a, Lds& lds, uint32_t loader,
+                                              uint32_t lane, const HKV_CONST int32_t* table,
+                                              uint32_t t0, uint32_t t1, uint32_t end) {
+    Cursor cur;
+    place(a, t0, &cur);
+    fetch_ids(table, t0, end, &cur);
+    uint32_t next = t0, buf = 0;
+    // Loads the next tile that holds anything (x->t >= t1: there is none), and
+    // asks for the ids of the one after it.
+    auto begin = [&](Stage* x) {
+      x->t = find_tile(a, table, next, t1, end, &cur, x->st);
+      load_tile(a, cur, loader, lane, x);
+      next = x->t + 1;
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i) {
+        cur.off[i] += kTile;
+        while (cur.off[i] >= a.block_tokens) {
+          cur.off[i] -= a.block_tokens;
+          ++cur.j[i];
+        }
+      }
+      fetch_ids(table, next, end, &cur);
+    };
+    auto stage = [&](Stage* x) {
+      stage_tile(a, end, loader, lane, *x, (HKV_LDS uint8_t*)lds.k[buf]);
+      if (loader == 0 && lane == 0) {
+        lds.tile[buf][0] = x->t;
+        lds.tile[buf][1] = x->st[0];
+        lds.tile[buf][2] = x->st[1];
+      }
+      buf = buf + 1 == kBuffers ? 0 : buf + 1;
+      begin(x);
+    };
+    Stage xa, xb;
+    begin(&xa);
+    begin(&xb);
+    uint32_t t = xa.t;
+    stage(&xa);
+    lds_barrier();
+    // Two tiles a turn and one exit: xa and xb stay in their registers, and the
+    // waits for the loads know which of them is older.  A tile past the last is
+    // staged as zeros and not looked at; after an odd number of tiles the other
+    // roles wait for its round.
+    while (t < t1) {
+      stage(&xb);
+      lds_barrier();
+      t = xa.t;
+      stage(&xa);
+      lds_barrier();
+    }
+    lds_barrier();
+  }
+
+  static __device__ __forceinline__ void score(const hkv::AttendArgs& a, Lds& lds,
+                                               uint32_t scorer, uint32_t lane, uint32_t s,
+                                               uint32_t ht, uint32_t t1, uint32_t len) {
+    const uint32_t col = lane & 15, quad = lane >> 4;
+    const uint32_t hl = scorer * 16 + col, h = ht * kHeads + hl, steps = a.width / 32;
+    v4u q[kWidthSteps];  // the queries, as the column operand
+    {
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)s * a.q_seq_stride +
+                            (int64_t)h * a.q_head_stride + quad * 8;
+#pragma unroll
+      for (uint32_t i = 0; i < kWidthSteps; ++i) {
+        v4u v = {0u, 0u, 0u, 0u};
+        if (h < a.n_heads && i < steps) v = *(const HKV_GLOBAL v4u*)(src + i * 32);
+        q[i] = v;
+      }
+    }
+    float m = -INFINITY, l = 0.0f;
+    uint32_t buf = 0, half = 0;
+    lds_barrier();
+    for (;;) {
+      const uint32_t t = uniform(lds.tile[buf][0]);
+      if (t >= t1) break;
+      const uint32_t st[2] = {uniform(lds.tile[buf][1]), uniform(lds.tile[buf][2])};
+      // S of 32 tokens (two 16-row results) x 16 heads.
+      const HKV_LDS uint8_t* row = (const HKV_LDS uint8_t*)lds.k[buf] + col * kPitch + quad * 16;
+      v4f sc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+      v4u k[2][kBatch][2];  // the next steps' rows are read while these are multiplied
+#pragma unroll
+      for (uint32_t i = 0; i < kWidthSteps + kBatch; ++i) {
+        if (i < kWidthSteps)
+#pragma unroll
+          for (uint32_t r = 0; r < 2; ++r)
+            k[i / kBatch & 1][i % kBatch][r] =
+                *(const HKV_LDS v4u*)(row + r * 16 * kPitch + i * 64);
+        if (i >= kBatch) {
+          const uint32_t o = i - kBatch;
+#pragma unroll
+          for (uint32_t r = 0; r < 2; ++r)
+            sc[r] = T::mma(k[o / kBatch & 1][o % kBatch][r], q[o], sc[r]);
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (uint32_t r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x = sc[r][i] * a.scale;
+          if (st[r] == kAbsent || t * kTile + r * 16 + quad * 4 + i >= len) x = -INFINITY;
+          else if (st[r] == kBad) x = NAN;
+          sc[r][i] = x;
+          top = fmaxf(top, x);
+        }
+      if (a.logits && h < a.n_heads) {
+        float* to = a.logits + (((uint64_t)s * a.max_tiles + t) * a.n_heads + h) * kTile + quad * 4;
+        *(HKV_GLOBAL v4f*)to = sc[0];
+        *(HKV_GLOBAL v4f*)(to + 16) = sc[1];
+      }
+      top = fmaxf(m, column_max(top));
+      const float base = top == -INFINITY ? 0.0f : top;
+      const float alpha = exp_of(m - base);
+      m = top;
+      l *= alpha;
+      HKV_LDS uint8_t* hi = (HKV_LDS uint8_t*)lds.p_hi[half] + hl * kPPitch + quad * 8;
+      HKV_LDS uint8_t* lo = (HKV_LDS uint8_t*)lds.p_lo[half] + hl * kPPitch + quad * 8;
+#pragma unroll
+      for (uint32_t r = 0; r < 2; ++r) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l += p[i] = exp_of(sc[r][i] - base);
+        const uint32_t h01 = T::pack(p[0], p[1]), h23 = T::pack(p[2], p[3]);
+        *(HKV_LDS v2u*)(hi + r * 32) = v2u{h01, h23};
+        *(HKV_LDS v2u*)(lo + r * 32) = v2u{T::pack(p[0] - T::low(h01), p[1] - T::high(h01)),
+                                          T::pack(p[2] - T::low(h23), p[3] - T::high(h23))};
+      }
+      if (quad == 0) lds.alpha[half][hl] = alpha;
+      buf = buf + 1 == kBuffers ? 0 : buf + 1;
+      half ^= 1;
+      lds_barrier();
+    }
+    l = column_sum(l);
+    if (quad == 0) {
+      lds.m[hl] = m;
+      lds.l[hl] = l;
+    }
+    if (half) lds_barrier();
+    lds_barrier();
+  }
+
+  // O^T of this wave's value columns (those past `values` are not written out)
+  // x all heads.  Transposing loads: in each group of 16 lanes, lane x supplies
+  // four columns of token x / 4 and receives column x of four tokens.
+  static __device__ __forceinline__ void sum(const hkv::AttendArgs& a, Lds& lds, uint32_t summer,
+                                             uint32_t lane, uint32_t t1,
+                                             v4f (&acc)[kHeadTiles][kOTiles]) {
+    const uint32_t col = lane & 15, quad = lane >> 4;
+#pragma unroll
+    for (uint32_t i = 0; i < kHeadTiles; ++i)
+#pragma unroll
+      for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t buf = 0, half = 0;
+    lds_barrier();
+    if (uniform(lds.tile[0][0]) < t1) {
+      lds_barrier();  // the first tile's P is being made
+      for (;;) {
+        const uint32_t next = buf + 1 == kBuffers ? 0 : buf + 1;
+        const uint32_t t_next = lds.tile[next][0];
+        const HKV_LDS uint8_t* vb = (const HKV_LDS uint8_t*)lds.k[buf] +
+                                    (quad * 8 + (col >> 2)) * kPitch + (col & 3) * 8 + summer * 32;
+        v4u ph[kHeadTiles], pl[kHeadTiles];
+#pragma unroll
+        for (uint32_t i = 0; i < kHeadTiles; ++i) {
+          const uint32_t from = (i * 16 + col) * kPPitch + quad * 16;
+          ph[i] = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_hi[half] + from);
+          pl[i] = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_lo[half] + from);
+          const float alpha = lds.alpha[half][i * 16 + col];
+#pragma unroll
+          for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] *= alpha;
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < kOTiles; ++j) {
+          const HKV_LDS uint8_t* from = vb + j * kSummers * 32;
+          const v2u lo = __builtin_bit_cast(
+              v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((HKV_LDS v4s*)from));
+          const v2u hi = __builtin_bit_cast(
+              v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((HKV_LDS v4s*)(from + 4 * kPitch)));
+          const v4u v = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+          for (uint32_t i = 0; i < kHeadTiles; ++i) acc[i][j] = T::mma(v, ph[i], acc[i][j]);
+#pragma unroll
+          for (uint32_t i = 0; i < kHeadTiles; ++i) acc[i][j] = T::mma(v, pl[i], acc[i][j]);
+        }
+        buf = next;
+        half ^= 1;
+        if (uniform(t_next) >= t1) break;
+        lds_barrier();
+      }
+    }
+    if (half) lds_barrier();
+    lds_barrier();
+  }
+
   static __device__ __forceinline__ void run(const hkv::AttendArgs& a, Lds& lds) {
     const uint32_t worker = blockIdx.x, ht = blockIdx.y;
-    const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const uint32_t col = lane & 15, quad = lane >> 4;
-    const uint32_t pitch = a.width * 2 + 32;
-    const uint32_t steps = a.width / 32, vtiles = a.values / 16;
-    const uint32_t my_ht = wave % kHeadTiles, my_kt = wave / kHeadTiles;
-    const bool scores = wave < kSTiles;
+    const uint32_t wave = uniform(threadIdx.x >> 6);
     uint64_t first, share, total, seq_start;
     uint32_t s = 0;
     find_run(a, lds, worker, &first, &share, &total, &s, &seq_start);
     if (first >= total) return;
     const uint64_t last = first + share < total ? first + share : total;
+    // Narrower rows leave the rest of the buffers' columns at zero, so that the
+    // products need no bounds.
+    if (a.width < hkv::kAttendMaxWidth)
+      for (uint32_t i = threadIdx.x; i < sizeof(lds.k) / 16; i += kThreads)
+        ((HKV_LDS v4u*)lds.k)[i] = v4u{0u, 0u, 0u, 0u};
+    lds_barrier();
 
     for (uint64_t at = first; at < last && s < a.n_seqs;) {
       const uint32_t len = uniform(served_len(a, s));
@@ -291,184 +573,51 @@ struct Attend {
       }
       const uint32_t t0 = (uint32_t)(at - seq_start);
       const uint32_t t1 = last - seq_start < n_tiles ? (uint32_t)(last - seq_start) : n_tiles;
-      const int32_t* table = a.table + (int64_t)s * a.table_stride;
       if (t0 == 0 && ht == 0 && threadIdx.x == 0) {
         a.spans[s * 4 + 0] = (int32_t)worker;
         a.spans[s * 4 + 1] = (int32_t)((seq_start + n_tiles - 1) / share);
         a.spans[s * 4 + 2] = at == first ? 0 : 1;
       }
-
-      // The queries of this wave's head tile, as the S product's column operand.
-      v4u q[kWidthSteps];
-      {
-        const uint32_t h = ht * kHeads + my_ht * 16 + col;
-        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)s * a.q_seq_stride +
-                              (int64_t)h * a.q_head_stride + quad * 8;
-#pragma unroll
-        for (uint32_t i = 0; i < kWidthSteps; ++i) {
-          v4u v = {0u, 0u, 0u, 0u};
-          if (scores && h < a.n_heads && i < steps) v = *(const HKV_GLOBAL v4u*)(src + i * 32);
-          q[i] = v;
-        }
-      }
-      v4f acc[kHeadTiles][kOTiles];
-#pragma unroll
-      for (uint32_t i = 0; i < kHeadTiles; ++i)
-#pragma unroll
-        for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      float m = -INFINITY, l = 0.0f;
-
-      v4u stage[kLoads];
-      RowGroup g[2], g_next[2];
-      int32_t id[2], id_next[2];
-      for (uint32_t i = 0; i < 2; ++i) id[i] = id_at(a, table, t0 * kTile + i * 16, len);
-      for (uint32_t i = 0; i < 2; ++i) id_next[i] = id_at(a, table, (t0 + 1) * kTile + i * 16, len);
-      for (uint32_t i = 0; i < 2; ++i) g[i] = group_of(a, id[i], t0 * kTile + i * 16);
-      load_tile(a, g, t0 * kTile, len, stage);
-      for (uint32_t i = 0; i < 2; ++i) {
-        g_next[i] = group_of(a, id_next[i], (t0 + 1) * kTile + i * 16);
-        id[i] = id_at(a, table, (t0 + 2) * kTile + i * 16, len);
-      }
-      stage_tile(a, pitch, stage, (HKV_LDS uint8_t*)lds.k[0]);
-      if (t0 + 1 < t1) load_tile(a, g_next, (t0 + 1) * kTile, len, stage);
-      lds_barrier();
-
-      for (uint32_t t = t0; t < t1; ++t) {
-        const HKV_LDS uint8_t* kb = (const HKV_LDS uint8_t*)lds.k[(t - t0) & 1];
-        // S: 16 tokens x 16 heads per wave.
-        v4f sc = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (scores) {
-          const HKV_LDS uint8_t* row = kb + (my_kt * 16 + col) * pitch + quad * 16;
-#pragma unroll
-          for (uint32_t i = 0; i < kWidthSteps; ++i)
-            if (i < steps) sc = T::mma(*(const HKV_LDS v4u*)(row + i * 64), q[i], sc);
-          const uint32_t state = my_kt ? g[1].state : g[0].state;
-          float top = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t tok = t * kTile + my_kt * 16 + quad * 4 + i;
-            float x = sc[i] * a.scale;
-            if (state == 1 || tok >= len) x = -INFINITY;
-            else if (state == 2) x = NAN;
-            sc[i] = x;
-            top = fmaxf(top, x);
-          }
-          top = fmaxf(top, lane_xor(top, 16));
-          top = fmaxf(top, lane_xor(top, 32));
-          if (quad == 0) lds.top[my_kt][my_ht * 16 + col] = top;
-          const uint32_t h = ht * kHeads + my_ht * 16 + col;
-          if (a.logits && h < a.n_heads) {
-            float* to = a.logits + (((uint64_t)s * a.max_tiles + t) * a.n_heads + h) * kTile +
-                        my_kt * 16 + quad * 4;
-            *(HKV_GLOBAL v4f*)to = sc;
-          }
-        }
-        lds_barrier();
-        if (scores) {
-          const uint32_t h = my_ht * 16 + col;
-          const float top = fmaxf(m, fmaxf(lds.top[0][h], lds.top[1][h]));
-          const float base = top == -INFINITY ? 0.0f : top;
-          const float alpha = exp_of(m - base);
-          m = top;
-          float p[4], sum = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            p[i] = exp_of(sc[i] - base);
-            sum += p[i];
-          }
-          l = l * alpha + sum;
-          const uint32_t h01 = T::pack(p[0], p[1]), h23 = T::pack(p[2], p[3]);
-          const uint32_t l01 = T::pack(p[0] - T::low(h01), p[1] - T::high(h01));
-          const uint32_t l23 = T::pack(p[2] - T::low(h23), p[3] - T::high(h23));
-          const uint32_t to = h * kPPitch + my_kt * 32 + quad * 8;
-          *(HKV_LDS v2u*)((HKV_LDS uint8_t*)lds.p_hi + to) = v2u{h01, h23};
-          *(HKV_LDS v2u*)((HKV_LDS uint8_t*)lds.p_lo + to) = v2u{l01, l23};
-          if (my_kt == 0 && quad == 0) lds.alpha[h] = alpha;
-        }
-        g[0] = g_next[0];
-        g[1] = g_next[1];
-        if (t + 1 < t1) {
-          stage_tile(a, pitch, stage, (HKV_LDS uint8_t*)lds.k[(t + 1 - t0) & 1]);
-          for (uint32_t i = 0; i < 2; ++i) {
-            g_next[i] = group_of(a, id[i], (t + 2) * kTile + i * 16);
-            id[i] = id_at(a, table, (t + 3) * kTile + i * 16, len);
-          }
-          if (t + 2 < t1) load_tile(a, g_next, (t + 2) * kTile, len, stage);
-        }
-        lds_barrier();
-        // O^T: this wave's value columns x all heads.
-        v4u ph[kHeadTiles], pl[kHeadTiles];
+      const uint32_t lane = opaque(threadIdx.x & 63);
+      if (wave < kLoaders) {
+        const uint32_t end = t1 * kTile < len ? t1 * kTile : len;  // of what this worker loads
+        load(a, lds, wave, lane, (const HKV_CONST int32_t*)(a.table + (int64_t)s * a.table_stride),
+             t0, t1, end);
+      } else if (wave < kLoaders + kScorers) {
+        score(a, lds, wave - kLoaders, lane, s, ht, t1, len);
+      } else {
+        const uint32_t summer = wave - kLoaders - kScorers;
+        v4f acc[kHeadTiles][kOTiles];
+        sum(a, lds, summer, lane, t1, acc);
+        const uint32_t out_lane = opaque(lane), col = out_lane & 15, quad = out_lane >> 4;
+        const bool whole = t0 == 0 && t1 == n_tiles;
+        const uint64_t slot = ((uint64_t)worker * a.head_tiles + ht) * 2 + (at == first ? 0 : 1);
 #pragma unroll
         for (uint32_t i = 0; i < kHeadTiles; ++i) {
-          const uint32_t from = (i * 16 + col) * kPPitch + quad * 16;
-          ph[i] = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_hi + from);
-          pl[i] = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_lo + from);
-          const float alpha = lds.alpha[i * 16 + col];
-          if (__any(alpha != 1.0f)) {
+          const uint32_t hl = i * 16 + col, h = ht * kHeads + hl;
+          const float l = lds.l[hl], top = lds.m[hl];
+          if (h >= a.n_heads) continue;
+          const float inv = whole ? (l == 0.0f ? 0.0f : a.cache_scale / l) : 1.0f;
 #pragma unroll
-            for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] *= alpha;
+          for (uint32_t j = 0; j < kOTiles; ++j) {
+            const uint32_t v = (j * kSummers + summer) * 16 + quad * 4;
+            if (v >= a.values) continue;
+            const v4f o = acc[i][j] * inv;
+            if (whole) {
+              uint16_t* to = static_cast<uint16_t*>(a.out) + (int64_t)s * a.out_seq_stride +
+                             (int64_t)h * a.out_head_stride + v;
+              *(HKV_GLOBAL v2u*)to = v2u{T::pack(o[0], o[1]), T::pack(o[2], o[3])};
+            } else {
+              *(HKV_GLOBAL v4f*)(a.part_o + (slot * kHeads + hl) * a.values + v) = o;
+            }
           }
-        }
-        // Transposing loads: in each group of 16 lanes, lane x supplies four
-        // columns of token x / 4 and receives column x of four tokens.
-        const HKV_LDS uint8_t* vb = kb + (quad * 8 + (col >> 2)) * pitch + (col & 3) * 8;
-#pragma unroll
-        for (uint32_t j = 0; j < kOTiles; ++j) {
-          const uint32_t vt = j * kWaves + wave;
-          if (vt >= vtiles) continue;
-          const HKV_LDS uint8_t* from = vb + vt * 32;
-          const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HKV_LDS v4s*)from);
-          const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HKV_LDS v4s*)(from + 4 * pitch));
-          const v2u lo2 = __builtin_bit_cast(v2u, lo), hi2 = __builtin_bit_cast(v2u, hi);
-          const v4u v = {lo2[0], lo2[1], hi2[0], hi2[1]};
-#pragma unroll
-          for (uint32_t i = 0; i < kHeadTiles; ++i) {
-            acc[i][j] = T::mma(v, ph[i], acc[i][j]);
-            acc[i][j] = T::mma(v, pl[i], acc[i][j]);
-          }
-        }
-      }
-
-      // The sums of the waves that hold a head's tokens, joined (lds.top was
-      // last read before the loop's last barrier).
-      if (scores) {
-        l += lane_xor(l, 16);
-        l += lane_xor(l, 32);
-        if (quad == 0) {
-          lds.top[my_kt][my_ht * 16 + col] = l;
-          if (my_kt == 0) lds.m[my_ht * 16 + col] = m;
-        }
-      }
-      lds_barrier();
-      const bool whole = t0 == 0 && t1 == n_tiles;
-      const uint64_t slot = ((uint64_t)worker * a.head_tiles + ht) * 2 + (at == first ? 0 : 1);
-#pragma unroll
-      for (uint32_t i = 0; i < kHeadTiles; ++i) {
-        const uint32_t hl = i * 16 + col, h = ht * kHeads + hl;
-        const float sum = lds.top[0][hl] + lds.top[1][hl];
-        const float top = lds.m[hl];
-        if (h >= a.n_heads) continue;
-        const float inv = whole ? (sum == 0.0f ? 0.0f : a.cache_scale / sum) : 1.0f;
-#pragma unroll
-        for (uint32_t j = 0; j < kOTiles; ++j) {
-          const uint32_t vt = j * kWaves + wave;
-          if (vt >= vtiles) continue;
-          const v4f o = acc[i][j] * inv;
-          const uint32_t v = vt * 16 + quad * 4;
-          if (whole) {
-            uint16_t* to = static_cast<uint16_t*>(a.out) + (int64_t)s * a.out_seq_stride +
-                           (int64_t)h * a.out_head_stride + v;
-            *(HKV_GLOBAL v2u*)to = v2u{T::pack(o[0], o[1]), T::pack(o[2], o[3])};
-          } else {
-            *(HKV_GLOBAL v4f*)(a.part_o + (slot * kHeads + hl) * a.values + v) = o;
-          }
-        }
-        if (wave == i % kWaves && quad == 0) {
-          if (whole) {
-            write_lse(a, s, h, top, sum);
-          } else {
-            a.part_ml[(slot * kHeads + hl) * 2 + 0] = top;
-            a.part_ml[(slot * kHeads + hl) * 2 + 1] = sum;
+          if (summer == i && quad == 0) {
+            if (whole) {
+              write_lse(a, s, h, top, l);
+            } else {
+              a.part_ml[(slot * kHeads + hl) * 2 + 0] = top;
+              a.part_ml[(slot * kHeads + hl) * 2 + 1] = l;
+            }
           }
         }
       }
@@ -544,15 +693,14 @@ __device__ __forceinline__ void join(const hkv::AttendArgs& a) {
 
 }  // namespace
 
-#define HKV_ATTEND(name, T, fp8, heads, waves)                                              \
-  extern "C" __global__ __launch_bounds__((waves) * 64, 2) void name(hkv::AttendArgs a) {   \
-    __shared__ __align__(16) Attend<T, fp8, heads, waves>::Lds lds;                         \
-    Attend<T, fp8, heads, waves>::run(a, lds);                                              \
+#define HKV_ATTEND(name, T, fp8, heads)                                                     \
+  extern "C" __global__ __launch_bounds__(attend_threads(heads)) void name(hkv::AttendArgs a) { \
+    __shared__ __align__(16) Attend<T, fp8, heads>::Lds lds;                                \
+    Attend<T, fp8, heads>::run(a, lds);                                                     \
   }
-#define HKV_ATTEND_HEADS(suffix, T, fp8)                  \
-  HKV_ATTEND(hkv_mla_attend_##suffix##_h16, T, fp8, 16, 4) \
-  HKV_ATTEND(hkv_mla_attend_##suffix##_h32, T, fp8, 32, 4) \
-  HKV_ATTEND(hkv_mla_attend_##suffix##_h64, T, fp8, 64, 8)
+#define HKV_ATTEND_HEADS(suffix, T, fp8)               \
+  HKV_ATTEND(hkv_mla_attend_##suffix##_h16, T, fp8, 16) \
+  HKV_ATTEND(hkv_mla_attend_##suffix##_h32, T, fp8, 32)
 HKV_ATTEND_HEADS(bf16, Bf16, false)
 HKV_ATTEND_HEADS(fp16, Fp16, false)
 HKV_ATTEND_HEADS(bf16_e4m3, Bf16, true)
@@ -577,7 +725,10 @@ extern "C" __global__ __launch_bounds__(256) void hkv_mla_attend_weights(hkv::At
   const uint32_t s = blockIdx.y;
   const uint32_t len = served_len(a, s);
   const uint32_t tok = blockIdx.x * 256 + threadIdx.x;
-  if (tok >= len) return;
+  // (tiles of null blocks have no logits)
+  if (tok >= len ||
+      a.table[(int64_t)s * a.table_stride + tok / a.block_tokens] == HKV_NULL_BLOCK)
+    return;
   const float* x = a.logits + ((uint64_t)s * a.max_tiles + tok / kTile) * a.n_heads * kTile +
                    tok % kTile;
   const float* norm = a.norm + (uint64_t)s * a.n_heads;
@@ -590,24 +741,20 @@ namespace hkv {
 
 int launch_attend(const AttendArgs& a, int32_t dtype, int32_t cache_dtype, void* stream) {
 #define HKV_FN(f) reinterpret_cast<const void*>(&f)
-  static const void* const kKernels[2][2][3] = {
-      {{HKV_FN(hkv_mla_attend_bf16_h16), HKV_FN(hkv_mla_attend_bf16_h32),
-        HKV_FN(hkv_mla_attend_bf16_h64)},
-       {HKV_FN(hkv_mla_attend_bf16_e4m3_h16), HKV_FN(hkv_mla_attend_bf16_e4m3_h32),
-        HKV_FN(hkv_mla_attend_bf16_e4m3_h64)}},
-      {{HKV_FN(hkv_mla_attend_fp16_h16), HKV_FN(hkv_mla_attend_fp16_h32),
-        HKV_FN(hkv_mla_attend_fp16_h64)},
-       {HKV_FN(hkv_mla_attend_fp16_e4m3_h16), HKV_FN(hkv_mla_attend_fp16_e4m3_h32),
-        HKV_FN(hkv_mla_attend_fp16_e4m3_h64)}}};
+  static const void* const kKernels[2][2][2] = {
+      {{HKV_FN(hkv_mla_attend_bf16_h16), HKV_FN(hkv_mla_attend_bf16_h32)},
+       {HKV_FN(hkv_mla_attend_bf16_e4m3_h16), HKV_FN(hkv_mla_attend_bf16_e4m3_h32)}},
+      {{HKV_FN(hkv_mla_attend_fp16_h16), HKV_FN(hkv_mla_attend_fp16_h32)},
+       {HKV_FN(hkv_mla_attend_fp16_e4m3_h16), HKV_FN(hkv_mla_attend_fp16_e4m3_h32)}}};
   const uint32_t ty = dtype == HKV_FP16, fp8 = cache_dtype == HKV_E4M3;
-  const void* main_fn = kKernels[ty][fp8][a.head_tile == 16 ? 0 : a.head_tile == 32 ? 1 : 2];
+  const void* main_fn = kKernels[ty][fp8][a.head_tile == 32];
   const void* join_fn = ty ? HKV_FN(hkv_mla_attend_join_fp16) : HKV_FN(hkv_mla_attend_join_bf16);
 #undef HKV_FN
   AttendArgs arg = a;
   void* params[] = {&arg};
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t e = hipLaunchKernel(main_fn, dim3(a.workers, a.head_tiles),
-                                 dim3(a.head_tile == 64 ? 512 : 256), params, 0, st);
+                                 dim3(attend_threads(a.head_tile)), params, 0, st);
   if (e == hipSuccess)
     e = hipLaunchKernel(join_fn, dim3(a.n_seqs * a.n_heads, (a.values + 127) / 128),
                         dim3(kJoinThreads), params, 0, st);

@@ -105,10 +105,9 @@ hkv_status check_table(const hkv::Plan& p, int32_t n_seqs, int32_t max_blocks,
 }
 
 // ---------------------------------------------------------------- attention
-// Two workgroups of the 16- and 32-head kernels fit a CU (their LDS), one of
-// the 64-head kernel.  Both head tiles of a batch of more than 64 heads run at
-// once, on the same XCD (a multiple of 8 apart), so that the second reads the
-// rows from L2.
+// One workgroup (16 waves, about 100 KB of LDS) fits a CU.  The head tiles of a
+// batch of more than 32 heads run at once, those of one run of tokens on the
+// same XCD (a multiple of 8 apart), so that only the first reads from HBM.
 constexpr uint32_t kCus = 256;
 
 hkv_status plan_attend(const hkv_layout* layout, const hkv_mla_attend_args* a, bool weights,
@@ -144,7 +143,7 @@ hkv_status plan_attend(const hkv_layout* layout, const hkv_mla_attend_args* a, b
   const uint64_t tiles = (uint64_t)k->n_seqs * k->max_tiles;
   if (tiles > 0x7FFFFFFFull)
     return set_error(HKV_E_ARG, "n_seqs x max_blocks x N exceeds 2^36 tokens; split the batch");
-  const uint64_t fit = (k->head_tile == 64 ? 1 : 2) * kCus / k->head_tiles;
+  const uint64_t fit = kCus / k->head_tiles / 8 * 8;
   const uint64_t useful = (tiles + hkv::kAttendMinTiles - 1) / hkv::kAttendMinTiles;
   k->workers = (uint32_t)std::max<uint64_t>(1, std::min(fit, useful));
   *ws = hkv::attend_workspace(k->workers, k->head_tiles, k->head_tile, k->values, k->n_seqs,
