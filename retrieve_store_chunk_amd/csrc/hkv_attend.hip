@@ -629,19 +629,23 @@ struct Attend {
   }
 };
 
-// Adds up the partial results of a sequence's workers for one head and 128
-// value columns; also writes the rows of sequences that own no tile (zeros for
-// an empty one, NaN for a length the table cannot hold).
-constexpr uint32_t kJoinThreads = 256;
-constexpr uint32_t kJoinGroups = kJoinThreads / 32;  // 32 lanes x 4 columns each
+// Adds up the partial results of a sequence's workers for one head and
+// 4 << a.join_shift value columns: the workgroup's threads are groups of
+// 1 << join_shift lanes, each taking every so many partial results.  Few
+// (sequence, head) pairs are spread over more workgroups by taking fewer
+// columns in each.  Also writes the rows of sequences that own no tile (zeros
+// for an empty one, NaN for a length the table cannot hold).
+constexpr uint32_t kJoinThreads = hkv::kAttendMaxWorkers;  // one partial result a thread
 
 template <class T>
 __device__ __forceinline__ void join(const hkv::AttendArgs& a) {
-  __shared__ float part[kJoinGroups][32][4];
+  __shared__ v4f part[kJoinThreads];
+  __shared__ float scale[kJoinThreads];
   __shared__ float red[2][kJoinThreads / 64];
   const uint32_t s = blockIdx.x / a.n_heads, h = blockIdx.x % a.n_heads;
-  const uint32_t t = threadIdx.x, lane = t & 31, grp = t >> 5;
-  const uint32_t v = blockIdx.y * 128 + lane * 4;
+  const uint32_t t = threadIdx.x, lanes = 1u << a.join_shift;
+  const uint32_t lane = t & (lanes - 1), grp = t >> a.join_shift, groups = kJoinThreads / lanes;
+  const uint32_t v = (blockIdx.y * lanes + lane) * 4;
   uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)s * a.out_seq_stride +
                   (int64_t)h * a.out_head_stride + v;
   const int32_t len = a.lens[s];
@@ -658,16 +662,16 @@ __device__ __forceinline__ void join(const hkv::AttendArgs& a) {
   auto row = [&](uint32_t i) {  // worker w0 + i: its first run, but slot0 for w0
     return (((uint64_t)(w0 + i) * a.head_tiles + ht) * 2 + (i == 0 ? slot0 : 0)) * a.head_tile + hl;
   };
-  float top = -INFINITY;
-  for (uint32_t i = t; i < n; i += kJoinThreads) top = fmaxf(top, a.part_ml[row(i) * 2]);
+  const float m = t < n ? a.part_ml[row(t) * 2] : -INFINITY;
+  const float l = t < n ? a.part_ml[row(t) * 2 + 1] : 0.0f;
+  float top = m;
   for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, lane_xor(top, d));
   if ((t & 63) == 0) red[0][t >> 6] = top;
   __syncthreads();
   for (uint32_t w = 0; w < kJoinThreads / 64; ++w) top = fmaxf(top, red[0][w]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
-  for (uint32_t i = t; i < n; i += kJoinThreads)
-    sum += a.part_ml[row(i) * 2 + 1] * exp_of(a.part_ml[row(i) * 2] - base);
+  const float x = exp_of(m - (top == -INFINITY ? 0.0f : top));
+  scale[t] = x;
+  float sum = l * x;
   for (int d = 1; d < 64; d <<= 1) sum += lane_xor(sum, d);
   if ((t & 63) == 0) red[1][t >> 6] = sum;
   __syncthreads();
@@ -675,16 +679,13 @@ __device__ __forceinline__ void join(const hkv::AttendArgs& a) {
   for (uint32_t w = 0; w < kJoinThreads / 64; ++w) sum += red[1][w];
   v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
   if (v < a.values)
-    for (uint32_t i = grp; i < n; i += kJoinGroups)
-      o += *(const HKV_GLOBAL v4f*)(a.part_o + row(i) * a.values + v) *
-           exp_of(a.part_ml[row(i) * 2] - base);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) part[grp][lane][i] = o[i];
+#pragma unroll 4
+    for (uint32_t i = grp; i < n; i += groups)
+      o += *(const HKV_GLOBAL v4f*)(a.part_o + row(i) * a.values + v) * scale[i];
+  part[t] = o;
   __syncthreads();
   if (grp == 0 && v < a.values) {
-    for (uint32_t k = 1; k < kJoinGroups; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] += part[k][lane][i];
+    for (uint32_t k = 1; k < groups && k < n; ++k) o += part[k * lanes + lane];
     o *= sum == 0.0f ? 0.0f : a.cache_scale / sum;
     *(HKV_GLOBAL v2u*)out = v2u{T::pack(o[0], o[1]), T::pack(o[2], o[3])};
   }
@@ -733,6 +734,7 @@ extern "C" __global__ __launch_bounds__(256) void hkv_mla_attend_weights(hkv::At
                    tok % kTile;
   const float* norm = a.norm + (uint64_t)s * a.n_heads;
   float sum = 0.0f;
+#pragma unroll 8
   for (uint32_t h = 0; h < a.n_heads; ++h) sum += exp_of(x[(uint64_t)h * kTile] - norm[h]);
   a.weights[(int64_t)s * a.weights_stride + tok] += sum;
 }
@@ -756,7 +758,9 @@ int launch_attend(const AttendArgs& a, int32_t dtype, int32_t cache_dtype, void*
   hipError_t e = hipLaunchKernel(main_fn, dim3(a.workers, a.head_tiles),
                                  dim3(attend_threads(a.head_tile)), params, 0, st);
   if (e == hipSuccess)
-    e = hipLaunchKernel(join_fn, dim3(a.n_seqs * a.n_heads, (a.values + 127) / 128),
+    e = hipLaunchKernel(join_fn,
+                        dim3(a.n_seqs * a.n_heads,
+                             (a.values + (4u << a.join_shift) - 1) / (4u << a.join_shift)),
                         dim3(kJoinThreads), params, 0, st);
   if (e == hipSuccess && a.weights)
     e = hipLaunchKernel(reinterpret_cast<const void*>(&hkv_mla_attend_weights),

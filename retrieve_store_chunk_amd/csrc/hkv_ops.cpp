@@ -105,11 +105,9 @@ hkv_status check_table(const hkv::Plan& p, int32_t n_seqs, int32_t max_blocks,
 }
 
 // ---------------------------------------------------------------- attention
-// One workgroup (16 waves, about 100 KB of LDS) fits a CU.  The head tiles of a
+// One workgroup (10 waves, about 125 KB of LDS) fits a CU.  The head tiles of a
 // batch of more than 32 heads run at once, those of one run of tokens on the
 // same XCD (a multiple of 8 apart), so that only the first reads from HBM.
-constexpr uint32_t kCus = 256;
-
 hkv_status plan_attend(const hkv_layout* layout, const hkv_mla_attend_args* a, bool weights,
                        hkv::AttendArgs* k, hkv::AttendWorkspace* ws) {
   const hkv::Plan& p = layout->plan;
@@ -143,9 +141,13 @@ hkv_status plan_attend(const hkv_layout* layout, const hkv_mla_attend_args* a, b
   const uint64_t tiles = (uint64_t)k->n_seqs * k->max_tiles;
   if (tiles > 0x7FFFFFFFull)
     return set_error(HKV_E_ARG, "n_seqs x max_blocks x N exceeds 2^36 tokens; split the batch");
-  const uint64_t fit = kCus / k->head_tiles / 8 * 8;
+  const uint64_t fit = hkv::kAttendMaxWorkers / k->head_tiles / 8 * 8;
   const uint64_t useful = (tiles + hkv::kAttendMinTiles - 1) / hkv::kAttendMinTiles;
   k->workers = (uint32_t)std::max<uint64_t>(1, std::min(fit, useful));
+  // 512, 128 or 64 columns a joining workgroup: all of them when there are
+  // workgroups enough to fill the card.
+  const uint64_t pairs = (uint64_t)k->n_seqs * k->n_heads;
+  k->join_shift = pairs >= 1024 ? 7 : pairs >= 256 ? 5 : 4;
   *ws = hkv::attend_workspace(k->workers, k->head_tiles, k->head_tile, k->values, k->n_seqs,
                               k->n_heads, k->max_tiles, weights);
   return HKV_OK;

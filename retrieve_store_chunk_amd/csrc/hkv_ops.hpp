@@ -14,7 +14,8 @@ namespace hkv {
 constexpr uint32_t kAttendTile = 32;        // cached tokens per step of a workgroup
 constexpr uint32_t kAttendMaxWidth = 576;   // values per cached row
 constexpr uint32_t kAttendMaxValues = 512;  // of them, values that are summed
-constexpr uint32_t kAttendMinTiles = 4;     // fewest tiles worth a worker of their own
+constexpr uint32_t kAttendMaxWorkers = 256; // one workgroup per CU
+constexpr uint32_t kAttendMinTiles = 1;     // fewest tiles worth a worker of their own
 
 // One call's geometry as the host plans it and the kernels follow it.
 struct AttendArgs {
@@ -40,6 +41,7 @@ struct AttendArgs {
   float cache_scale;
   uint32_t num_blocks, block_tokens, row_bytes, width, values;
   uint32_t n_seqs, n_heads, head_tile, head_tiles, max_blocks, workers;
+  uint32_t join_shift;   // lanes a joining group has (log2)
   uint32_t max_tiles;    // tiles of the longest sequence the table can hold
 };
 
