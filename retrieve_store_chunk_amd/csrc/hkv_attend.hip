@@ -166,11 +166,18 @@ struct Cursor {
 };
 
 // Largest value over the lanes that hold one column of a 16x16 result (lane,
-// lane ^ 16, lane ^ 32, lane ^ 48), and their sum.
+// lane ^ 16, lane ^ 32, lane ^ 48), and their sum.  The swaps exchange half the
+// rows of 16 (32) lanes of one register with the other half of a second: given
+// two copies of a value they leave both partners' values, without LDS.  (The
+// builtins' second result comes out equal to the first with this compiler.)
 __device__ __forceinline__ float column_max(float m) {
-  m = fmaxf(m, __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(  // lane ^ 16
-                                             __builtin_bit_cast(int, m), 0x401F)));
-  return fmaxf(m, lane_xor(m, 32));
+  float x = m, y = m;
+  asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  m = fmaxf(x, y);
+  x = m;
+  y = m;
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  return fmaxf(x, y);
 }
 __device__ __forceinline__ float column_sum(float m) {
   m += lane_xor(m, 16);
@@ -197,6 +204,7 @@ struct Attend {
   static_assert(kLoaders * 8 == kTile, "8 rows to a loader");
   static constexpr uint32_t kBatch = 3;    // k steps a scorer reads ahead
   static constexpr uint32_t kBuffers = 3;  // a tile is loaded, scored and summed in turn
+  static constexpr uint32_t kTileSlots = 4;
 
   // A tile on its way: this lane's pieces, which tile, its groups' states.
   struct Stage {
@@ -207,11 +215,11 @@ struct Attend {
   // The small arrays come first: the LDS instructions' 16-bit offsets reach
   // them, and the first row buffer, from one register.
   struct Lds {
+    uint32_t tile[kTileSlots][4];  // which tile the i-th is, its groups' states
     uint8_t p_hi[2][kHeads * kPPitch];
     uint8_t p_lo[2][kHeads * kPPitch];
     float alpha[2][kHeads];
     float m[kHeads], l[kHeads];
-    uint32_t tile[kBuffers][4];  // which tile a buffer holds, its groups' states
     uint32_t sums[kWaves];
     uint32_t start[2];
     __align__(16) uint8_t k[kBuffers][kTile * kPitch];
@@ -378,13 +386,16 @@ struct Attend {
       }
       fetch_ids(table, next, end, &cur);
     };
+    // Says what tile `slot` is: a round before it is scored, so that nobody
+    // waits for it.
+    uint32_t slot = 0;
+    auto announce = [&](const Stage& x) {
+      if (loader == 0 && lane == 0)
+        *(HKV_LDS v4u*)lds.tile[slot] = v4u{x.t, x.st[0], x.st[1], 0u};
+      slot = (slot + 1) % kTileSlots;
+    };
     auto stage = [&](Stage* x) {
       stage_tile(a, end, loader, lane, *x, (HKV_LDS uint8_t*)lds.k[buf]);
-      if (loader == 0 && lane == 0) {
-        lds.tile[buf][0] = x->t;
-        lds.tile[buf][1] = x->st[0];
-        lds.tile[buf][2] = x->st[1];
-      }
       buf = buf + 1 == kBuffers ? 0 : buf + 1;
       begin(x);
     };
@@ -392,6 +403,8 @@ struct Attend {
     begin(&xa);
     begin(&xb);
     uint32_t t = xa.t;
+    announce(xa);
+    announce(xb);
     stage(&xa);
     lds_barrier();
     // Two tiles a turn and one exit: xa and xb stay in their registers, and the
@@ -399,9 +412,11 @@ struct Attend {
     // staged as zeros and not looked at; after an odd number of tiles the other
     // roles wait for its round.
     while (t < t1) {
+      announce(xa);
       stage(&xb);
       lds_barrier();
       t = xa.t;
+      announce(xb);
       stage(&xa);
       lds_barrier();
     }
@@ -425,12 +440,15 @@ struct Attend {
       }
     }
     float m = -INFINITY, l = 0.0f;
-    uint32_t buf = 0, half = 0;
+    uint32_t buf = 0, half = 0, slot = 0;
     lds_barrier();
+    v4u info = *(const HKV_LDS v4u*)lds.tile[0];
     for (;;) {
-      const uint32_t t = uniform(lds.tile[buf][0]);
+      const uint32_t t = uniform(info[0]);
       if (t >= t1) break;
-      const uint32_t st[2] = {uniform(lds.tile[buf][1]), uniform(lds.tile[buf][2])};
+      const uint32_t st[2] = {uniform(info[1]), uniform(info[2])};
+      slot = (slot + 1) % kTileSlots;
+      info = *(const HKV_LDS v4u*)lds.tile[slot];  // the next tile's
       // S of 32 tokens (two 16-row results) x 16 heads.
       const HKV_LDS uint8_t* row = (const HKV_LDS uint8_t*)lds.k[buf] + col * kPitch + quad * 16;
       v4f sc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
@@ -507,13 +525,13 @@ struct Attend {
     for (uint32_t i = 0; i < kHeadTiles; ++i)
 #pragma unroll
       for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t buf = 0, half = 0;
+    uint32_t buf = 0, half = 0, slot = 0;
     lds_barrier();
     if (uniform(lds.tile[0][0]) < t1) {
       lds_barrier();  // the first tile's P is being made
       for (;;) {
-        const uint32_t next = buf + 1 == kBuffers ? 0 : buf + 1;
-        const uint32_t t_next = lds.tile[next][0];
+        slot = (slot + 1) % kTileSlots;
+        const uint32_t t_next = lds.tile[slot][0];
         const HKV_LDS uint8_t* vb = (const HKV_LDS uint8_t*)lds.k[buf] +
                                     (quad * 8 + (col >> 2)) * kPitch + (col & 3) * 8 + summer * 32;
         v4u ph[kHeadTiles], pl[kHeadTiles];
@@ -523,8 +541,10 @@ struct Attend {
           ph[i] = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_hi[half] + from);
           pl[i] = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_lo[half] + from);
           const float alpha = lds.alpha[half][i * 16 + col];
+          if (__any(alpha != 1.0f)) {  // rare once the maxima have settled
 #pragma unroll
-          for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] *= alpha;
+            for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] *= alpha;
+          }
         }
 #pragma unroll
         for (uint32_t j = 0; j < kOTiles; ++j) {
@@ -539,7 +559,7 @@ struct Attend {
 #pragma unroll
           for (uint32_t i = 0; i < kHeadTiles; ++i) acc[i][j] = T::mma(v, pl[i], acc[i][j]);
         }
-        buf = next;
+        buf = buf + 1 == kBuffers ? 0 : buf + 1;
         half ^= 1;
         if (uniform(t_next) >= t1) break;
         lds_barrier();
