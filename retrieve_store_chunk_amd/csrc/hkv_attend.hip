@@ -184,24 +184,23 @@ __device__ __forceinline__ float column_sum(float m) {
   return m + lane_xor(m, 32);
 }
 
-// The waves' roles: kLoaders bring rows into LDS, one wave per 16 heads takes
-// their logits and probabilities, kSummers add up the values.
-constexpr uint32_t kLoaders = 4, kSummers = 4;
-constexpr uint32_t attend_threads(uint32_t heads) {
-  return (kLoaders + heads / 16 + kSummers) * 64;
-}
+// The waves' roles: one scorer per 16 heads takes their logits and
+// probabilities, kCarriers bring rows into LDS and add up the values.
+constexpr uint32_t kCarriers = 8;
+constexpr uint32_t attend_threads(uint32_t heads) { return (heads / 16 + kCarriers) * 64; }
 
 template <class T, bool kFp8, uint32_t kHeads>
 struct Attend {
   static constexpr uint32_t kHeadTiles = kHeads / 16;
   static constexpr uint32_t kScorers = kHeadTiles;
-  static constexpr uint32_t kWaves = kLoaders + kScorers + kSummers;
+  static constexpr uint32_t kWaves = kScorers + kCarriers;
   static constexpr uint32_t kThreads = attend_threads(kHeads);
   static_assert(kThreads == kWaves * 64, "the launch has a wave for every role");
-  static constexpr uint32_t kOTiles = kValueTiles / kSummers;  // column tiles per summer
-  // A loader has 8 of a tile's rows, 8 lanes to a row, 16 bytes to a lane.
-  static constexpr uint32_t kLoads = (hkv::kAttendMaxWidth * (kFp8 ? 1 : 2) / 16 + 7) / 8;
-  static_assert(kLoaders * 8 == kTile, "8 rows to a loader");
+  static constexpr uint32_t kOTiles = kValueTiles / kCarriers;  // column tiles per carrier
+  // A carrier loads half of 8 of a tile's rows, 8 lanes to a row, 16 bytes to a
+  // lane and load.
+  static constexpr uint32_t kLoads = (hkv::kAttendMaxWidth * (kFp8 ? 1 : 2) / 16 + 15) / 16;
+  static_assert(kCarriers / 2 * 8 == kTile, "8 rows to two carriers");
   static constexpr uint32_t kBatch = 3;    // k steps a scorer reads ahead
   static constexpr uint32_t kBuffers = 3;  // a tile is loaded, scored and summed in turn
   static constexpr uint32_t kTileSlots = 4;
@@ -273,8 +272,8 @@ struct Attend {
   // pool's first bytes instead and is put to zero in stage_tile, so that the
   // loads need no branch and 0 x anything the memory holds never reaches a sum.
   static __device__ __forceinline__ void load_tile(const hkv::AttendArgs& a, const Cursor& c,
-                                                   uint32_t loader, uint32_t lane, Stage* x) {
-    const uint32_t g = loader >> 1, row = (loader & 1) * 8 + lane / 8;
+                                                   uint32_t carrier, uint32_t lane, Stage* x) {
+    const uint32_t g = carrier >> 1 & 1, row = (carrier & 1) * 8 + lane / 8;
     const uint32_t id = (uint32_t)(g ? c.id[1] : c.id[0]);
     const uint32_t off = g ? c.off[1] : c.off[0];
     const bool present = (g ? x->st[1] : x->st[0]) == kPresent;
@@ -283,7 +282,7 @@ struct Attend {
     const uint32_t pieces = a.row_bytes / 16;
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; ++i) {
-      const uint32_t k = i * 8 + (lane & 7);
+      const uint32_t k = ((carrier >> 2) + i * 2) * 8 + (lane & 7);
       x->x[i] = *(const HKV_GLOBAL v4u*)((const HKV_GLOBAL uint8_t*)base +
                                          (k < pieces ? row * a.row_bytes + k * 16 : 0));
     }
@@ -291,14 +290,15 @@ struct Attend {
 
   // Writes the loaded pieces to LDS, widening e4m3.
   static __device__ __forceinline__ void stage_tile(const hkv::AttendArgs& a, uint32_t end,
-                                                    uint32_t loader, uint32_t lane,
+                                                    uint32_t carrier, uint32_t lane,
                                                     const Stage& x, HKV_LDS uint8_t* lds) {
-    const uint32_t row = loader * 8 + lane / 8, pieces = a.row_bytes / 16;
-    const bool live = (loader >> 1 ? x.st[1] : x.st[0]) == kPresent && x.t * kTile + row < end;
+    const uint32_t row = (carrier & 3) * 8 + lane / 8, pieces = a.row_bytes / 16;
+    const bool live =
+        (carrier >> 1 & 1 ? x.st[1] : x.st[0]) == kPresent && x.t * kTile + row < end;
     HKV_LDS uint8_t* d = lds + row * kPitch;
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; ++i) {
-      const uint32_t k = i * 8 + (lane & 7);
+      const uint32_t k = ((carrier >> 2) + i * 2) * 8 + (lane & 7);
       v4u v = x.x[i];
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = live ? v[e] : 0u;
@@ -359,22 +359,69 @@ struct Attend {
   }
 
   // The roles' parts of one run of tiles [t0, t1) of a sequence.  Round i (the
-  // time between two barriers): the loaders write tile i + 1 to its buffer, the
-  // scorers make P of tile i, the summers add tile i - 1.  "Tile i" counts
-  // tiles that hold anything; the loaders say in lds.tile which one it is, and
-  // every role stops after the same round.
-  static __device__ __forceinline__ void load(const hkv::AttendArgs& a, Lds& lds, uint32_t loader,
-                                              uint32_t lane, const HKV_CONST int32_t* table,
-                                              uint32_t t0, uint32_t t1, uint32_t end) {
+  // time between two barriers): the carriers write tile i + 1 to its buffer and
+  // add tile i - 1, the scorers make P of tile i.  "Tile i" counts tiles that
+  // hold anything; the carriers say in lds.tile which one it is, a round before
+  // it is scored, and rounds go in pairs.
+
+  // Adds a tile: O^T of this wave's value columns (those past `values` are not
+  // written out) x all heads.  Transposing loads: in each group of 16 lanes,
+  // lane x supplies four columns of token x / 4 and receives column x of four
+  // tokens.
+  static __device__ __forceinline__ void add_tile(Lds& lds, uint32_t buf, uint32_t half,
+                                                  uint32_t carrier, uint32_t lane,
+                                                  v4f (&acc)[kHeadTiles][kOTiles]) {
+    const uint32_t col = lane & 15, quad = lane >> 4;
+    const HKV_LDS uint8_t* vb = (const HKV_LDS uint8_t*)lds.k[buf] +
+                                (quad * 8 + (col >> 2)) * kPitch + (col & 3) * 8 + carrier * 32;
+#pragma unroll
+    for (uint32_t i = 0; i < kHeadTiles; ++i) {
+      const float alpha = lds.alpha[half][i * 16 + col];
+      if (__any(alpha != 1.0f)) {  // rare once the maxima have settled
+#pragma unroll
+        for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] *= alpha;
+      }
+    }
+    v4u v[kOTiles];
+#pragma unroll
+    for (uint32_t j = 0; j < kOTiles; ++j) {
+      const HKV_LDS uint8_t* from = vb + j * kCarriers * 32;
+      const v2u lo = __builtin_bit_cast(
+          v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((HKV_LDS v4s*)from));
+      const v2u hi = __builtin_bit_cast(
+          v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((HKV_LDS v4s*)(from + 4 * kPitch)));
+      v[j] = v4u{lo[0], lo[1], hi[0], hi[1]};
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kHeadTiles; ++i) {
+      const uint32_t from = (i * 16 + col) * kPPitch + quad * 16;
+      const v4u ph = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_hi[half] + from);
+      const v4u pl = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_lo[half] + from);
+#pragma unroll
+      for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], ph, acc[i][j]);
+#pragma unroll
+      for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], pl, acc[i][j]);
+    }
+  }
+
+  static __device__ __forceinline__ void carry(const hkv::AttendArgs& a, Lds& lds,
+                                               uint32_t carrier, uint32_t lane,
+                                               const HKV_CONST int32_t* table, uint32_t t0,
+                                               uint32_t t1, uint32_t end,
+                                               v4f (&acc)[kHeadTiles][kOTiles]) {
+#pragma unroll
+    for (uint32_t i = 0; i < kHeadTiles; ++i)
+#pragma unroll
+      for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     Cursor cur;
     place(a, t0, &cur);
     fetch_ids(table, t0, end, &cur);
-    uint32_t next = t0, buf = 0;
+    uint32_t next = t0, slot = 0;
     // Loads the next tile that holds anything (x->t >= t1: there is none), and
     // asks for the ids of the one after it.
     auto begin = [&](Stage* x) {
       x->t = find_tile(a, table, next, t1, end, &cur, x->st);
-      load_tile(a, cur, loader, lane, x);
+      load_tile(a, cur, carrier, lane, x);
       next = x->t + 1;
 #pragma unroll
       for (uint32_t i = 0; i < 2; ++i) {
@@ -386,40 +433,46 @@ struct Attend {
       }
       fetch_ids(table, next, end, &cur);
     };
-    // Says what tile `slot` is: a round before it is scored, so that nobody
-    // waits for it.
-    uint32_t slot = 0;
     auto announce = [&](const Stage& x) {
-      if (loader == 0 && lane == 0)
+      if (carrier == 0 && lane == 0)
         *(HKV_LDS v4u*)lds.tile[slot] = v4u{x.t, x.st[0], x.st[1], 0u};
       slot = (slot + 1) % kTileSlots;
     };
-    auto stage = [&](Stage* x) {
-      stage_tile(a, end, loader, lane, *x, (HKV_LDS uint8_t*)lds.k[buf]);
-      buf = buf + 1 == kBuffers ? 0 : buf + 1;
+    auto stage = [&](Stage* x, uint32_t buf) {
+      stage_tile(a, end, carrier, lane, *x, (HKV_LDS uint8_t*)lds.k[buf]);
       begin(x);
     };
+    auto after = [](uint32_t buf) { return buf + 1 == kBuffers ? 0 : buf + 1; };
     Stage xa, xb;
     begin(&xa);
     begin(&xb);
-    uint32_t t = xa.t;
     announce(xa);
     announce(xb);
-    stage(&xa);
+    uint32_t t = xa.t;
+    stage(&xa, 0);
     lds_barrier();
-    // Two tiles a turn and one exit: xa and xb stay in their registers, and the
+    // Two rounds a turn and one exit: xa and xb stay in their registers, and the
     // waits for the loads know which of them is older.  A tile past the last is
-    // staged as zeros and not looked at; after an odd number of tiles the other
-    // roles wait for its round.
+    // staged as zeros and not looked at.
+    bool left = false;      // whether a tile waits to be added
+    uint32_t b0 = 0;        // the buffer of the round's scored tile
+    uint32_t b_last = 0;    // and of the tile before it
     while (t < t1) {
+      const uint32_t b1 = after(b0), b2 = after(b1);
       announce(xa);
-      stage(&xb);
+      left = xb.t < t1;     // of the tile scored in the second round
+      stage(&xb, b1);
+      if (b_last != b0) add_tile(lds, b_last, 1, carrier, lane, acc);
       lds_barrier();
       t = xa.t;
       announce(xb);
-      stage(&xa);
+      stage(&xa, b2);
+      add_tile(lds, b0, 0, carrier, lane, acc);
       lds_barrier();
+      b_last = b1;
+      b0 = b2;
     }
+    if (left) add_tile(lds, b_last, 1, carrier, lane, acc);
     lds_barrier();
   }
 
@@ -514,61 +567,6 @@ struct Attend {
     lds_barrier();
   }
 
-  // O^T of this wave's value columns (those past `values` are not written out)
-  // x all heads.  Transposing loads: in each group of 16 lanes, lane x supplies
-  // four columns of token x / 4 and receives column x of four tokens.
-  static __device__ __forceinline__ void sum(const hkv::AttendArgs& a, Lds& lds, uint32_t summer,
-                                             uint32_t lane, uint32_t t1,
-                                             v4f (&acc)[kHeadTiles][kOTiles]) {
-    const uint32_t col = lane & 15, quad = lane >> 4;
-#pragma unroll
-    for (uint32_t i = 0; i < kHeadTiles; ++i)
-#pragma unroll
-      for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t buf = 0, half = 0, slot = 0;
-    lds_barrier();
-    if (uniform(lds.tile[0][0]) < t1) {
-      lds_barrier();  // the first tile's P is being made
-      for (;;) {
-        slot = (slot + 1) % kTileSlots;
-        const uint32_t t_next = lds.tile[slot][0];
-        const HKV_LDS uint8_t* vb = (const HKV_LDS uint8_t*)lds.k[buf] +
-                                    (quad * 8 + (col >> 2)) * kPitch + (col & 3) * 8 + summer * 32;
-        v4u ph[kHeadTiles], pl[kHeadTiles];
-#pragma unroll
-        for (uint32_t i = 0; i < kHeadTiles; ++i) {
-          const uint32_t from = (i * 16 + col) * kPPitch + quad * 16;
-          ph[i] = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_hi[half] + from);
-          pl[i] = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_lo[half] + from);
-          const float alpha = lds.alpha[half][i * 16 + col];
-          if (__any(alpha != 1.0f)) {  // rare once the maxima have settled
-#pragma unroll
-            for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] *= alpha;
-          }
-        }
-#pragma unroll
-        for (uint32_t j = 0; j < kOTiles; ++j) {
-          const HKV_LDS uint8_t* from = vb + j * kSummers * 32;
-          const v2u lo = __builtin_bit_cast(
-              v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((HKV_LDS v4s*)from));
-          const v2u hi = __builtin_bit_cast(
-              v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((HKV_LDS v4s*)(from + 4 * kPitch)));
-          const v4u v = {lo[0], lo[1], hi[0], hi[1]};
-#pragma unroll
-          for (uint32_t i = 0; i < kHeadTiles; ++i) acc[i][j] = T::mma(v, ph[i], acc[i][j]);
-#pragma unroll
-          for (uint32_t i = 0; i < kHeadTiles; ++i) acc[i][j] = T::mma(v, pl[i], acc[i][j]);
-        }
-        buf = buf + 1 == kBuffers ? 0 : buf + 1;
-        half ^= 1;
-        if (uniform(t_next) >= t1) break;
-        lds_barrier();
-      }
-    }
-    if (half) lds_barrier();
-    lds_barrier();
-  }
-
   static __device__ __forceinline__ void run(const hkv::AttendArgs& a, Lds& lds) {
     const uint32_t worker = blockIdx.x, ht = blockIdx.y;
     const uint32_t wave = uniform(threadIdx.x >> 6);
@@ -599,16 +597,14 @@ struct Attend {
         a.spans[s * 4 + 2] = at == first ? 0 : 1;
       }
       const uint32_t lane = opaque(threadIdx.x & 63);
-      if (wave < kLoaders) {
-        const uint32_t end = t1 * kTile < len ? t1 * kTile : len;  // of what this worker loads
-        load(a, lds, wave, lane, (const HKV_CONST int32_t*)(a.table + (int64_t)s * a.table_stride),
-             t0, t1, end);
-      } else if (wave < kLoaders + kScorers) {
-        score(a, lds, wave - kLoaders, lane, s, ht, t1, len);
+      if (wave < kScorers) {
+        score(a, lds, wave, lane, s, ht, t1, len);
       } else {
-        const uint32_t summer = wave - kLoaders - kScorers;
+        const uint32_t carrier = wave - kScorers;
+        const uint32_t end = t1 * kTile < len ? t1 * kTile : len;  // of what this worker loads
         v4f acc[kHeadTiles][kOTiles];
-        sum(a, lds, summer, lane, t1, acc);
+        carry(a, lds, carrier, lane,
+              (const HKV_CONST int32_t*)(a.table + (int64_t)s * a.table_stride), t0, t1, end, acc);
         const uint32_t out_lane = opaque(lane), col = out_lane & 15, quad = out_lane >> 4;
         const bool whole = t0 == 0 && t1 == n_tiles;
         const uint64_t slot = ((uint64_t)worker * a.head_tiles + ht) * 2 + (at == first ? 0 : 1);
@@ -620,7 +616,7 @@ struct Attend {
           const float inv = whole ? (l == 0.0f ? 0.0f : a.cache_scale / l) : 1.0f;
 #pragma unroll
           for (uint32_t j = 0; j < kOTiles; ++j) {
-            const uint32_t v = (j * kSummers + summer) * 16 + quad * 4;
+            const uint32_t v = (j * kCarriers + carrier) * 16 + quad * 4;
             if (v >= a.values) continue;
             const v4f o = acc[i][j] * inv;
             if (whole) {
@@ -631,7 +627,7 @@ struct Attend {
               *(HKV_GLOBAL v4f*)(a.part_o + (slot * kHeads + hl) * a.values + v) = o;
             }
           }
-          if (summer == i && quad == 0) {
+          if (carrier == i && quad == 0) {
             if (whole) {
               write_lse(a, s, h, top, l);
             } else {
@@ -721,7 +717,8 @@ __device__ __forceinline__ void join(const hkv::AttendArgs& a) {
   }
 #define HKV_ATTEND_HEADS(suffix, T, fp8)               \
   HKV_ATTEND(hkv_mla_attend_##suffix##_h16, T, fp8, 16) \
-  HKV_ATTEND(hkv_mla_attend_##suffix##_h32, T, fp8, 32)
+  HKV_ATTEND(hkv_mla_attend_##suffix##_h32, T, fp8, 32) \
+  HKV_ATTEND(hkv_mla_attend_##suffix##_h64, T, fp8, 64)
 HKV_ATTEND_HEADS(bf16, Bf16, false)
 HKV_ATTEND_HEADS(fp16, Fp16, false)
 HKV_ATTEND_HEADS(bf16_e4m3, Bf16, true)
@@ -763,13 +760,13 @@ namespace hkv {
 
 int launch_attend(const AttendArgs& a, int32_t dtype, int32_t cache_dtype, void* stream) {
 #define HKV_FN(f) reinterpret_cast<const void*>(&f)
-  static const void* const kKernels[2][2][2] = {
-      {{HKV_FN(hkv_mla_attend_bf16_h16), HKV_FN(hkv_mla_attend_bf16_h32)},
-       {HKV_FN(hkv_mla_attend_bf16_e4m3_h16), HKV_FN(hkv_mla_attend_bf16_e4m3_h32)}},
-      {{HKV_FN(hkv_mla_attend_fp16_h16), HKV_FN(hkv_mla_attend_fp16_h32)},
-       {HKV_FN(hkv_mla_attend_fp16_e4m3_h16), HKV_FN(hkv_mla_attend_fp16_e4m3_h32)}}};
+#define HKV_SIZES(name) {HKV_FN(name##_h16), HKV_FN(name##_h32), HKV_FN(name##_h64)}
+  static const void* const kKernels[2][2][3] = {
+      {HKV_SIZES(hkv_mla_attend_bf16), HKV_SIZES(hkv_mla_attend_bf16_e4m3)},
+      {HKV_SIZES(hkv_mla_attend_fp16), HKV_SIZES(hkv_mla_attend_fp16_e4m3)}};
+#undef HKV_SIZES
   const uint32_t ty = dtype == HKV_FP16, fp8 = cache_dtype == HKV_E4M3;
-  const void* main_fn = kKernels[ty][fp8][a.head_tile == 32];
+  const void* main_fn = kKernels[ty][fp8][a.head_tile / 32];
   const void* join_fn = ty ? HKV_FN(hkv_mla_attend_join_fp16) : HKV_FN(hkv_mla_attend_join_bf16);
 #undef HKV_FN
   AttendArgs arg = a;

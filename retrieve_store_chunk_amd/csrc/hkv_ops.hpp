@@ -45,9 +45,12 @@ struct AttendArgs {
   uint32_t max_tiles;    // tiles of the longest sequence the table can hold
 };
 
-// Heads one workgroup takes; more heads are more head tiles, which read the
-// same rows at about the same time, through L2.
-inline constexpr uint32_t attend_head_tile(uint32_t n_heads) { return n_heads <= 16 ? 16u : 32u; }
+// Heads one workgroup takes: 16, 32 or 64, the least that holds all of them.
+// More than 64 heads are two head tiles, which read the same rows at about the
+// same time, through L2.
+inline constexpr uint32_t attend_head_tile(uint32_t n_heads) {
+  return n_heads <= 16 ? 16u : n_heads <= 32 ? 32u : 64u;
+}
 
 // Tiles per worker: an even share of all tiles, but no fewer than
 // kAttendMinTiles, so that short batches are not cut into more partial
