@@ -295,13 +295,16 @@ struct Attend {
     const uint32_t row = (carrier & 3) * 8 + lane / 8, pieces = a.row_bytes / 16;
     const bool live =
         (carrier >> 1 & 1 ? x.st[1] : x.st[0]) == kPresent && x.t * kTile + row < end;
+    const bool all_live = __all(live);
     HKV_LDS uint8_t* d = lds + row * kPitch;
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; ++i) {
       const uint32_t k = ((carrier >> 2) + i * 2) * 8 + (lane & 7);
       v4u v = x.x[i];
+      if (!all_live) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = live ? v[e] : 0u;
+        for (int e = 0; e < 4; ++e) v[e] = live ? v[e] : 0u;
+      }
       if (k >= pieces) continue;
       if constexpr (kFp8) {
         const v4u lo = {T::template widen<false>(v[0]), T::template widen<true>(v[0]),
@@ -494,6 +497,7 @@ struct Attend {
     }
     float m = -INFINITY, l = 0.0f;
     uint32_t buf = 0, half = 0, slot = 0;
+    __builtin_amdgcn_s_setprio(2);  // the carriers wait for P, with more waves to fill the time
     lds_barrier();
     v4u info = *(const HKV_LDS v4u*)lds.tile[0];
     for (;;) {
@@ -520,17 +524,24 @@ struct Attend {
             sc[r] = T::mma(k[o / kBatch & 1][o % kBatch][r], q[o], sc[r]);
         }
       }
+      sc[0] *= a.scale;
+      sc[1] *= a.scale;
+      if (st[0] != kPresent || st[1] != kPresent || t * kTile + kTile > len) {
+#pragma unroll
+        for (uint32_t r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (st[r] == kAbsent || t * kTile + r * 16 + quad * 4 + i >= len)
+              sc[r][i] = -INFINITY;
+            else if (st[r] == kBad)
+              sc[r][i] = NAN;
+          }
+      }
       float top = -INFINITY;
 #pragma unroll
       for (uint32_t r = 0; r < 2; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x = sc[r][i] * a.scale;
-          if (st[r] == kAbsent || t * kTile + r * 16 + quad * 4 + i >= len) x = -INFINITY;
-          else if (st[r] == kBad) x = NAN;
-          sc[r][i] = x;
-          top = fmaxf(top, x);
-        }
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[r][i]);
       if (a.logits && h < a.n_heads) {
         float* to = a.logits + (((uint64_t)s * a.max_tiles + t) * a.n_heads + h) * kTile + quad * 4;
         *(HKV_GLOBAL v4f*)to = sc[0];
@@ -558,6 +569,7 @@ struct Attend {
       half ^= 1;
       lds_barrier();
     }
+    __builtin_amdgcn_s_setprio(0);
     l = column_sum(l);
     if (quad == 0) {
       lds.m[hl] = m;
