@@ -32,6 +32,8 @@
 // result (m, l, unnormalised O) that hkv_mla_attend_join adds up.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "hkv.h"
 #include "hkv_ops.hpp"
 
@@ -157,6 +159,12 @@ enum RowState : uint32_t {
   kBad = 2      // a block id outside the pool
 };
 
+// The states of a tile's two groups in one word.
+constexpr uint32_t kBothAbsent = kAbsent | kAbsent << 2;
+__device__ __forceinline__ uint32_t state_of(uint32_t st, uint32_t group) {
+  return st >> (2 * group) & 3;
+}
+
 // Where the two row groups of a tile are: their entries of the block table,
 // their first token's place in the block, and the blocks' ids (asked for a
 // tile early).
@@ -189,8 +197,16 @@ __device__ __forceinline__ float column_sum(float m) {
 constexpr uint32_t kCarriers = 8;
 constexpr uint32_t attend_threads(uint32_t heads) { return (heads / 16 + kCarriers) * 64; }
 
-template <class T, bool kFp8, uint32_t kHeads>
+// Q: the type of q and out.  The products' type T is Q's for a cache of Q's
+// type, and fp16 for an e4m3 cache: fp16 holds every e4m3 value exactly, and a
+// bf16 query too once its head is scaled by a power of two (see score), and P
+// rounded to fp16's 11 bits is finer than a bf16 output, so that only an fp16
+// output needs P's second term.
+template <class Q, bool kFp8, uint32_t kHeads>
 struct Attend {
+  using T = std::conditional_t<kFp8, Fp16, Q>;
+  static constexpr bool kScaleQ = !std::is_same_v<Q, T>;
+  static constexpr bool kLow = !kScaleQ;  // P has a second term
   static constexpr uint32_t kHeadTiles = kHeads / 16;
   static constexpr uint32_t kScorers = kHeadTiles;
   static constexpr uint32_t kWaves = kScorers + kCarriers;
@@ -201,22 +217,22 @@ struct Attend {
   // lane and load.
   static constexpr uint32_t kLoads = (hkv::kAttendMaxWidth * (kFp8 ? 1 : 2) / 16 + 15) / 16;
   static_assert(kCarriers / 2 * 8 == kTile, "8 rows to two carriers");
-  static constexpr uint32_t kBatch = 3;    // k steps a scorer reads ahead
+  static constexpr uint32_t kAhead = 5;    // k steps a scorer reads ahead
   static constexpr uint32_t kBuffers = 3;  // a tile is loaded, scored and summed in turn
   static constexpr uint32_t kTileSlots = 4;
 
   // A tile on its way: this lane's pieces, which tile, its groups' states.
   struct Stage {
     v4u x[kLoads];
-    uint32_t t, st[2];
+    uint32_t t, st;
   };
 
   // The small arrays come first: the LDS instructions' 16-bit offsets reach
   // them, and the first row buffer, from one register.
   struct Lds {
-    uint32_t tile[kTileSlots][4];  // which tile the i-th is, its groups' states
+    uint32_t tile[kTileSlots][2];  // which tile the i-th is, its groups' states
     uint8_t p_hi[2][kHeads * kPPitch];
-    uint8_t p_lo[2][kHeads * kPPitch];
+    uint8_t p_lo[2][kLow ? kHeads * kPPitch : 16];
     float alpha[2][kHeads];
     float m[kHeads], l[kHeads];
     uint32_t sums[kWaves];
@@ -239,16 +255,19 @@ struct Attend {
       c->off[i] = (t * kTile + i * 16) - c->j[i] * a.block_tokens;
     }
   }
-  // The state of tile t's groups.
-  static __device__ __forceinline__ void states(const hkv::AttendArgs& a, uint32_t t,
-                                                uint32_t end, const Cursor& c, uint32_t* st) {
+  // The states of tile t's groups.
+  static __device__ __forceinline__ uint32_t states(const hkv::AttendArgs& a, uint32_t t,
+                                                    uint32_t end, const Cursor& c) {
+    uint32_t st = 0;
 #pragma unroll
     for (uint32_t i = 0; i < 2; ++i) {
       const uint32_t id = (uint32_t)c.id[i];
-      st[i] = t * kTile + i * 16 >= end || id == (uint32_t)HKV_NULL_BLOCK ? kAbsent
-              : id < a.num_blocks                                         ? kPresent
-                                                                          : kBad;
+      const uint32_t x = t * kTile + i * 16 >= end || id == (uint32_t)HKV_NULL_BLOCK ? kAbsent
+                         : id < a.num_blocks                                         ? kPresent
+                                                                                     : kBad;
+      st |= x << (2 * i);
     }
+    return st;
   }
   // From tile t (its ids fetched) to the first tile that holds anything, or to
   // t1: a null block costs one look at the table, not a tile's work for each
@@ -257,50 +276,57 @@ struct Attend {
                                                        const HKV_CONST int32_t* table,
                                                        uint32_t t, uint32_t t1, uint32_t end,
                                                        Cursor* c, uint32_t* st) {
-    states(a, t, end, *c, st);
-    while (st[0] == kAbsent && st[1] == kAbsent && t < t1) {
+    uint32_t now = states(a, t, end, *c);
+    while (now == kBothAbsent && t < t1) {
       const uint64_t next = (uint64_t)(c->j[1] + 1) * a.block_tokens / kTile;
       t = next < t1 ? (uint32_t)next : t1;
       place(a, t, c);
       fetch_ids(table, t, end, c);
-      states(a, t, end, *c, st);
+      now = states(a, t, end, *c);
     }
+    *st = now;
     return t;
   }
 
-  // Starts this lane's loads of its row of tile x->t.  What is absent loads the
-  // pool's first bytes instead and is put to zero in stage_tile, so that the
-  // loads need no branch and 0 x anything the memory holds never reaches a sum.
-  static __device__ __forceinline__ void load_tile(const hkv::AttendArgs& a, const Cursor& c,
-                                                   uint32_t carrier, uint32_t lane, Stage* x) {
-    const uint32_t g = carrier >> 1 & 1, row = (carrier & 1) * 8 + lane / 8;
-    const uint32_t id = (uint32_t)(g ? c.id[1] : c.id[0]);
-    const uint32_t off = g ? c.off[1] : c.off[0];
-    const bool present = (g ? x->st[1] : x->st[0]) == kPresent;
+  // Where this wave's rows of tile t are.  What is absent reads the pool's first
+  // bytes instead and is put to zero in stage_tile, so that the loads need no
+  // branch and 0 x anything the memory holds never reaches a sum.
+  static __device__ __forceinline__ const uint8_t* rows_of(const hkv::AttendArgs& a,
+                                                           const Cursor& c, uint32_t st,
+                                                           uint32_t carrier) {
+    const uint32_t g = carrier >> 1 & 1;
+    const uint32_t id = (uint32_t)(g ? c.id[1] : c.id[0]), off = g ? c.off[1] : c.off[0];
     const uint8_t* base = a.pages;
-    if (present) base += (uint64_t)id * a.stride + (uint64_t)off * a.row_bytes;
-    const uint32_t pieces = a.row_bytes / 16;
+    if (state_of(st, g) == kPresent)
+      base += (uint64_t)id * a.stride + (uint64_t)off * a.row_bytes;
+    return base;
+  }
+
+  static __device__ __forceinline__ void load_rows(const hkv::AttendArgs& a, const uint8_t* base,
+                                                   uint32_t carrier, uint32_t lane, v4u* x) {
+    const uint32_t row = (carrier & 1) * 8 + lane / 8, pieces = a.row_bytes / 16;
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; ++i) {
       const uint32_t k = ((carrier >> 2) + i * 2) * 8 + (lane & 7);
-      x->x[i] = *(const HKV_GLOBAL v4u*)((const HKV_GLOBAL uint8_t*)base +
-                                         (k < pieces ? row * a.row_bytes + k * 16 : 0));
+      x[i] = *(const HKV_GLOBAL v4u*)((const HKV_GLOBAL uint8_t*)base +
+                                      (k < pieces ? row * a.row_bytes + k * 16 : 0));
     }
   }
 
   // Writes the loaded pieces to LDS, widening e4m3.
   static __device__ __forceinline__ void stage_tile(const hkv::AttendArgs& a, uint32_t end,
-                                                    uint32_t carrier, uint32_t lane,
-                                                    const Stage& x, HKV_LDS uint8_t* lds) {
+                                                    uint32_t carrier, uint32_t lane, uint32_t t,
+                                                    uint32_t st, const v4u* x,
+                                                    HKV_LDS uint8_t* lds) {
     const uint32_t row = (carrier & 3) * 8 + lane / 8, pieces = a.row_bytes / 16;
     const bool live =
-        (carrier >> 1 & 1 ? x.st[1] : x.st[0]) == kPresent && x.t * kTile + row < end;
+        state_of(st, carrier >> 1 & 1) == kPresent && t * kTile + row < end;
     const bool all_live = __all(live);
     HKV_LDS uint8_t* d = lds + row * kPitch;
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; ++i) {
       const uint32_t k = ((carrier >> 2) + i * 2) * 8 + (lane & 7);
-      v4u v = x.x[i];
+      v4u v = x[i];
       if (!all_live) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = live ? v[e] : 0u;
@@ -399,11 +425,13 @@ struct Attend {
     for (uint32_t i = 0; i < kHeadTiles; ++i) {
       const uint32_t from = (i * 16 + col) * kPPitch + quad * 16;
       const v4u ph = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_hi[half] + from);
-      const v4u pl = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_lo[half] + from);
 #pragma unroll
       for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], ph, acc[i][j]);
+      if constexpr (kLow) {
+        const v4u pl = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_lo[half] + from);
 #pragma unroll
-      for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], pl, acc[i][j]);
+        for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], pl, acc[i][j]);
+      }
     }
   }
 
@@ -420,11 +448,11 @@ struct Attend {
     place(a, t0, &cur);
     fetch_ids(table, t0, end, &cur);
     uint32_t next = t0, slot = 0;
-    // Loads the next tile that holds anything (x->t >= t1: there is none), and
+    // Finds the next tile that holds anything (x->t >= t1: there is none) and
     // asks for the ids of the one after it.
-    auto begin = [&](Stage* x) {
-      x->t = find_tile(a, table, next, t1, end, &cur, x->st);
-      load_tile(a, cur, carrier, lane, x);
+    auto find = [&](Stage* x) {
+      x->t = find_tile(a, table, next, t1, end, &cur, &x->st);
+      const uint8_t* base = rows_of(a, cur, x->st, carrier);
       next = x->t + 1;
 #pragma unroll
       for (uint32_t i = 0; i < 2; ++i) {
@@ -435,20 +463,25 @@ struct Attend {
         }
       }
       fetch_ids(table, next, end, &cur);
+      return base;
     };
     auto announce = [&](const Stage& x) {
       if (carrier == 0 && lane == 0)
-        *(HKV_LDS v4u*)lds.tile[slot] = v4u{x.t, x.st[0], x.st[1], 0u};
+        *(HKV_LDS v2u*)lds.tile[slot] = v2u{x.t, x.st};
       slot = (slot + 1) % kTileSlots;
     };
+    // Writes a loaded tile to its buffer and starts the loads of another (found
+    // first: the scalar loads' wait would include the writes).
     auto stage = [&](Stage* x, uint32_t buf) {
-      stage_tile(a, end, carrier, lane, *x, (HKV_LDS uint8_t*)lds.k[buf]);
-      begin(x);
+      const uint32_t t_now = x->t, st_now = x->st;
+      const uint8_t* base = find(x);
+      stage_tile(a, end, carrier, lane, t_now, st_now, x->x, (HKV_LDS uint8_t*)lds.k[buf]);
+      load_rows(a, base, carrier, lane, x->x);
     };
     auto after = [](uint32_t buf) { return buf + 1 == kBuffers ? 0 : buf + 1; };
     Stage xa, xb;
-    begin(&xa);
-    begin(&xb);
+    load_rows(a, find(&xa), carrier, lane, xa.x);
+    load_rows(a, find(&xb), carrier, lane, xb.x);
     announce(xa);
     announce(xb);
     uint32_t t = xa.t;
@@ -495,45 +528,67 @@ struct Attend {
         q[i] = v;
       }
     }
+    float scale = a.scale;
+    if constexpr (kScaleQ) {
+      // The head's largest value goes to [2^14, 2^15): values down to 2^-31 of
+      // it stay exact in fp16, and what smaller ones lose is below the fp32 sum's
+      // rounding.  The power of two is taken out of the logits again.
+      float big = 0.0f;
+#pragma unroll
+      for (uint32_t i = 0; i < kWidthSteps; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          big = fmaxf(big, fmaxf(fabsf(Q::low(q[i][e])), fabsf(Q::high(q[i][e]))));
+      big = column_max(big);
+      int ex = 0;
+      if (big > 0.0f && big < INFINITY) ex = 14 - ilogbf(big);
+      ex = ex > 120 ? 120 : ex < -120 ? -120 : ex;
+      const float up = __builtin_ldexpf(1.0f, ex);
+      scale *= __builtin_ldexpf(1.0f, -ex);
+#pragma unroll
+      for (uint32_t i = 0; i < kWidthSteps; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t u = opaque(q[i][e]);  // unpacked again, not kept unpacked
+          q[i][e] = T::pack(Q::low(u) * up, Q::high(u) * up);
+        }
+    }
     float m = -INFINITY, l = 0.0f;
     uint32_t buf = 0, half = 0, slot = 0;
     __builtin_amdgcn_s_setprio(2);  // the carriers wait for P, with more waves to fill the time
     lds_barrier();
-    v4u info = *(const HKV_LDS v4u*)lds.tile[0];
+    v2u info = *(const HKV_LDS v2u*)lds.tile[0];
     for (;;) {
       const uint32_t t = uniform(info[0]);
       if (t >= t1) break;
-      const uint32_t st[2] = {uniform(info[1]), uniform(info[2])};
+      const uint32_t st = uniform(info[1]);
       slot = (slot + 1) % kTileSlots;
-      info = *(const HKV_LDS v4u*)lds.tile[slot];  // the next tile's
+      info = *(const HKV_LDS v2u*)lds.tile[slot];  // the next tile's
       // S of 32 tokens (two 16-row results) x 16 heads.
       const HKV_LDS uint8_t* row = (const HKV_LDS uint8_t*)lds.k[buf] + col * kPitch + quad * 16;
       v4f sc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-      v4u k[2][kBatch][2];  // the next steps' rows are read while these are multiplied
+      v4u k[kAhead + 1][2];  // rows are read kAhead steps before they are multiplied
 #pragma unroll
-      for (uint32_t i = 0; i < kWidthSteps + kBatch; ++i) {
+      for (uint32_t i = 0; i < kWidthSteps + kAhead; ++i) {
         if (i < kWidthSteps)
 #pragma unroll
           for (uint32_t r = 0; r < 2; ++r)
-            k[i / kBatch & 1][i % kBatch][r] =
-                *(const HKV_LDS v4u*)(row + r * 16 * kPitch + i * 64);
-        if (i >= kBatch) {
-          const uint32_t o = i - kBatch;
+            k[i % (kAhead + 1)][r] = *(const HKV_LDS v4u*)(row + r * 16 * kPitch + i * 64);
+        if (i >= kAhead)
 #pragma unroll
           for (uint32_t r = 0; r < 2; ++r)
-            sc[r] = T::mma(k[o / kBatch & 1][o % kBatch][r], q[o], sc[r]);
-        }
+            sc[r] = T::mma(k[(i - kAhead) % (kAhead + 1)][r], q[i - kAhead], sc[r]);
       }
-      sc[0] *= a.scale;
-      sc[1] *= a.scale;
-      if (st[0] != kPresent || st[1] != kPresent || t * kTile + kTile > len) {
+      sc[0] *= scale;
+      sc[1] *= scale;
+      if (st != 0 || t * kTile + kTile > len) {  // not all present
 #pragma unroll
         for (uint32_t r = 0; r < 2; ++r)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (st[r] == kAbsent || t * kTile + r * 16 + quad * 4 + i >= len)
+            if (state_of(st, r) == kAbsent || t * kTile + r * 16 + quad * 4 + i >= len)
               sc[r][i] = -INFINITY;
-            else if (st[r] == kBad)
+            else if (state_of(st, r) == kBad)
               sc[r][i] = NAN;
           }
       }
@@ -561,8 +616,9 @@ struct Attend {
         for (int i = 0; i < 4; ++i) l += p[i] = exp_of(sc[r][i] - base);
         const uint32_t h01 = T::pack(p[0], p[1]), h23 = T::pack(p[2], p[3]);
         *(HKV_LDS v2u*)(hi + r * 32) = v2u{h01, h23};
-        *(HKV_LDS v2u*)(lo + r * 32) = v2u{T::pack(p[0] - T::low(h01), p[1] - T::high(h01)),
-                                          T::pack(p[2] - T::low(h23), p[3] - T::high(h23))};
+        if constexpr (kLow)
+          *(HKV_LDS v2u*)(lo + r * 32) = v2u{T::pack(p[0] - T::low(h01), p[1] - T::high(h01)),
+                                            T::pack(p[2] - T::low(h23), p[3] - T::high(h23))};
       }
       if (quad == 0) lds.alpha[half][hl] = alpha;
       buf = buf + 1 == kBuffers ? 0 : buf + 1;
@@ -634,7 +690,7 @@ struct Attend {
             if (whole) {
               uint16_t* to = static_cast<uint16_t*>(a.out) + (int64_t)s * a.out_seq_stride +
                              (int64_t)h * a.out_head_stride + v;
-              *(HKV_GLOBAL v2u*)to = v2u{T::pack(o[0], o[1]), T::pack(o[2], o[3])};
+              *(HKV_GLOBAL v2u*)to = v2u{Q::pack(o[0], o[1]), Q::pack(o[2], o[3])};
             } else {
               *(HKV_GLOBAL v4f*)(a.part_o + (slot * kHeads + hl) * a.values + v) = o;
             }
