@@ -567,6 +567,7 @@ struct Attend {
       // S of 32 tokens (two 16-row results) x 16 heads.
       const HKV_LDS uint8_t* row = (const HKV_LDS uint8_t*)lds.k[buf] + col * kPitch + quad * 16;
       v4f sc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+      __builtin_amdgcn_sched_barrier(0);
       v4u k[kAhead + 1][2];  // rows are read kAhead steps before they are multiplied
 #pragma unroll
       for (uint32_t i = 0; i < kWidthSteps + kAhead; ++i) {
@@ -579,6 +580,17 @@ struct Attend {
           for (uint32_t r = 0; r < 2; ++r)
             sc[r] = T::mma(k[(i - kAhead) % (kAhead + 1)][r], q[i - kAhead], sc[r]);
       }
+      // The order just written, which the compiler would otherwise shorten to
+      // one read ahead: 2 kAhead LDS reads, then two products and two reads in
+      // turn (1450 -> 1000 cycles a tile).
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 0);
+#pragma unroll
+      for (uint32_t i = 0; i < kWidthSteps - kAhead; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, 2 * kAhead, 0);
+      __builtin_amdgcn_sched_barrier(0);
       sc[0] *= scale;
       sc[1] *= scale;
       if (st != 0 || t * kTile + kTile > len) {  // not all present
