@@ -403,36 +403,46 @@ struct Attend {
     const uint32_t col = lane & 15, quad = lane >> 4;
     const HKV_LDS uint8_t* vb = (const HKV_LDS uint8_t*)lds.k[buf] +
                                 (quad * 8 + (col >> 2)) * kPitch + (col & 3) * 8 + carrier * 32;
+    // Everything is read before anything is used: one wait instead of one for
+    // each read.
+    const HKV_LDS uint8_t* hi = (const HKV_LDS uint8_t*)lds.p_hi[half] + col * kPPitch + quad * 16;
+    const HKV_LDS uint8_t* lo = (const HKV_LDS uint8_t*)lds.p_lo[half] + col * kPPitch + quad * 16;
+    float alpha[kHeadTiles];
+    bool moved = false;
+    v4u v[kOTiles], p[kHeadTiles];
 #pragma unroll
-    for (uint32_t i = 0; i < kHeadTiles; ++i) {
-      const float alpha = lds.alpha[half][i * 16 + col];
-      if (__any(alpha != 1.0f)) {  // rare once the maxima have settled
+    for (uint32_t i = 0; i < kHeadTiles; ++i) alpha[i] = lds.alpha[half][i * 16 + col];
 #pragma unroll
-        for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] *= alpha;
-      }
-    }
-    v4u v[kOTiles];
+    for (uint32_t i = 0; i < kHeadTiles; ++i) p[i] = *(const HKV_LDS v4u*)(hi + i * 16 * kPPitch);
 #pragma unroll
     for (uint32_t j = 0; j < kOTiles; ++j) {
       const HKV_LDS uint8_t* from = vb + j * kCarriers * 32;
-      const v2u lo = __builtin_bit_cast(
+      const v2u x = __builtin_bit_cast(
           v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((HKV_LDS v4s*)from));
-      const v2u hi = __builtin_bit_cast(
+      const v2u y = __builtin_bit_cast(
           v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((HKV_LDS v4s*)(from + 4 * kPitch)));
-      v[j] = v4u{lo[0], lo[1], hi[0], hi[1]};
+      v[j] = v4u{x[0], x[1], y[0], y[1]};
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (uint32_t i = 0; i < kHeadTiles; ++i) moved |= alpha[i] != 1.0f;
+    if (__any(moved)) {  // rare once the maxima have settled
+#pragma unroll
+      for (uint32_t i = 0; i < kHeadTiles; ++i)
+#pragma unroll
+        for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] *= alpha[i];
     }
 #pragma unroll
     for (uint32_t i = 0; i < kHeadTiles; ++i) {
-      const uint32_t from = (i * 16 + col) * kPPitch + quad * 16;
-      const v4u ph = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_hi[half] + from);
 #pragma unroll
-      for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], ph, acc[i][j]);
-      if constexpr (kLow) {
-        const v4u pl = *(const HKV_LDS v4u*)((const HKV_LDS uint8_t*)lds.p_lo[half] + from);
-#pragma unroll
-        for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], pl, acc[i][j]);
-      }
+      for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], p[i], acc[i][j]);
+      if constexpr (kLow) p[i] = *(const HKV_LDS v4u*)(lo + i * 16 * kPPitch);
     }
+    if constexpr (kLow)
+#pragma unroll
+      for (uint32_t i = 0; i < kHeadTiles; ++i)
+#pragma unroll
+        for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], p[i], acc[i][j]);
   }
 
   static __device__ __forceinline__ void carry(const hkv::AttendArgs& a, Lds& lds,
