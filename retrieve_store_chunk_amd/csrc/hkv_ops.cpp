@@ -276,8 +276,15 @@ hkv_status plan_evict(const hkv_layout* layout, const hkv_mla_evict_args* a, hkv
   const uint64_t slots = (uint64_t)a->max_blocks * (uint64_t)p.block_size;
   k->max_moves =
       slots > k->budget ? (uint32_t)std::min<uint64_t>(k->budget, slots - k->budget) : 0u;
+  // Chunks of [0, budget) and of the slots after it.
+  auto chunks = [](uint64_t n) { return (n + hkv::kEvictChunkSlots - 1) / hkv::kEvictChunkSlots; };
+  if (slots > hkv::kEvictSelectSlots)
+    k->chunks = (uint32_t)(chunks(std::min<uint64_t>(k->budget, slots)) +
+                           chunks(slots > k->budget ? slots - k->budget : 0));
+  k->by_pairs = k->max_blocks <= hkv::kEvictPairBlocks &&
+                (uint64_t)k->n_seqs * k->max_blocks * k->max_blocks <= hkv::kEvictPairs;
   *w = hkv::evict_workspace(k->num_blocks, k->n_seqs, (uint64_t)k->n_layers * k->n_seqs,
-                            k->max_moves);
+                            k->max_moves, k->chunks, k->by_pairs != 0);
   return HKV_OK;
 }
 
@@ -361,6 +368,9 @@ hkv_status evict(const hkv_layout* layout, void* pool, const hkv_mla_evict_args*
   k.ok = reinterpret_cast<int32_t*>(wsb + w.ok);
   k.moves = reinterpret_cast<uint32_t*>(wsb + w.moves);
   k.lists = reinterpret_cast<uint32_t*>(wsb + w.lists);
+  k.hist = reinterpret_cast<uint32_t*>(wsb + w.hist);
+  k.totals = reinterpret_cast<uint32_t*>(wsb + w.totals);
+  k.least = reinterpret_cast<uint32_t*>(wsb + w.least);
   int dev = 0;
   st = stream_device(reinterpret_cast<hipStream_t>(stream), &dev);
   if (st != HKV_OK) return st;

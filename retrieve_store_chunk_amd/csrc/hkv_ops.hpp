@@ -85,6 +85,13 @@ int launch_attend(const AttendArgs& a, int32_t dtype, int32_t cache_dtype, void*
 
 // ---------------------------------------------------------------- eviction
 constexpr uint32_t kEvictMaxLayers = 64;
+constexpr uint32_t kEvictSelectSlots = 16384;  // a row's slots that one workgroup takes
+constexpr uint32_t kEvictChunkSlots = 8192;    // slots of a longer row per workgroup
+// Block ids are checked pair by pair up to this many of one sequence and this
+// many pairs for it, by counting in the workspace beyond (4 sequences of 2
+// blocks: 2 us against 12; 2^20 pairs: about 4 us).
+constexpr uint32_t kEvictPairBlocks = 1024;
+constexpr uint64_t kEvictPairs = uint64_t(1) << 20;
 
 struct EvictArgs {
   uint8_t* pool;
@@ -105,22 +112,30 @@ struct EvictArgs {
   int32_t* ok;           // [n_seqs] 1: the sequence can be evicted from
   uint32_t* moves;       // [rows]: slots that move
   uint32_t* lists;       // [rows][2 * max_moves]: freed slots, then the slots that fill them
+  uint32_t* hist;        // long rows: [rows][3][2048] keys by digit
+  uint32_t* totals;      // long rows: [rows][chunks][2] keys above the least kept, ties with it
+  uint32_t* least;       // long rows: [rows][2] the least kept key, how many ties with it stay
   uint32_t num_blocks, block_tokens, row_bytes;
   uint32_t n_layers, n_seqs, max_blocks, budget, sinks, recent;
   uint32_t max_moves;    // min(budget, max_blocks * block_tokens - budget)
+  uint32_t chunks;       // of a long row's slots; 0: rows are short
+  uint32_t by_pairs;     // how the block ids are checked
 };
 
 struct EvictWorkspace {
-  uint64_t claims, ok, moves, lists, total;
+  uint64_t claims, ok, moves, lists, hist, totals, least, total;
 };
 inline EvictWorkspace evict_workspace(uint64_t num_blocks, uint64_t n_seqs, uint64_t rows,
-                                      uint64_t max_moves) {
+                                      uint64_t max_moves, uint64_t chunks, bool by_pairs) {
   EvictWorkspace w{};
   w.claims = 0;
-  w.ok = w.claims + align256(num_blocks * 4);
+  w.ok = w.claims + (by_pairs ? 0 : align256(num_blocks * 4));
   w.moves = w.ok + align256(n_seqs * 4);
   w.lists = w.moves + align256(rows * 4);
-  w.total = w.lists + align256(rows * 2 * max_moves * 4);
+  w.hist = w.lists + align256(rows * 2 * max_moves * 4);
+  w.totals = w.hist + (chunks ? align256(rows * 3 * 2048 * 4) : 0);
+  w.least = w.totals + align256(rows * chunks * 2 * 4);
+  w.total = w.least + (chunks ? align256(rows * 2 * 4) : 0);
   return w;
 }
 
