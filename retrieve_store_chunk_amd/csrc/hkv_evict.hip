@@ -29,6 +29,7 @@
 namespace {
 
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef int32_t v4i __attribute__((ext_vector_type(4)));
 typedef float v4f_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef int32_t v4i_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -80,26 +81,31 @@ __device__ __forceinline__ void write_new_len(const hkv::EvictArgs& a, uint32_t 
 // Whether sequence s can be evicted from: a valid length, and every live block
 // id in the pool and named once in the call.  By comparing each id with each
 // (for calls with few ids; `own` holds the sequence's).
-__device__ __forceinline__ bool check_by_pairs(const hkv::EvictArgs& a, uint32_t s, int32_t* own,
+__device__ __forceinline__ bool check_by_pairs(const hkv::EvictArgs& a, uint32_t s, v4i* own,
                                                uint32_t* bad) {
   const uint32_t t = threadIdx.x;
   const int32_t len = a.lens[s];
   const uint32_t blocks = blocks_of(a, len);
   if (t == 0) *bad = !valid_len(a, len);
   __syncthreads();
-  for (uint32_t j = t; j < blocks; j += kThreads) {
-    const int32_t id = a.table[(int64_t)s * a.table_stride + j];
-    own[j] = id;
-    if (id < 0 || (uint32_t)id >= a.num_blocks) *bad = 1;
+  const uint32_t quads = (blocks + 3) / 4;
+  for (uint32_t j = t; j < quads * 4; j += kThreads) {
+    const int32_t id = j < blocks ? a.table[(int64_t)s * a.table_stride + j] : -1;
+    ((int32_t*)own)[j] = id;
+    if (j < blocks && (id < 0 || (uint32_t)id >= a.num_blocks)) *bad = 1;
   }
   __syncthreads();
   for (uint32_t i = t; i < a.n_seqs * a.max_blocks; i += kThreads) {
     const uint32_t s2 = i / a.max_blocks, j2 = i - s2 * a.max_blocks;
     if (j2 >= blocks_of(a, a.lens[s2])) continue;
     const int32_t id = a.table[(int64_t)s2 * a.table_stride + j2];
-    bool same = false;
-    for (uint32_t j = 0; j < blocks; ++j) same |= own[j] == id && !(s2 == s && j2 == j);
-    if (same) *bad = 1;
+    int same = s2 == s ? -1 : 0;  // it meets itself once
+#pragma unroll 4
+    for (uint32_t j = 0; j < quads; ++j) {
+      const v4i o = own[j];
+      same += (o[0] == id) + (o[1] == id) + (o[2] == id) + (o[3] == id);
+    }
+    if (id >= 0 && same > 0) *bad = 1;
   }
   __syncthreads();
   return *bad == 0;
@@ -147,34 +153,46 @@ __device__ __forceinline__ void find_bin(const uint32_t* hist, uint32_t left, ui
   __syncthreads();
 }
 
-// Up to kItems consecutive slots of a row, from `first` on.
+// A workgroup's slots [first, end) of a row, at most kItems x kThreads: group g
+// of four of thread t starts at first + (g x kThreads + t) x 4, so that a
+// wave's loads and stores are of consecutive bytes.
 template <uint32_t kItems>
 struct Slots {
+  static constexpr uint32_t kGroups = kItems / 4;
+  static_assert(kGroups >= 1 && kGroups <= 4, "a count of each group in 16 bits of 64");
   float w[kItems];
   int32_t pos[kItems];
   uint32_t key[kItems];
-  uint32_t first, n;  // n of them exist
+  uint32_t first, end;
+  __device__ __forceinline__ uint32_t slot(uint32_t i) const {
+    return first + (i / 4 * kThreads + threadIdx.x) * 4 + i % 4;
+  }
+  __device__ __forceinline__ bool live(uint32_t i) const { return slot(i) < end; }
   __device__ __forceinline__ void load(const hkv::EvictArgs& a, const float* wp,
-                                       const int32_t* pp, uint32_t at, uint32_t end,
+                                       const int32_t* pp, uint32_t from, uint32_t to,
                                        int32_t next) {
-    first = at;
-    n = at >= end ? 0 : end - at < kItems ? end - at : kItems;
-    if (n == kItems) {  // four at a time (aligned to one: global loads may be)
+    first = from;
+    end = to;
 #pragma unroll
-      for (uint32_t i = 0; i < kItems; i += 4) {
-        const v4f_a4 x = *(const HKV_GLOBAL v4f_a4*)(wp + at + i);
-        const v4i_a4 y = *(const HKV_GLOBAL v4i_a4*)(pp + at + i);
+    for (uint32_t g = 0; g < kGroups; ++g) {
+      const uint32_t at = slot(g * 4);
+      v4f_a4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+      v4i_a4 y = {0, 0, 0, 0};
+      if (at + 4 <= end) {  // (aligned to one value: global loads may be)
+        x = *(const HKV_GLOBAL v4f_a4*)(wp + at);
+        y = *(const HKV_GLOBAL v4i_a4*)(pp + at);
+      } else {
 #pragma unroll
-        for (uint32_t k = 0; k < 4; ++k) {
-          w[i + k] = x[k];
-          pos[i + k] = y[k];
-        }
+        for (uint32_t k = 0; k < 4; ++k)
+          if (at + k < end) {
+            x[k] = wp[at + k];
+            y[k] = pp[at + k];
+          }
       }
-    } else {
 #pragma unroll
-      for (uint32_t i = 0; i < kItems; ++i) {
-        w[i] = i < n ? wp[at + i] : 0.0f;
-        pos[i] = i < n ? pp[at + i] : 0;
+      for (uint32_t k = 0; k < 4; ++k) {
+        w[g * 4 + k] = x[k];
+        pos[g * 4 + k] = y[k];
       }
     }
 #pragma unroll
@@ -183,59 +201,106 @@ struct Slots {
   __device__ __forceinline__ void count(uint32_t* hist, uint32_t prefix, int d) const {
 #pragma unroll
     for (uint32_t i = 0; i < kItems; ++i)
-      if (i < n && (key[i] & above_mask(d)) == prefix)
+      if (live(i) && (key[i] & above_mask(d)) == prefix)
         atomicAdd(&hist[(key[i] >> digit_shift(d)) & digit_mask(d)], 1u);
   }
 };
 
+// The exclusive prefix over the workgroup of four 16-bit counts at once, and
+// their totals.
+__device__ __forceinline__ uint64_t block_scan4(uint64_t x, uint64_t* waves, uint64_t* total) {
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint64_t scan = x;
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t up = __shfl_up((unsigned long long)scan, d, 64);
+    if (lane >= (uint32_t)d) scan += up;
+  }
+  if (lane == 63) waves[wave] = scan;
+  __syncthreads();
+  uint64_t before = scan - x, all = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < kWaves; ++w) {
+    if (w < wave) before += waves[w];
+    all += waves[w];
+  }
+  __syncthreads();
+  *total = all;
+  return before;
+}
+
 // In slot order: which ties with the smallest kept key stay (the first `left`
-// of them), and the number of each move.  `ties`, `holes`, `movers`: how many
-// of each come before this thread's workgroup.  Writes the lists, and the
-// weights and positions of every slot that does not move.
-template <uint32_t kItems>
+// of them), and the number of each move.  `ties`, `moves`: how many ties, and
+// how many freed (or filling) slots, come before this workgroup's.  Writes the
+// lists, and the weights and positions of every slot that does not move; the
+// two slots of a move keep theirs for the move kernel.  kWhole: the workgroup
+// has the whole row, else slots of one side of the budget.
+template <uint32_t kItems, bool kWhole>
 __device__ __forceinline__ void assign(const hkv::EvictArgs& a, const Slots<kItems>& x,
                                        uint32_t row, uint32_t least, uint32_t left,
-                                       uint32_t* waves, uint32_t ties, uint32_t holes,
-                                       uint32_t movers, uint32_t* all_holes) {
-  uint32_t n = 0, all;
+                                       uint64_t* waves, uint32_t ties, uint32_t moves,
+                                       uint32_t* all_moves) {
+  constexpr uint32_t kGroups = Slots<kItems>::kGroups;
+  auto add_group = [](uint64_t n, uint32_t g, uint32_t by) { return n + ((uint64_t)by << 16 * g); };
+  auto group = [](uint64_t n, uint32_t g) { return (uint32_t)(n >> 16 * g) & 0xFFFFu; };
+  uint64_t n = 0, all;
 #pragma unroll
-  for (uint32_t i = 0; i < kItems; ++i) n += i < x.n && x.key[i] == least;
-  uint32_t rank = ties + block_scan(n, waves, &all);
-  uint32_t keep = 0, n_holes = 0, n_movers = 0;  // keep: one bit a slot
+  for (uint32_t i = 0; i < kItems; ++i) n = add_group(n, i / 4, x.live(i) && x.key[i] == least);
+  uint64_t before = block_scan4(n, waves, &all);
+  uint32_t keep = 0;  // one bit a slot
+  uint64_t m = 0;     // slots that are freed below the budget, or kept from it on
 #pragma unroll
-  for (uint32_t i = 0; i < kItems; ++i) {
-    if (i >= x.n) continue;
-    const bool tie = x.key[i] == least;
-    const bool k = x.key[i] > least || (tie && rank < left);
-    rank += tie;
-    keep |= (uint32_t)k << i;
-    if (x.first + i < a.budget)
-      n_holes += !k;
-    else
-      n_movers += k;
+  for (uint32_t g = 0; g < kGroups; ++g) {
+    uint32_t rank = ties + group(before, g);
+#pragma unroll
+    for (uint32_t i = g * 4; i < g * 4 + 4; ++i) {
+      if (!x.live(i)) continue;
+      const bool tie = x.key[i] == least;
+      const bool k = x.key[i] > least || (tie && rank < left);
+      rank += tie;
+      keep |= (uint32_t)k << i;
+      m = add_group(m, g, k != (x.slot(i) < a.budget));
+    }
+    ties += group(all, g);
   }
-  holes += block_scan(n_holes, waves, all_holes);
-  movers += block_scan(n_movers, waves, &all);
+  before = block_scan4(m, waves, &all);
+  uint32_t total = 0;
+#pragma unroll
+  for (uint32_t g = 0; g < kGroups; ++g) total += group(all, g);
+  // Over a whole row as many slots are freed as fill them.
+  *all_moves = kWhole ? total / 2 : total;
+  const uint32_t fill0 = kWhole ? total / 2 : 0;
   const int64_t base = meta_row(a, row);
   uint32_t* list = a.lists + (uint64_t)row * 2 * a.max_moves;
 #pragma unroll
-  for (uint32_t i = 0; i < kItems; ++i) {
-    if (i >= x.n) continue;
-    const uint32_t slot = x.first + i;
-    const bool k = keep >> i & 1;
-    if (slot < a.budget && k) {
-      a.weights_out[base + slot] = x.w[i];
-      a.positions_out[base + slot] = x.pos[i];
-    } else if (slot < a.budget) {
-      if (holes < a.max_moves) list[holes] = slot;
-      ++holes;
-    } else if (k) {
-      if (movers < a.max_moves) list[a.max_moves + movers] = slot;
-      ++movers;
-    } else {
-      a.weights_out[base + slot] = 0.0f;
-      a.positions_out[base + slot] = -1;
+  for (uint32_t g = 0; g < kGroups; ++g) {
+    uint32_t number = moves + group(before, g);
+    v4f_a4 wo;
+    v4i_a4 po;
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint32_t i = g * 4 + k, slot = x.slot(i);
+      const bool kept = keep >> i & 1, low = slot < a.budget;
+      wo[k] = low || kept ? x.w[i] : 0.0f;
+      po[k] = low || kept ? x.pos[i] : -1;
+      if (x.live(i) && kept != low) {
+        const uint32_t at = low ? number : number - fill0;
+        if (at < a.max_moves) list[(low ? 0 : a.max_moves) + at] = slot;
+        ++number;
+      }
     }
+    const uint32_t at = x.slot(g * 4);
+    if (at + 4 <= x.end) {
+      *(HKV_GLOBAL v4f_a4*)(a.weights_out + base + at) = wo;
+      *(HKV_GLOBAL v4i_a4*)(a.positions_out + base + at) = po;
+    } else {
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k)
+        if (at + k < x.end) {
+          a.weights_out[base + at + k] = wo[k];
+          a.positions_out[base + at + k] = po[k];
+        }
+    }
+    moves += group(all, g);
   }
 }
 
@@ -257,8 +322,9 @@ __device__ __forceinline__ void copy_meta(const hkv::EvictArgs& a, uint32_t row,
 template <uint32_t kItems>
 __device__ __forceinline__ void select(const hkv::EvictArgs& a) {
   __shared__ uint32_t hist[kBins];
-  __shared__ int32_t own[hkv::kEvictPairBlocks];
+  __shared__ v4i own[hkv::kEvictPairBlocks / 4];
   __shared__ uint32_t waves[kWaves];
+  __shared__ uint64_t waves4[kWaves];
   __shared__ uint32_t found[2];
   __shared__ uint32_t bad;
   const uint32_t row = blockIdx.x, s = row % a.n_seqs, t = threadIdx.x;
@@ -267,7 +333,7 @@ __device__ __forceinline__ void select(const hkv::EvictArgs& a) {
   const uint32_t len = valid_len(a, raw_len) ? (uint32_t)raw_len : 0u;
   // The loads are in flight while the block ids are checked.
   Slots<kItems> x;
-  x.load(a, a.weights + base, a.positions + base, t * kItems, len > a.budget ? len : 0u, next);
+  x.load(a, a.weights + base, a.positions + base, 0, len > a.budget ? len : 0u, next);
   bool ok;
   if (a.by_pairs) {
     ok = check_by_pairs(a, s, own, &bad);
@@ -292,9 +358,9 @@ __device__ __forceinline__ void select(const hkv::EvictArgs& a) {
     prefix |= bin << digit_shift(d);
     left -= above;
   }
-  uint32_t holes;
-  assign(a, x, row, prefix, left, waves, 0, 0, 0, &holes);
-  if (t == 0) a.moves[row] = holes;
+  uint32_t moves;
+  assign<kItems, true>(a, x, row, prefix, left, waves4, 0, 0, &moves);
+  if (t == 0) a.moves[row] = moves;
 }
 
 // ---------------------------------------------------------------- long rows
@@ -352,7 +418,7 @@ __device__ __forceinline__ void count_digit(const hkv::EvictArgs& a) {
   const uint32_t t = threadIdx.x;
   const int64_t base = meta_row(a, r.row);
   Slots<kChunkItems> x;
-  x.load(a, a.weights + base, a.positions + base, c.first + t * kChunkItems, c.end, r.next);
+  x.load(a, a.weights + base, a.positions + base, c.first, c.end, r.next);
   uint32_t prefix, left;
   prefix_of(a, r.row, kDigit, waves, found, &prefix, &left);
   hist[t] = 0;
@@ -416,7 +482,7 @@ extern "C" __global__ __launch_bounds__(kThreads) void hkv_mla_evict_check(hkv::
 // Long rows, before the first digit: cleared histograms, and (for calls with
 // few block ids) the check of each sequence.
 extern "C" __global__ __launch_bounds__(kThreads) void hkv_mla_evict_clear(hkv::EvictArgs a) {
-  __shared__ int32_t own[hkv::kEvictPairBlocks];
+  __shared__ v4i own[hkv::kEvictPairBlocks / 4];
   __shared__ uint32_t bad;
   const uint32_t row = blockIdx.x;
   uint32_t* h = a.hist + (uint64_t)row * 3 * kBins;
@@ -449,14 +515,13 @@ extern "C" __global__ __launch_bounds__(kThreads) void hkv_mla_evict_totals(hkv:
   if (!r.evicts) return;
   const int64_t base = meta_row(a, r.row);
   Slots<kChunkItems> x;
-  x.load(a, a.weights + base, a.positions + base, c.first + threadIdx.x * kChunkItems, c.end,
-         r.next);
+  x.load(a, a.weights + base, a.positions + base, c.first, c.end, r.next);
   uint32_t prefix, left, above = 0, ties = 0;
   prefix_of(a, r.row, 3, waves, found, &prefix, &left);
 #pragma unroll
   for (uint32_t i = 0; i < kChunkItems; ++i) {
-    above += i < x.n && x.key[i] > prefix;
-    ties += i < x.n && x.key[i] == prefix;
+    above += x.live(i) && x.key[i] > prefix;
+    ties += x.live(i) && x.key[i] == prefix;
   }
   uint32_t all_above, all_ties;
   block_scan(above, waves, &all_above);
@@ -475,6 +540,7 @@ extern "C" __global__ __launch_bounds__(kThreads) void hkv_mla_evict_totals(hkv:
 // Long rows: the lists, and the weights and positions of slots that do not move.
 extern "C" __global__ __launch_bounds__(kThreads) void hkv_mla_evict_assign(hkv::EvictArgs a) {
   __shared__ uint32_t waves[kWaves];
+  __shared__ uint64_t waves4[kWaves];
   const Row r = row_at(a);
   const Chunk c = chunk_at(a, blockIdx.x, r.len);
   if (!r.evicts) {
@@ -484,32 +550,36 @@ extern "C" __global__ __launch_bounds__(kThreads) void hkv_mla_evict_assign(hkv:
   }
   const int64_t base = meta_row(a, r.row);
   Slots<kChunkItems> x;
-  x.load(a, a.weights + base, a.positions + base, c.first + threadIdx.x * kChunkItems, c.end,
-         r.next);
+  x.load(a, a.weights + base, a.positions + base, c.first, c.end, r.next);
   const uint32_t least = a.least[r.row * 2], left = a.least[r.row * 2 + 1];
-  // What comes before this chunk, from the chunks' totals; and over all of the
-  // row's lower chunks the number of moves.
+  // From the chunks' totals: the ties and the moves before this chunk, and the
+  // row's moves.
   const uint32_t low = (a.budget + kChunkSlots - 1) / kChunkSlots;
-  uint32_t ties = 0, holes = 0, movers = 0, moves = 0, all_ties = 0;
-  for (uint32_t i = 0; i < a.chunks && (i < blockIdx.x || i < low); ++i) {
-    const uint32_t* tot = a.totals + ((uint64_t)r.row * a.chunks + i) * 2;
-    const Chunk ci = chunk_at(a, i, r.len);
-    const uint32_t open = all_ties < left ? left - all_ties : 0;  // ties that may still stay
-    const uint32_t kept = tot[0] + (tot[1] < open ? tot[1] : open);
-    const uint32_t freed = ci.end - ci.first - kept;
-    if (i < low) moves += freed;
-    if (i < blockIdx.x) {
-      ties += tot[1];
-      if (i < low)
-        holes += freed;
-      else
-        movers += kept;
+  const uint32_t mine = blockIdx.x, lowest = mine < low ? 0 : low;
+  uint32_t ties_all = 0, ties = 0, before = 0, moves = 0, all;
+  for (uint32_t i0 = 0; i0 < a.chunks; i0 += kThreads) {
+    const uint32_t i = i0 + threadIdx.x;
+    uint32_t above = 0, n_ties = 0;
+    if (i < a.chunks) {
+      const uint32_t* tot = a.totals + ((uint64_t)r.row * a.chunks + i) * 2;
+      above = tot[0];
+      n_ties = tot[1];
     }
-    all_ties += tot[1];
+    const uint32_t at = ties_all + block_scan(n_ties, waves, &all);
+    ties_all += all;
+    const uint32_t open = at < left ? left - at : 0;  // ties that may still stay
+    const uint32_t kept = above + (n_ties < open ? n_ties : open);
+    const Chunk ci = chunk_at(a, i < a.chunks ? i : 0, r.len);
+    const uint32_t n = i >= a.chunks ? 0 : i < low ? ci.end - ci.first - kept : kept;
+    block_scan(i < mine ? n_ties : 0, waves, &all);
+    ties += all;
+    block_scan(i >= lowest && i < mine ? n : 0, waves, &all);
+    before += all;
+    block_scan(i < low ? n : 0, waves, &all);
+    moves += all;
   }
-  uint32_t all;
-  assign(a, x, r.row, least, left, waves, ties, holes, movers, &all);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.moves[r.row] = moves;
+  assign<kChunkItems, false>(a, x, r.row, least, left, waves4, ties, before, &all);
+  if (mine == 0 && threadIdx.x == 0) a.moves[r.row] = moves;
 }
 
 namespace {
