@@ -587,27 +587,27 @@ namespace {
 constexpr uint32_t kMoveThreads = 256;
 constexpr uint32_t kMoveRows = 8;  // rows a wave moves together
 
-// The rows of one wave's moves, as one run of kUnit-byte pieces over all its
-// lanes.  Lane i < count holds row i's addresses.
+// One wave's rows, 8 lanes to a row: each lane copies every eighth piece of its
+// row, so that an instruction moves 128 consecutive bytes of each of 8 rows
+// and a lane needs one address of each side.  Lane i < count holds row i's.
 template <class V>
 __device__ __forceinline__ void move_rows(uint64_t src, uint64_t dst, uint32_t count,
                                           uint32_t row_bytes) {
-  const uint32_t lane = threadIdx.x & 63, per = row_bytes / sizeof(V), total = count * per;
-  constexpr uint32_t kUnroll = 3;
-  for (uint32_t c0 = 0; c0 < total; c0 += 64 * kUnroll) {
+  const uint32_t lane = threadIdx.x & 63, r = lane / 8, pieces = row_bytes / sizeof(V);
+  const uint64_t from = __shfl((unsigned long long)src, (int)r, 64);
+  const uint64_t to = __shfl((unsigned long long)dst, (int)r, 64);
+  if (r >= count) return;
+  const HKV_GLOBAL V* f = (const HKV_GLOBAL V*)from;
+  HKV_GLOBAL V* t = (HKV_GLOBAL V*)to;
+  constexpr uint32_t kUnroll = 9;
+  for (uint32_t c0 = lane & 7; c0 < pieces; c0 += 8 * kUnroll) {
     V v[kUnroll];
-    HKV_GLOBAL V* to[kUnroll];
-#pragma unroll
-    for (uint32_t u = 0; u < kUnroll; ++u) {
-      const uint32_t c = c0 + u * 64 + lane;
-      const uint32_t r = c < total ? c / per : 0, off = c - r * per;
-      const uint64_t from = __shfl((unsigned long long)src, (int)r, 64);
-      to[u] = (HKV_GLOBAL V*)__shfl((unsigned long long)dst, (int)r, 64) + off;
-      if (c < total) v[u] = __builtin_nontemporal_load((const HKV_GLOBAL V*)from + off);
-    }
 #pragma unroll
     for (uint32_t u = 0; u < kUnroll; ++u)
-      if (c0 + u * 64 + lane < total) __builtin_nontemporal_store(v[u], to[u]);
+      if (c0 + u * 8 < pieces) v[u] = __builtin_nontemporal_load(f + c0 + u * 8);
+#pragma unroll
+    for (uint32_t u = 0; u < kUnroll; ++u)
+      if (c0 + u * 8 < pieces) __builtin_nontemporal_store(v[u], t + c0 + u * 8);
   }
 }
 
