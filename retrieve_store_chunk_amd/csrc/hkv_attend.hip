@@ -540,18 +540,20 @@ struct Attend {
     }
     float scale = a.scale;
     if constexpr (kScaleQ) {
-      // The head's largest value goes to [2^14, 2^15): values down to 2^-31 of
+      // The head's largest finite value goes to [2^14, 2^15): values down to 2^-31 of
       // it stay exact in fp16, and what smaller ones lose is below the fp32 sum's
       // rounding.  The power of two is taken out of the logits again.
       float big = 0.0f;
 #pragma unroll
       for (uint32_t i = 0; i < kWidthSteps; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          big = fmaxf(big, fmaxf(fabsf(Q::low(q[i][e])), fabsf(Q::high(q[i][e]))));
+        for (int e = 0; e < 4; ++e) {
+          const float x = fabsf(Q::low(q[i][e])), y = fabsf(Q::high(q[i][e]));
+          big = fmaxf(big, fmaxf(x < INFINITY ? x : 0.0f, y < INFINITY ? y : 0.0f));
+        }
       big = column_max(big);
       int ex = 0;
-      if (big > 0.0f && big < INFINITY) ex = 14 - ilogbf(big);
+      if (big > 0.0f) ex = 14 - ilogbf(big);
       ex = ex > 120 ? 120 : ex < -120 ? -120 : ex;
       const float up = __builtin_ldexpf(1.0f, ex);
       scale *= __builtin_ldexpf(1.0f, -ex);

@@ -287,3 +287,21 @@ def test_rows_behind_four_gigabytes():
     c.d_table.fill_(59)
     assert L["pool_offset"] + 59 * L["stride"] > (1 << 32)
     c.run().check()
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-4, 1.0, 1e4, 1e20])
+def test_query_sizes_with_an_e4m3_cache(size):
+    """A bf16 query of any size next to e4m3 rows (the logits' scale undoes it)."""
+    c = Case([70, 300], heads=33, cache="e4m3", seed=22)
+    c.q = (c.q.float() * size * torch.logspace(-3, 3, 33, base=2.0, device="cuda").view(1, 33, 1)).to(c.dt)
+    c.scale = c.scale / size if size < 1e18 else float(np.float32(c.scale / size))
+    c.run().check()
+
+
+def test_an_infinite_query_value_keeps_the_others():
+    c = Case([40], heads=3, cache="e4m3", seed=23)
+    c.q[0, 1, 5] = math.inf
+    c.q[0, 1, 6] = 1e30
+    c.run()
+    assert c.out[0, 1].isnan().all()                # inf logits of both signs
+    assert c.out[0, 0].isfinite().all() and c.out[0, 2].isfinite().all()

@@ -238,3 +238,31 @@ def test_strided_metadata():
     assert c.w_out.stride() == c.d_w.stride()
     c.run()
     assert (out_w[:, :, c.cap:] == 9.0).all() and (out_p[:, :, c.cap:] == 9).all()
+
+
+@pytest.mark.parametrize("long_rows", [False, True])
+def test_many_blocks_are_counted(long_rows):
+    """Tables too large to compare id by id."""
+    if long_rows:
+        c = Case([16 * 1100 - 3, 5000, 17000], 9000, recent=100, layers=2, width=16, mla_bytes=1, seed=17)
+        assert c.table.shape[1] > 1024
+    else:
+        c = Case([8000] + [1000 + 7 * i for i in range(8)], 900, recent=50, layers=2, width=16, mla_bytes=1,
+                 seed=18, columns=512)
+        assert c.table.shape[0] * c.table.shape[1] ** 2 > 1 << 20
+    c.table[1, 7] = c.table[2, 9]
+    c.d_table = torch.from_numpy(c.table).cuda()
+    c.left = {1, 2}
+    c.run()
+    c = Case([16 * 1100 - 3, 5000, 17000], 9000, layers=1, width=16, mla_bytes=1, seed=19)
+    c.table[0, 700] = c.pool.blocks
+    c.table[1, 3] = -1
+    c.d_table = torch.from_numpy(c.table).cuda()
+    c.left = {0, 1}
+    c.run()
+
+
+def test_budgets_around_the_chunks_of_long_rows():
+    for n, budget in ((20000, 8192), (20000, 8191), (16385, 16384), (30000, 1), (24576, 16384)):
+        Case([n], budget, recent=min(budget, 7), layers=1, width=16, mla_bytes=1, seed=n + budget,
+             block_size=512, weights="ties").run()
