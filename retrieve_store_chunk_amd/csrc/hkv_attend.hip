@@ -32,6 +32,7 @@
 // result (m, l, unnormalised O) that hkv_mla_attend_join adds up.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "hkv.h"
@@ -829,23 +830,43 @@ extern "C" __global__ __launch_bounds__(kJoinThreads) void hkv_mla_attend_join_f
 
 // weights[s][t] += sum over heads of exp(s_ht - lse_h), from the logits that
 // the attention left in the workspace (4 bytes per head and token, where a
-// second pass over the cache would read a row again): one thread per token,
-// heads in order, so the result does not depend on the schedule.
+// second pass over the cache would read a row again).  kWeightParts threads
+// share a token, each takes every so many heads, and their sums are added in
+// order, so the result does not depend on the schedule.  Bound: the logits'
+// bytes, and for few tokens the latency of the loads, for which the parts are:
+// 1 sequence of 16000 tokens, 64 heads, 34.8 us with 4 parts, 37.2 with one
+// (the whole call); with 8 parts, that is 32 tokens a workgroup, a large call
+// loses (64 of 14001 tokens, 32 heads: 186 us, 206).
+constexpr uint32_t kWeightParts = 4;
+constexpr uint32_t kWeightTokens = 256 / kWeightParts;
+constexpr uint32_t kWeightGroups = 16384;  // workgroups at most: several pieces each if need be
+
 extern "C" __global__ __launch_bounds__(256) void hkv_mla_attend_weights(hkv::AttendArgs a) {
-  const uint32_t s = blockIdx.y;
-  const uint32_t len = served_len(a, s);
-  const uint32_t tok = blockIdx.x * 256 + threadIdx.x;
-  // (tiles of null blocks have no logits)
-  if (tok >= len ||
-      a.table[(int64_t)s * a.table_stride + tok / a.block_tokens] == HKV_NULL_BLOCK)
-    return;
-  const float* x = a.logits + ((uint64_t)s * a.max_tiles + tok / kTile) * a.n_heads * kTile +
-                   tok % kTile;
+  __shared__ float part[kWeightParts][kWeightTokens];
+  const uint32_t s = blockIdx.y, len = served_len(a, s);
+  const uint32_t col = threadIdx.x % kWeightTokens, p = threadIdx.x / kWeightTokens;
   const float* norm = a.norm + (uint64_t)s * a.n_heads;
-  float sum = 0.0f;
-#pragma unroll 8
-  for (uint32_t h = 0; h < a.n_heads; ++h) sum += exp_of(x[(uint64_t)h * kTile] - norm[h]);
-  a.weights[(int64_t)s * a.weights_stride + tok] += sum;
+  for (uint32_t at = blockIdx.x * kWeightTokens; at < len; at += gridDim.x * kWeightTokens) {
+    const uint32_t tok = at + col;
+    // (tiles of null blocks have no logits)
+    const bool live = tok < len && a.table[(int64_t)s * a.table_stride + tok / a.block_tokens] !=
+                                       HKV_NULL_BLOCK;
+    float sum = 0.0f;
+    if (live) {
+      const float* x = a.logits + ((uint64_t)s * a.max_tiles + tok / kTile) * a.n_heads * kTile +
+                       tok % kTile;
+#pragma unroll 4
+      for (uint32_t h = p; h < a.n_heads; h += kWeightParts)
+        sum += exp_of(x[(uint64_t)h * kTile] - norm[h]);
+    }
+    part[p][col] = sum;
+    __syncthreads();
+    if (p == 0 && live) {
+      for (uint32_t k = 1; k < kWeightParts; ++k) sum += part[k][col];
+      a.weights[(int64_t)s * a.weights_stride + tok] += sum;
+    }
+    __syncthreads();
+  }
 }
 
 namespace hkv {
@@ -873,8 +894,10 @@ int launch_attend(const AttendArgs& a, int32_t dtype, int32_t cache_dtype, void*
                         dim3(kJoinThreads), params, 0, st);
   if (e == hipSuccess && a.weights)
     e = hipLaunchKernel(reinterpret_cast<const void*>(&hkv_mla_attend_weights),
-                        dim3((a.max_tiles * kTile + 255) / 256, a.n_seqs), dim3(256), params, 0,
-                        st);
+                        dim3(std::min((a.max_tiles * kTile + kWeightTokens - 1) / kWeightTokens,
+                                      std::max(kWeightGroups / a.n_seqs, 1u)),
+                             a.n_seqs),
+                        dim3(256), params, 0, st);
   return (int)e;
 }
 

@@ -142,8 +142,7 @@ hkv_status plan_attend(const hkv_layout* layout, const hkv_mla_attend_args* a, b
   if (tiles > 0x7FFFFFFFull)
     return set_error(HKV_E_ARG, "n_seqs x max_blocks x N exceeds 2^36 tokens; split the batch");
   const uint64_t fit = hkv::kAttendMaxWorkers / k->head_tiles / 8 * 8;
-  const uint64_t useful = (tiles + hkv::kAttendMinTiles - 1) / hkv::kAttendMinTiles;
-  k->workers = (uint32_t)std::max<uint64_t>(1, std::min(fit, useful));
+  k->workers = (uint32_t)std::max<uint64_t>(1, std::min(fit, tiles));
   // 512, 128 or 64 columns a joining workgroup: all of them when there are
   // workgroups enough to fill the card.
   const uint64_t pairs = (uint64_t)k->n_seqs * k->n_heads;

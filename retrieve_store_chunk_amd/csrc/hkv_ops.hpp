@@ -15,7 +15,6 @@ constexpr uint32_t kAttendTile = 32;        // cached tokens per step of a workg
 constexpr uint32_t kAttendMaxWidth = 576;   // values per cached row
 constexpr uint32_t kAttendMaxValues = 512;  // of them, values that are summed
 constexpr uint32_t kAttendMaxWorkers = 256; // one workgroup per CU
-constexpr uint32_t kAttendMinTiles = 1;     // fewest tiles worth a worker of their own
 
 // One call's geometry as the host plans it and the kernels follow it.
 struct AttendArgs {
@@ -52,12 +51,16 @@ inline constexpr uint32_t attend_head_tile(uint32_t n_heads) {
   return n_heads <= 16 ? 16u : n_heads <= 32 ? 32u : 64u;
 }
 
-// Tiles per worker: an even share of all tiles, but no fewer than
-// kAttendMinTiles, so that short batches are not cut into more partial
-// results than their keys are worth.
+// Tiles per worker: an even share of all tiles, down to one, but three instead
+// of two: a worker's start and the joining of its result cost about as much as
+// a tile, so that a third fewer of them outweigh one more tile each (1 sequence
+// of 16000 tokens: 18.9 us for 20.0 with 16 heads, 28.3 for 30.3 with 64; 24 of
+// 700: 18.7 for 20.0).  More than that is no gain where the tiles are few (4
+// sequences of 2300 tokens, 16 heads: 16.5 us with one tile each, 17.7 with
+// three, 19.4 with four).
 inline constexpr uint64_t attend_share(uint64_t tiles, uint64_t workers) {
   const uint64_t s = (tiles + workers - 1) / workers;
-  return s < kAttendMinTiles ? kAttendMinTiles : s;
+  return s == 2 ? 3 : s;
 }
 
 // Workspace sections, each on a 256-byte boundary.
