@@ -105,9 +105,9 @@ hkv_status check_table(const hkv::Plan& p, int32_t n_seqs, int32_t max_blocks,
 }
 
 // ---------------------------------------------------------------- attention
-// One workgroup (10 waves, about 125 KB of LDS) fits a CU.  The head tiles of a
-// batch of more than 32 heads run at once, those of one run of tokens on the
-// same XCD (a multiple of 8 apart), so that only the first reads from HBM.
+// One workgroup (9 to 12 waves, about 120 KB of LDS) fits a CU.  The head tiles
+// of a batch run at once, those of one run of tokens on the same XCD (a
+// multiple of 8 apart), so that only the first reads from HBM.
 hkv_status plan_attend(const hkv_layout* layout, const hkv_mla_attend_args* a, bool weights,
                        hkv::AttendArgs* k, hkv::AttendWorkspace* ws) {
   const hkv::Plan& p = layout->plan;
@@ -133,18 +133,20 @@ hkv_status plan_attend(const hkv_layout* layout, const hkv_mla_attend_args* a, b
   k->values = (uint32_t)a->value_width;
   k->n_seqs = (uint32_t)a->n_seqs;
   k->n_heads = (uint32_t)a->n_heads;
-  k->head_tile = hkv::attend_head_tile(k->n_heads);
-  k->head_tiles = (k->n_heads + k->head_tile - 1) / k->head_tile;
   k->max_blocks = (uint32_t)a->max_blocks;
   const uint64_t tokens = (uint64_t)a->max_blocks * (uint64_t)p.block_size;
   k->max_tiles = (uint32_t)((tokens + hkv::kAttendTile - 1) / hkv::kAttendTile);
   const uint64_t tiles = (uint64_t)k->n_seqs * k->max_tiles;
   if (tiles > 0x7FFFFFFFull)
     return set_error(HKV_E_ARG, "n_seqs x max_blocks x N exceeds 2^36 tokens; split the batch");
+  k->head_tile = hkv::attend_head_tile(k->n_heads, tiles * ((k->n_heads + 15) / 16), bytes == 1);
+  k->head_tiles = (k->n_heads + k->head_tile - 1) / k->head_tile;
   const uint64_t fit = hkv::kAttendMaxWorkers / k->head_tiles / 8 * 8;
   k->workers = (uint32_t)std::max<uint64_t>(1, std::min(fit, tiles));
-  // 512, 128 or 64 columns a joining workgroup: all of them when there are
-  // workgroups enough to fill the card.
+  // 512, 128 or 64 columns a joining workgroup: few (sequence, head) pairs are
+  // spread over more workgroups, many need no more (in us, with 64, 128 and 512:
+  // 1 sequence of 16000 tokens, 16 heads 18.8, 21.4, 38.6; 22 of 2011, 16 heads
+  // 23.9, 22.5, 23.7; 64 of 500, 64 heads 66.5, 50.2, 39.3).
   const uint64_t pairs = (uint64_t)k->n_seqs * k->n_heads;
   k->join_shift = pairs >= 1024 ? 7 : pairs >= 256 ? 5 : 4;
   *ws = hkv::attend_workspace(k->workers, k->head_tiles, k->head_tile, k->values, k->n_seqs,

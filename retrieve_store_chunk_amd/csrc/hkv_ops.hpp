@@ -44,11 +44,21 @@ struct AttendArgs {
   uint32_t max_tiles;    // tiles of the longest sequence the table can hold
 };
 
-// Heads one workgroup takes: 16, 32 or 64, the least that holds all of them.
-// More than 64 heads are two head tiles, which read the same rows at about the
-// same time, through L2.
-inline constexpr uint32_t attend_head_tile(uint32_t n_heads) {
-  return n_heads <= 16 ? 16u : n_heads <= 32 ? 32u : 64u;
+// Heads one workgroup takes.  `units`: the tiles that the tables can hold, times
+// the groups of 16 heads, which is as much as the host knows of a call's size.
+// More heads to a workgroup read a row from L2 and from LDS for fewer
+// workgroups, but make its rounds longer and the partial results of a short
+// call more: with 16 heads, 32 and 64 to a workgroup
+//   1 sequence of 1000 tokens, 64 heads: 14.4, 15.5, 19.3 us
+//   16 of up to 2400: 28.1, 29.1, 37.6 (7600 units)
+//   16 of up to 4800: 37.6, 34.0, 43.9 (11000)
+//   16 of up to 20000: 101.7, 75.8, 82.7 (42000); 40000: 182.8, 128.0, 125.5
+// An e4m3 cache has half the bytes to wait for in a round and turns earlier
+// (16 of up to 9600: 57.1, 46.2, 47.1 at 20000 units; 20000: 95.6, 67.7, 62.7).
+inline constexpr uint32_t attend_head_tile(uint32_t n_heads, uint64_t units, bool fp8) {
+  const uint32_t most = units <= 8192 ? 16u : units <= (fp8 ? 24576u : 49152u) ? 32u : 64u;
+  const uint32_t need = n_heads <= 16 ? 16u : n_heads <= 32 ? 32u : 64u;
+  return need < most ? need : most;
 }
 
 // Tiles per worker: an even share of all tiles, down to one, but three instead

@@ -148,6 +148,21 @@ def test_types(dtype, cache, heads):
          weights=True).run().check()
 
 
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"),
+                                         ("fp16", "e4m3")])
+@pytest.mark.parametrize("heads", [20, 32, 64, 100, 128])
+@pytest.mark.parametrize("columns", [2000, 5300])
+def test_wide_tables_take_more_heads_to_a_workgroup(dtype, cache, heads, columns):
+    Case([1, 400, 0, 97, 33], heads=heads, dtype=dtype, cache=cache, seed=heads, block_size=16,
+         columns=columns, weights=True).run().check()
+
+
+@pytest.mark.parametrize("heads", [40, 64, 128])
+def test_a_wide_table_of_split_sequences(heads):
+    Case([9001, 40, 3000], heads=heads, seed=heads, block_size=944, columns=180,
+         holes=[(0, 1), (2, 0)]).run().check()
+
+
 @pytest.mark.parametrize("width,values", [(32, 16), (32, 32), (64, 48), (96, 96), (160, 128),
                                           (320, 256), (544, 512), (576, 576 - 64), (576, 208)])
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
