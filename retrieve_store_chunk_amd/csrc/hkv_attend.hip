@@ -15,21 +15,31 @@
 // with 16x16x32 matrix instructions and fp32 accumulators.  P is split into
 // two 16-bit terms (p = hi + lo, about 16 significant bits for bf16), because
 // one rounding of P to 16 bits would be as large as the rounding of the
-// output itself.  e4m3 rows are widened to the query's type as they are
-// staged, which is exact.
+// output itself; see Attend for an e4m3 cache, whose rows are widened to fp16
+// as they are staged, which is exact.
 //
-// Bound: reading the cache once (row_bytes per token).  A tile's rows are
-// loaded two tiles ahead into registers and written to the other of two LDS
-// buffers one tile ahead, so a tile's loads have a whole tile's time to
-// arrive.  LDS rows are padded to an odd multiple of 32 bytes: eight rows at
-// the same column, and four rows of the transposing loads, then fall into
-// different banks.
+// Bound: reading the cache once (row_bytes per token).  The waves have roles,
+// so that loads, both products and the softmax of different tiles overlap:
+// scorers (one for 16 heads) turn a tile into P, 8 carriers load rows and sum
+// values.  In the round between two barriers tile i + 1 goes to LDS, tile i is
+// scored, tile i - 1 is summed (three row buffers), and the rows of tiles i + 2
+// and i + 3 are on their way in the carriers' registers.  (1 sequence of 10^6
+// tokens, 32 heads: 273 us when all waves loaded, scored and summed in turn, 215
+// with roles; a round is 1.7 us there.)  LDS rows are padded to an odd multiple
+// of 32 bytes: eight rows at the same column, and four rows of the transposing
+// loads, then fall into different banks.
 //
 // The batch's tiles, all sequences after one another, are cut into equal
 // runs, one per worker (workgroup), whatever the lengths are: a million-token
 // sequence and a ragged batch both fill the card, and no length is needed on
 // the host.  A worker whose run covers part of a sequence leaves a partial
 // result (m, l, unnormalised O) that hkv_mla_attend_join adds up.
+//
+// Measured: 64 ragged sequences of up to 14001 tokens, 32 heads, bf16 (648 MB)
+// 137 us, 4.7 TB/s; 1 of 10^6 tokens (1.15 GB) 215 us, 5.4 TB/s; 24 of up to
+// 40000, 64 heads, e4m3, a third of the blocks null (234 MB, 54 GFLOP) 101 us,
+// where the two products' LDS reads fill the rounds; 1 of 333 tokens 12 us, two
+// launches and one round.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -8,7 +8,9 @@
 // row, the sums over rows are joined across the workgroup through LDS.
 //
 // Bound: reading and writing the page (2 x heads x d x d x 4 bytes a
-// sequence); the arithmetic is 7 flops a value.  The state's loads are issued
+// sequence); the arithmetic is 7 flops a value.  Measured: 256 sequences, 32
+// heads of 128, a fifth without a state (1.01 GB) 183 us, 5.5 TB/s; 1 sequence, 16
+// heads 6.6 us, a launch.  The state's loads are issued
 // first, and the conv, the norms and the check of the block ids run while they
 // are in flight.
 //
@@ -195,8 +197,11 @@ __device__ __forceinline__ void step(const hkv::KdaArgs& a) {
 
 }  // namespace
 
-// (threads: 8 rows a thread at d = 128, so that 3 workgroups and their loads fit
-// a CU; with 16 rows a step of 256 sequences took 188 us, with 8 185 us.)
+// Threads by head dim, so that a thread holds up to 16 rows of 4 columns and its
+// state stays in registers (256 sequences, 32 heads: d = 64 67 us with 256
+// threads, 70 with 512, 625 with 128, which spill; d = 128 203 us with 512, 202
+// with 256, 304 with 1024; 16 sequences 12.1, 12.9, 18.1; 16 heads of d = 256 386
+// us with 1024, 666 with 512; d = 32 23 us with 64, 22 with 128, 29 with 256).
 #define HKV_KDA(name, T, d, threads)                                                        \
   extern "C" __global__ __launch_bounds__(threads, (threads) == 512 ? 6 : 4) void name(     \
       hkv::KdaArgs a) {                                                                     \

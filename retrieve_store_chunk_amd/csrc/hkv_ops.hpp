@@ -100,9 +100,11 @@ int launch_attend(const AttendArgs& a, int32_t dtype, int32_t cache_dtype, void*
 constexpr uint32_t kEvictMaxLayers = 64;
 constexpr uint32_t kEvictSelectSlots = 16384;  // a row's slots that one workgroup takes
 constexpr uint32_t kEvictChunkSlots = 8192;    // slots of a longer row per workgroup
-// Block ids are checked pair by pair up to this many of one sequence and this
-// many pairs for it, by counting in the workspace beyond (4 sequences of 2
-// blocks: 2 us against 12; 2^20 pairs: about 4 us).
+// Block ids are checked pair by pair, by every workgroup for its sequence, up to
+// this many of one sequence and this many pairs for it; beyond by counting in the
+// workspace, a launch of one workgroup (16 sequences of 128 blocks of 16 tokens:
+// 18 us for the call, 32 when counted; at the limit, 4 of 512: 37 and 40, 1 of
+// 1024: 38 and 45; pairs grow with the square).
 constexpr uint32_t kEvictPairBlocks = 1024;
 constexpr uint64_t kEvictPairs = uint64_t(1) << 20;
 
