@@ -218,6 +218,10 @@ struct Attend {
   using T = std::conditional_t<kFp8, Fp16, Q>;
   static constexpr bool kScaleQ = !std::is_same_v<Q, T>;
   static constexpr bool kLow = !kScaleQ;  // P has a second term
+  // P in fp16 is taken 2^15 times as large (P <= 1), and O with it: beside a
+  // weight of 1, fp16 would round those below 2^-14 ever more coarsely and lose
+  // those below 2^-25, which a long sequence holds many of.
+  static constexpr float kUp = std::is_same_v<T, Fp16> ? 32768.0f : 1.0f;
   static constexpr uint32_t kHeadTiles = kHeads / 16;
   static constexpr uint32_t kScorers = kHeadTiles;
   static constexpr uint32_t kWaves = kScorers + kCarriers;
@@ -648,7 +652,11 @@ struct Attend {
       for (uint32_t r = 0; r < 2; ++r) {
         float p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) l += p[i] = exp_of(sc[r][i] - base);
+        for (int i = 0; i < 4; ++i) {
+          p[i] = exp_of(sc[r][i] - base);
+          l += p[i];
+          p[i] *= kUp;
+        }
         const uint32_t h01 = T::pack(p[0], p[1]), h23 = T::pack(p[2], p[3]);
         *(HKV_LDS v2u*)(hi + r * 32) = v2u{h01, h23};
         if constexpr (kLow)
@@ -716,7 +724,8 @@ struct Attend {
           const uint32_t hl = i * 16 + col, h = ht * kHeads + hl;
           const float l = lds.l[hl], top = lds.m[hl];
           if (h >= a.n_heads) continue;
-          const float inv = whole ? (l == 0.0f ? 0.0f : a.cache_scale / l) : 1.0f;
+          const float inv =
+              (whole ? (l == 0.0f ? 0.0f : a.cache_scale / l) : 1.0f) * (1.0f / kUp);
 #pragma unroll
           for (uint32_t j = 0; j < kOTiles; ++j) {
             const uint32_t v = (j * kCarriers + carrier) * 16 + quad * 4;

@@ -163,6 +163,36 @@ def test_a_wide_table_of_split_sequences(heads):
          holes=[(0, 1), (2, 0)]).run().check()
 
 
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"),
+                                         ("fp16", "e4m3")])
+def test_the_many_beside_one_large_weight(dtype, cache):
+    """One token takes nearly all the weight and has the value 0, so the output
+    is what the 31 others, e^-L below it, add up to.  Their P is rounded to
+    11 bits where it is kept as one term (e4m3 with bf16) and to 16 or more
+    otherwise; a logit of L and its difference to the largest are off by 4 L
+    2^-24, the sums by 64 2^-24, and the output is rounded once."""
+    c = Case([32], heads=16, dtype=dtype, cache=cache, seed=1, block_size=32)
+    top = torch.tensor([1.0, 4.0, 8.0, 10.0, 11.0, 12.0, 12.5, 13.0, 13.5, 14.0, 14.5, 15.0, 15.5,
+                        16.0, 17.0, 18.0])
+    stored = 448.0 if cache == "e4m3" else 28.0
+    row = torch.zeros(32, 576)
+    row[1:, :512] = stored
+    row[0, 575] = 1 / c.cache_scale
+    rows = c.pool.rows(c.layer, torch.uint8 if c.cache.itemsize == 1 else c.cache)
+    rows[c.table[0, 0], :32] = (row.to(c.cache).view(torch.uint8) if cache == "e4m3"
+                                else row.to(c.cache)).cuda()
+    c.q.zero_()
+    c.q[0, :, 575] = top.to(c.dt).cuda()
+    c.scale = 1.0
+    c.run()
+    p = 31 * torch.exp(-top.double())
+    want = (28.0 * p / (1 + p)).view(-1, 1)
+    u, h = 2.0 ** -24, half_step(c.dt)
+    term = 2.0 ** -11 if (dtype, cache) == ("bf16", "e4m3") else 2.0 ** -16
+    tol = want * (h + term + (4 * 18 + 64) * u) * (1 + h) + torch.finfo(c.dt).tiny * h
+    assert (c.out[0].cpu().double() - want).abs().le(tol).all()
+
+
 @pytest.mark.parametrize("width,values", [(32, 16), (32, 32), (64, 48), (96, 96), (160, 128),
                                           (320, 256), (544, 512), (576, 576 - 64), (576, 208)])
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
