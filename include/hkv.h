@@ -9,20 +9,24 @@
  *   store    : block-table gather, pool pages -> chunk objects;
  *   retrieve : scatter of chunk objects into newly allocated block ids.
  *
- * Pages are opaque bytes: the KDA state (recurrent heads x d x d plus conv
- * (conv_dim, kernel-1)) is one opaque page, as LMCache treats it ("Kimi-Linear"
- * and "Kimi K3" recipes, introduction; "Hybrid Attention Models",
- * Mamba / Linear-Attention Hybrids), so the copies are exact byte copies.
+ * and runs the operators of a decode step that read and update the pool's
+ * pages in place: MLA attention, eviction by attention weight, the KDA step.
+ *
+ * To the copies pages are opaque bytes: the KDA state (recurrent heads x d x d
+ * plus conv (conv_dim, kernel-1)) is one opaque page, as LMCache treats it
+ * ("Kimi-Linear" and "Kimi K3" recipes, introduction; "Hybrid Attention
+ * Models", Mamba / Linear-Attention Hybrids), so they are exact byte copies.
  *
  * Conventions for every call:
  *   - returns hkv_status: HKV_OK (0) or a negative error code; nothing aborts
  *     or throws; hkv_last_error() gives a message for the calling thread;
  *   - all validation happens on the host, synchronously, before any work is
- *     enqueued; a call that returns an error has enqueued nothing (except
- *     HKV_E_HIP, which reports a failure of the HIP runtime itself);
+ *     enqueued (but of the DEVICE tables that the decode step's operators
+ *     take, see there); a call that returns an error has enqueued nothing
+ *     (except HKV_E_HIP, which reports a failure of the HIP runtime itself);
  *   - "HOST" arrays are read only during the call; "DEVICE" buffers must stay
  *     allocated until the stream has passed the enqueued work;
- *   - store/retrieve enqueue on the caller's stream and never synchronise it.
+ *   - work is enqueued on the caller's stream, which is never synchronised.
  *
  * Sizes are bytes unless stated; block ids are int32 in [0, num_blocks).
  */

@@ -10,9 +10,8 @@
 // Bound: reading and writing the page (2 x heads x d x d x 4 bytes a
 // sequence); the arithmetic is 7 flops a value.  Measured: 256 sequences, 32
 // heads of 128, a fifth without a state (1.01 GB) 183 us, 5.5 TB/s; 1 sequence, 16
-// heads 6.6 us, a launch.  The state's loads are issued
-// first, and the conv, the norms and the check of the block ids run while they
-// are in flight.
+// heads 6.7 us, a launch.  The state's loads are issued first, and the conv, the
+// norms and the check of the block ids run while they are in flight.
 //
 // One workgroup owns a head entirely (its q, k and v channels of the conv
 // state too), so a page may be updated in place without any other workgroup
