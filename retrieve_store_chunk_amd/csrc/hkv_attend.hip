@@ -317,14 +317,17 @@ struct Attend {
     return base;
   }
 
+  template <bool kStream>
   static __device__ __forceinline__ void load_rows(const hkv::AttendArgs& a, const uint8_t* base,
                                                    uint32_t carrier, uint32_t lane, v4u* x) {
     const uint32_t row = (carrier & 1) * 8 + lane / 8, pieces = a.row_bytes / 16;
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; ++i) {
       const uint32_t k = ((carrier >> 2) + i * 2) * 8 + (lane & 7);
-      x[i] = *(const HKV_GLOBAL v4u*)((const HKV_GLOBAL uint8_t*)base +
-                                      (k < pieces ? row * a.row_bytes + k * 16 : 0));
+      const HKV_GLOBAL v4u* from =
+          (const HKV_GLOBAL v4u*)((const HKV_GLOBAL uint8_t*)base +
+                                  (k < pieces ? row * a.row_bytes + k * 16 : 0));
+      x[i] = kStream ? __builtin_nontemporal_load(from) : *from;
     }
   }
 
@@ -460,6 +463,7 @@ struct Attend {
         for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], p[i], acc[i][j]);
   }
 
+  template <bool kStream>
   static __device__ __forceinline__ void carry(const hkv::AttendArgs& a, Lds& lds,
                                                uint32_t carrier, uint32_t lane,
                                                const HKV_CONST int32_t* table, uint32_t t0,
@@ -501,12 +505,12 @@ struct Attend {
       const uint32_t t_now = x->t, st_now = x->st;
       const uint8_t* base = find(x);
       stage_tile(a, end, carrier, lane, t_now, st_now, x->x, (HKV_LDS uint8_t*)lds.k[buf]);
-      load_rows(a, base, carrier, lane, x->x);
+      load_rows<kStream>(a, base, carrier, lane, x->x);
     };
     auto after = [](uint32_t buf) { return buf + 1 == kBuffers ? 0 : buf + 1; };
     Stage xa, xb;
-    load_rows(a, find(&xa), carrier, lane, xa.x);
-    load_rows(a, find(&xb), carrier, lane, xb.x);
+    load_rows<kStream>(a, find(&xa), carrier, lane, xa.x);
+    load_rows<kStream>(a, find(&xb), carrier, lane, xb.x);
     announce(xa);
     announce(xb);
     uint32_t t = xa.t;
@@ -714,8 +718,12 @@ struct Attend {
         const uint32_t carrier = wave - kScorers;
         const uint32_t end = t1 * kTile < len ? t1 * kTile : len;  // of what this worker loads
         v4f acc[kHeadTiles][kOTiles];
-        carry(a, lds, carrier, lane,
-              (const HKV_CONST int32_t*)(a.table + (int64_t)s * a.table_stride), t0, t1, end, acc);
+        const HKV_CONST int32_t* table =
+            (const HKV_CONST int32_t*)(a.table + (int64_t)s * a.table_stride);
+        if (a.streams)
+          carry<true>(a, lds, carrier, lane, table, t0, t1, end, acc);
+        else
+          carry<false>(a, lds, carrier, lane, table, t0, t1, end, acc);
         const uint32_t out_lane = opaque(lane), col = out_lane & 15, quad = out_lane >> 4;
         const bool whole = t0 == 0 && t1 == n_tiles;
         const uint64_t slot = ((uint64_t)worker * a.head_tiles + ht) * 2 + (at == first ? 0 : 1);

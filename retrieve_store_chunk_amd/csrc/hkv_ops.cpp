@@ -143,6 +143,7 @@ hkv_status plan_attend(const hkv_layout* layout, const hkv_mla_attend_args* a, b
   k->head_tiles = (k->n_heads + k->head_tile - 1) / k->head_tile;
   const uint64_t fit = hkv::kAttendMaxWorkers / k->head_tiles / 8 * 8;
   k->workers = (uint32_t)std::max<uint64_t>(1, std::min(fit, tiles));
+  k->streams = tiles * hkv::kAttendTile * k->row_bytes > hkv::kAttendStreamBytes;
   // 512, 128 or 64 columns a joining workgroup: few (sequence, head) pairs are
   // spread over more workgroups, many need no more (in us, with 64, 128 and 512:
   // 1 sequence of 16000 tokens, 16 heads 18.8, 21.4, 38.6; 22 of 2011, 16 heads

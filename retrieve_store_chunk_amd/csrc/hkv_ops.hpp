@@ -15,6 +15,13 @@ constexpr uint32_t kAttendTile = 32;        // cached tokens per step of a workg
 constexpr uint32_t kAttendMaxWidth = 576;   // values per cached row
 constexpr uint32_t kAttendMaxValues = 512;  // of them, values that are summed
 constexpr uint32_t kAttendMaxWorkers = 256; // one workgroup per CU
+// Rows of a call whose tables can hold more than the last-level cache are read
+// past the caches (nontemporal): they cannot be there from the call before, and
+// should not evict what is (1 sequence of 10^6 tokens, 32 heads: 191 us, 213
+// without; 64 of up to 14001: 126, 140).  Smaller calls keep them, where a layer
+// that is read again finds them (16 of up to 9000, 32 heads: 36 us, 39 past the
+// caches; 16 of up to 2400, 64 heads: 27, 29.5).
+constexpr uint64_t kAttendStreamBytes = uint64_t(256) << 20;
 
 // One call's geometry as the host plans it and the kernels follow it.
 struct AttendArgs {
@@ -40,6 +47,7 @@ struct AttendArgs {
   float cache_scale;
   uint32_t num_blocks, block_tokens, row_bytes, width, values;
   uint32_t n_seqs, n_heads, head_tile, head_tiles, max_blocks, workers;
+  uint32_t streams;      // rows are read past the caches
   uint32_t join_shift;   // lanes a joining group has (log2)
   uint32_t max_tiles;    // tiles of the longest sequence the table can hold
 };

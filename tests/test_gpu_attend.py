@@ -157,6 +157,13 @@ def test_wide_tables_take_more_heads_to_a_workgroup(dtype, cache, heads, columns
          columns=columns, weights=True).run().check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads", [7, 32, 48])
+def test_e4m3_tables_of_more_than_the_last_level_cache(dtype, heads):
+    Case([1, 400, 0, 97, 1200], heads=heads, dtype=dtype, cache="e4m3", seed=heads, block_size=16,
+         columns=6100, holes=[(1, 3), (4, 0)], weights=True).run().check()
+
+
 @pytest.mark.parametrize("heads", [40, 64, 128])
 def test_a_wide_table_of_split_sequences(heads):
     Case([9001, 40, 3000], heads=heads, seed=heads, block_size=944, columns=180,
