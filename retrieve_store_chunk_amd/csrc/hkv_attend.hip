@@ -24,8 +24,8 @@
 // values.  In the round between two barriers tile i + 1 goes to LDS, tile i is
 // scored, tile i - 1 is summed (three row buffers), and the rows of tiles i + 2
 // and i + 3 are on their way in the carriers' registers.  (1 sequence of 10^6
-// tokens, 32 heads: 273 us when all waves loaded, scored and summed in turn, 215
-// with roles; a round is 1.7 us there.)  LDS rows are padded to an odd multiple
+// tokens, 32 heads: 273 us when all waves loaded, scored and summed in turn, 220
+// with roles; a round is 1.5 us now.)  LDS rows are padded to an odd multiple
 // of 32 bytes: eight rows at the same column, and four rows of the transposing
 // loads, then fall into different banks.
 //
@@ -36,10 +36,10 @@
 // result (m, l, unnormalised O) that hkv_mla_attend_join adds up.
 //
 // Measured: 64 ragged sequences of up to 14001 tokens, 32 heads, bf16 (648 MB)
-// 137 us, 4.7 TB/s; 1 of 10^6 tokens (1.15 GB) 215 us, 5.4 TB/s; 24 of up to
-// 40000, 64 heads, e4m3, a third of the blocks null (234 MB, 54 GFLOP) 101 us,
-// where the two products' LDS reads fill the rounds; 1 of 333 tokens 12 us, two
-// launches and one round.
+// 126 us, 5.1 TB/s; 1 of 10^6 tokens (1.15 GB) 190 us, 6.1 TB/s, what a large
+// read reaches; 24 of up to 40000, 64 heads, e4m3, a third of the blocks null
+// (229 MB, 55 GFLOP) 100 us, where the two products' LDS reads fill the rounds; 1
+// of 333 tokens 12 us, two launches and one round.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
