@@ -400,17 +400,28 @@ __device__ __forceinline__ Row row_at(const hkv::EvictArgs& a) {
   return r;
 }
 
-// The first `digits` digits of the least kept key, from the histograms.
+// The first `digits` digits of the least kept key and how many keys with them
+// stay: the last of them from its histogram, the ones before it from what the
+// launch before found.  The row's first workgroup leaves the result for the next.
 __device__ __forceinline__ void prefix_of(const hkv::EvictArgs& a, uint32_t row, int digits,
                                           uint32_t* waves, uint32_t* found, uint32_t* prefix,
                                           uint32_t* left) {
   *prefix = 0;
   *left = a.budget;
-  for (int d = 0; d < digits; ++d) {
-    uint32_t bin, above;
-    find_bin(a.hist + ((uint64_t)row * 3 + d) * kBins, *left, waves, found, &bin, &above);
-    *prefix |= bin << digit_shift(d);
-    *left -= above;
+  if (digits == 0) return;
+  uint32_t* least = a.least + (uint64_t)row * 3 * 2 + (digits - 1) * 2;
+  if (digits > 1) {
+    *prefix = least[-2];
+    *left = least[-1];
+  }
+  const int d = digits - 1;
+  uint32_t bin, above;
+  find_bin(a.hist + ((uint64_t)row * 3 + d) * kBins, *left, waves, found, &bin, &above);
+  *prefix |= bin << digit_shift(d);
+  *left -= above;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    least[0] = *prefix;
+    least[1] = *left;
   }
 }
 
@@ -537,10 +548,6 @@ extern "C" __global__ __launch_bounds__(kThreads) void hkv_mla_evict_totals(hkv:
     uint32_t* out = a.totals + ((uint64_t)r.row * a.chunks + blockIdx.x) * 2;
     out[0] = all_above;
     out[1] = all_ties;
-    if (blockIdx.x == 0) {
-      a.least[r.row * 2] = prefix;
-      a.least[r.row * 2 + 1] = left;
-    }
   }
 }
 
@@ -558,7 +565,7 @@ extern "C" __global__ __launch_bounds__(kThreads) void hkv_mla_evict_assign(hkv:
   const int64_t base = meta_row(a, r.row);
   Slots<kChunkItems> x;
   x.load(a, a.weights + base, a.positions + base, c.first, c.end, r.next);
-  const uint32_t least = a.least[r.row * 2], left = a.least[r.row * 2 + 1];
+  const uint32_t least = a.least[r.row * 6 + 4], left = a.least[r.row * 6 + 5];
   // From the chunks' totals: the ties and the moves before this chunk, and the
   // row's moves.
   const uint32_t low = (a.budget + kChunkSlots - 1) / kChunkSlots;

@@ -137,7 +137,8 @@ struct EvictArgs {
   uint32_t* lists;       // [rows][2 * max_moves]: freed slots, then the slots that fill them
   uint32_t* hist;        // long rows: [rows][3][2048] keys by digit
   uint32_t* totals;      // long rows: [rows][chunks][2] keys above the least kept, ties with it
-  uint32_t* least;       // long rows: [rows][2] the least kept key, how many ties with it stay
+  uint32_t* least;       // long rows: [rows][3][2] after each digit: the least kept key so far,
+                         // how many keys that match it stay
   uint32_t num_blocks, block_tokens, row_bytes;
   uint32_t n_layers, n_seqs, max_blocks, budget, sinks, recent;
   uint32_t max_moves;    // min(budget, max_blocks * block_tokens - budget)
@@ -158,7 +159,7 @@ inline EvictWorkspace evict_workspace(uint64_t num_blocks, uint64_t n_seqs, uint
   w.hist = w.lists + align256(rows * 2 * max_moves * 4);
   w.totals = w.hist + (chunks ? align256(rows * 3 * 2048 * 4) : 0);
   w.least = w.totals + align256(rows * chunks * 2 * 4);
-  w.total = w.least + (chunks ? align256(rows * 2 * 4) : 0);
+  w.total = w.least + (chunks ? align256(rows * 3 * 2 * 4) : 0);
   return w;
 }
 
