@@ -202,7 +202,7 @@ __device__ __forceinline__ void step(const hkv::KdaArgs& a) {
 // with 256, 304 with 1024; 16 sequences 12.1, 12.9, 18.1; 16 heads of d = 256 386
 // us with 1024, 666 with 512; d = 32 23 us with 64, 22 with 128, 29 with 256).
 #define HKV_KDA(name, T, d, threads)                                                        \
-  extern "C" __global__ __launch_bounds__(threads, (threads) == 512 ? 6 : 4) void name(     \
+  extern "C" __global__ __launch_bounds__(threads, 4) void name(                            \
       hkv::KdaArgs a) {                                                                     \
     step<T, d, threads>(a);                                                                 \
   }
