@@ -21,9 +21,8 @@
 // written once; only rows that must move do.  Measured: 16 sequences of up to
 // 8192 slots, 7 layers, bf16, half of them kept: 63 us, of which the selection
 // 20 and the moves 43 to 47; 1 sequence of 262144 slots, 24 layers, e4m3, 100000
-// kept: 491 us, the moves 359 at 4.8 TB/s (what a large copy reaches), the
-// passes over the slots 119; 4 sequences of up to 1500, 1 layer: 13 us, two
-// launches.
+// kept: 485 us, the moves 370 at 4.6 TB/s (a large copy reaches 4.8), the passes
+// over the slots 112; 4 sequences of up to 1500, 1 layer: 13 us, two launches.
 #include <hip/hip_runtime.h>
 
 #include "hkv.h"
@@ -323,7 +322,8 @@ __device__ __forceinline__ void copy_meta(const hkv::EvictArgs& a, uint32_t row,
 
 // One workgroup per (layer, sequence) of at most kItems x kThreads slots.
 // One launch instead of the chunked path's six: 8000 slots 22 us for 38, 112 rows
-// of 8192 23 for 42 (whole calls).  16 slots a thread, 48 registers of them, are
+// of 8192 23 for 42 (whole calls, when a chunked row of 20000 took 38; it takes 36
+// now).  16 slots a thread, 48 registers of them, are
 // as many as fit without spills; 4 a thread where they are enough (1500 slots: 13
 // us, 19 with 16).
 template <uint32_t kItems>
