@@ -15,8 +15,11 @@
 // with 16x16x32 matrix instructions and fp32 accumulators.  P is split into
 // two 16-bit terms (p = hi + lo, about 16 significant bits for bf16), because
 // one rounding of P to 16 bits would be as large as the rounding of the
-// output itself; see Attend for an e4m3 cache, whose rows are widened to fp16
-// as they are staged, which is exact.
+// output itself.  An e4m3 cache's rows are widened to the query's type as they
+// are staged, which is exact.  (For a bf16 query fp16 products with one term of
+// P took 108 us for 118 on the e4m3 case below, but P then has 11 bits, and a
+// query scaled by a power of two to fit fp16 loses what is 2^31 below its
+// largest value.)
 //
 // Bound: reading the cache once (row_bytes per token).  The waves have roles,
 // so that loads, both products and the softmax of different tiles overlap:
@@ -38,7 +41,7 @@
 // Measured: 64 ragged sequences of up to 14001 tokens, 32 heads, bf16 (648 MB)
 // 126 us, 5.1 TB/s; 1 of 10^6 tokens (1.15 GB) 190 us, 6.1 TB/s, what a large
 // read reaches; 24 of up to 40000, 64 heads, e4m3, a third of the blocks null
-// (229 MB, 55 GFLOP) 100 us, where the two products' LDS reads fill the rounds; 1
+// (229 MB, 55 GFLOP) 118 us; 1
 // of 333 tokens 12 us, two launches and one round.
 #include <hip/hip_runtime.h>
 
@@ -208,16 +211,10 @@ __device__ __forceinline__ float column_sum(float m) {
 constexpr uint32_t kCarriers = 8;
 constexpr uint32_t attend_threads(uint32_t heads) { return (heads / 16 + kCarriers) * 64; }
 
-// Q: the type of q and out.  The products' type T is Q's for a cache of Q's
-// type, and fp16 for an e4m3 cache: fp16 holds every e4m3 value exactly, and a
-// bf16 query too once its head is scaled by a power of two (see score), and P
-// rounded to fp16's 11 bits is finer than a bf16 output, so that only an fp16
-// output needs P's second term.
-template <class Q, bool kFp8, uint32_t kHeads>
+// T: the type of q, of out and of both products' operands (it holds every e4m3
+// value exactly).
+template <class T, bool kFp8, uint32_t kHeads>
 struct Attend {
-  using T = std::conditional_t<kFp8, Fp16, Q>;
-  static constexpr bool kScaleQ = !std::is_same_v<Q, T>;
-  static constexpr bool kLow = !kScaleQ;  // P has a second term
   // P in fp16 is taken 2^15 times as large (P <= 1), and O with it: beside a
   // weight of 1, fp16 would round those below 2^-14 ever more coarsely and lose
   // those below 2^-25, which a long sequence holds many of.
@@ -247,7 +244,7 @@ struct Attend {
   struct Lds {
     uint32_t tile[kTileSlots][2];  // which tile the i-th is, its groups' states
     uint8_t p_hi[2][kHeads * kPPitch];
-    uint8_t p_lo[2][kLow ? kHeads * kPPitch : 16];
+    uint8_t p_lo[2][kHeads * kPPitch];
     float alpha[2][kHeads];
     float m[kHeads], l[kHeads];
     uint32_t sums[kWaves];
@@ -454,13 +451,12 @@ struct Attend {
     for (uint32_t i = 0; i < kHeadTiles; ++i) {
 #pragma unroll
       for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], p[i], acc[i][j]);
-      if constexpr (kLow) p[i] = *(const HKV_LDS v4u*)(lo + i * 16 * kPPitch);
+      p[i] = *(const HKV_LDS v4u*)(lo + i * 16 * kPPitch);
     }
-    if constexpr (kLow)
 #pragma unroll
-      for (uint32_t i = 0; i < kHeadTiles; ++i)
+    for (uint32_t i = 0; i < kHeadTiles; ++i)
 #pragma unroll
-        for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], p[i], acc[i][j]);
+      for (uint32_t j = 0; j < kOTiles; ++j) acc[i][j] = T::mma(v[j], p[i], acc[i][j]);
   }
 
   template <bool kStream>
@@ -557,33 +553,6 @@ struct Attend {
         q[i] = v;
       }
     }
-    float scale = a.scale;
-    if constexpr (kScaleQ) {
-      // The head's largest finite value goes to [2^14, 2^15): values down to 2^-31 of
-      // it stay exact in fp16, and what smaller ones lose is below the fp32 sum's
-      // rounding.  The power of two is taken out of the logits again.
-      float big = 0.0f;
-#pragma unroll
-      for (uint32_t i = 0; i < kWidthSteps; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = fabsf(Q::low(q[i][e])), y = fabsf(Q::high(q[i][e]));
-          big = fmaxf(big, fmaxf(x < INFINITY ? x : 0.0f, y < INFINITY ? y : 0.0f));
-        }
-      big = column_max(big);
-      int ex = 0;
-      if (big > 0.0f) ex = 14 - ilogbf(big);
-      ex = ex > 120 ? 120 : ex < -120 ? -120 : ex;
-      const float up = __builtin_ldexpf(1.0f, ex);
-      scale *= __builtin_ldexpf(1.0f, -ex);
-#pragma unroll
-      for (uint32_t i = 0; i < kWidthSteps; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t u = opaque(q[i][e]);  // unpacked again, not kept unpacked
-          q[i][e] = T::pack(Q::low(u) * up, Q::high(u) * up);
-        }
-    }
     float m = -INFINITY, l = 0.0f;
     uint32_t buf = 0, half = 0, slot = 0;
     __builtin_amdgcn_s_setprio(2);  // the carriers wait for P, with more waves to fill the time
@@ -622,8 +591,8 @@ struct Attend {
       }
       __builtin_amdgcn_sched_group_barrier(0x008, 2 * kAhead, 0);
       __builtin_amdgcn_sched_barrier(0);
-      sc[0] *= scale;
-      sc[1] *= scale;
+      sc[0] *= a.scale;
+      sc[1] *= a.scale;
       if (st != 0 || t * kTile + kTile > len) {  // not all present
 #pragma unroll
         for (uint32_t r = 0; r < 2; ++r)
@@ -663,9 +632,8 @@ struct Attend {
         }
         const uint32_t h01 = T::pack(p[0], p[1]), h23 = T::pack(p[2], p[3]);
         *(HKV_LDS v2u*)(hi + r * 32) = v2u{h01, h23};
-        if constexpr (kLow)
-          *(HKV_LDS v2u*)(lo + r * 32) = v2u{T::pack(p[0] - T::low(h01), p[1] - T::high(h01)),
-                                            T::pack(p[2] - T::low(h23), p[3] - T::high(h23))};
+        *(HKV_LDS v2u*)(lo + r * 32) = v2u{T::pack(p[0] - T::low(h01), p[1] - T::high(h01)),
+                                          T::pack(p[2] - T::low(h23), p[3] - T::high(h23))};
       }
       if (quad == 0) lds.alpha[half][hl] = alpha;
       buf = buf + 1 == kBuffers ? 0 : buf + 1;
@@ -742,7 +710,7 @@ struct Attend {
             if (whole) {
               uint16_t* to = static_cast<uint16_t*>(a.out) + (int64_t)s * a.out_seq_stride +
                              (int64_t)h * a.out_head_stride + v;
-              *(HKV_GLOBAL v2u*)to = v2u{Q::pack(o[0], o[1]), Q::pack(o[2], o[3])};
+              *(HKV_GLOBAL v2u*)to = v2u{T::pack(o[0], o[1]), T::pack(o[2], o[3])};
             } else {
               *(HKV_GLOBAL v4f*)(a.part_o + (slot * kHeads + hl) * a.values + v) = o;
             }

@@ -62,7 +62,8 @@ struct AttendArgs {
 //   16 of up to 4800: 37.6, 34.0, 43.9 (11000)
 //   16 of up to 20000: 101.7, 75.8, 82.7 (42000); 40000: 182.8, 128.0, 125.5
 // An e4m3 cache has half the bytes to wait for in a round and turns earlier
-// (16 of up to 9600: 57.1, 46.2, 47.1 at 20000 units; 20000: 95.6, 67.7, 62.7).
+// (16 of up to 9600: 58.4, 45.5, 47.1 at 20000 units; 14000: 76.5, 56.7, 55.0 at
+// 29000; 20000: 102.7, 70.3, 65.5).
 inline constexpr uint32_t attend_head_tile(uint32_t n_heads, uint64_t units, bool fp8) {
   const uint32_t most = units <= 8192 ? 16u : units <= (fp8 ? 24576u : 49152u) ? 32u : 64u;
   const uint32_t need = n_heads <= 16 ? 16u : n_heads <= 32 ? 32u : 64u;
