@@ -1,6 +1,8 @@
 """MLA attention (hkv_mla_attend) where the logits are exact, so that what is
 left of the error is the probabilities' and the sums': a few non-zero entries
 of the queries and keys, small whole numbers times powers of two."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -29,6 +31,55 @@ def put(c, s, rows):
         if c.table[s, j] >= 0:
             k = min(n, rows.shape[0] - j * n)
             stored[int(c.table[s, j]), :k] = x[j * n:j * n + k]
+
+
+def live_tokens(c, s):
+    n = c.pool.n
+    return [t for t in range(c.lens[s]) if c.table[s, t // n] >= 0]
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("heads,columns", SIZES)
+def test_every_token_counts_once(dtype, cache, heads, columns):
+    """All logits of a head are the same, so that P = 1 and the sums are whole
+    numbers, which fp32 holds exactly: out is count / live tokens, off by two
+    fp32 roundings and the output's one; a token more or less changes a column
+    by a twentieth and lse by 1 / tokens."""
+    c = Case([9001, 0, 333, 2050, 1], heads=heads, dtype=dtype, cache=cache, seed=1, block_size=16,
+             columns=columns, holes=[(0, 0), (0, 7), (0, 100), (0, 101), (0, 562), (2, 20), (3, 1)],
+             weights=True)
+    c.scale = 1.0
+    c.weights.zero_()
+    z = torch.arange(heads) % 9 - 4.0
+    c.q.zero_()
+    c.q[:, :, 575] = z.to(c.dt).cuda()
+    for s, n in enumerate(c.lens):
+        rows = torch.zeros(n, 576)
+        rows[torch.arange(n), torch.arange(n) % 512] = 1.0
+        rows[:, 575] = 1.0
+        put(c, s, rows)
+    c.run()
+    h = half_step(c.dt)
+    for s in range(len(c.lens)):
+        live = live_tokens(c, s)
+        want = torch.zeros(512, dtype=torch.float64)
+        if live:
+            want += torch.bincount(torch.tensor(live) % 512, minlength=512).double() / len(live)
+        tol = want * (h + 3 * U) + torch.finfo(c.dt).tiny * h
+        out = c.out[s].cpu().double()
+        assert (out - want).abs().le(tol).all(), (s, ((out - want).abs() / tol.clamp(min=1e-30)).max())
+        # log2 to an ulp or two, its product with ln 2, the sum with the maximum
+        lse = torch.full((heads,), -math.inf, dtype=torch.float64)
+        off = 0.0
+        if live:
+            lse = z.double() + math.log(len(live))
+            off = 8 * U * (4 + math.log(len(live)))
+        got = c.lse[s].cpu().double()
+        assert torch.equal(got, lse) if not live else (got - lse).abs().le(off).all(), s
+        weights = torch.zeros(c.weights.shape[1], dtype=torch.float64)
+        weights[live] = heads / max(1, len(live))
+        tol = weights * (off + (heads + 16) * U)  # exp of (z - lse), sums over the heads
+        assert (c.weights[s].cpu().double() - weights).abs().le(tol).all(), s
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
