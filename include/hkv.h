@@ -421,7 +421,8 @@ typedef struct hkv_mla_attend_args {
   int32_t cache_dtype;       /* mla_bytes = 2: the same as dtype; 1: HKV_E4M3 */
   int32_t max_blocks;        /* entries of a block_table row, >= 1 */
   float scale;               /* softmax scale */
-  float cache_scale;         /* what a cached 1.0 stands for (1 unless e4m3) */
+  float cache_scale;         /* what a cached 1.0 stands for (1 unless e4m3); both and their
+                                product are finite */
   const void* q;             /* DEVICE [n_seqs][n_heads][mla_width] */
   int64_t q_seq_stride;      /* elements; multiples of 8, >= 0 */
   int64_t q_head_stride;

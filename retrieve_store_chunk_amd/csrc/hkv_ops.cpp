@@ -172,8 +172,9 @@ hkv_status attend(const hkv_layout* layout, const void* pool, const hkv_mla_atte
   if (a->cache_dtype != (bytes == 1 ? HKV_E4M3 : a->dtype))
     return set_error(HKV_E_ARG, bytes == 1 ? "a cache of 1-byte values must be HKV_E4M3"
                                            : "a cache of 2-byte values must be of q's type");
-  if (!std::isfinite(a->scale) || !std::isfinite(a->cache_scale))
-    return set_error(HKV_E_ARG, "scale and cache_scale must be finite");
+  if (!std::isfinite(a->scale) || !std::isfinite(a->cache_scale) ||
+      !std::isfinite(a->scale * a->cache_scale))
+    return set_error(HKV_E_ARG, "scale, cache_scale and their product must be finite");
   if (a->n_seqs == 0) return HKV_OK;
   if (!pool || !a->q || !a->block_table || !a->seq_lens || !a->out)
     return set_error(HKV_E_ARG, "pool, q, block_table, seq_lens and out must not be NULL");
