@@ -481,7 +481,11 @@ hkv_status hkv_mla_attend(const hkv_layout* layout, const void* pool,
  * starts with no weight); shorter sequences' are copied.  Entries past
  * seq_lens[s] are left as they were.  The arrays may be the inputs themselves;
  * where they are not, the same call can be repeated: it finds its inputs
- * unchanged and moves the same rows to the same places. */
+ * unchanged and moves the same rows to the same places.
+ * The blocks of a sequence that was cut no longer hold the tokens, or the
+ * order, that its prefix hashes and hkv_chunk_keys name.  Store them under keys
+ * of their own, never under the prefix's, and give an eviction no block that a
+ * prefix cache or another sequence still reads. */
 typedef struct hkv_mla_evict_args {
   int32_t n_layers;          /* 1..64 */
   const int32_t* layers;     /* HOST [n_layers] distinct MLA layers of one KV group (they
