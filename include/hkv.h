@@ -391,7 +391,13 @@ hkv_status hkv_move_chunks_noalloc(const hkv_layout* layout, int32_t op, void* p
  * launches on the caller's stream and may all be captured into a HIP graph.
  * A workspace may be shared by calls and by captured graphs that the stream
  * runs one after another, not by ones that may run at once; nothing in it
- * has to be kept or cleared between calls.
+ * has to be kept or cleared between calls.  No array of a call may be written
+ * by anything else while the call runs.
+ * A table holds at most 2^31 - 1 tokens (max_blocks x N; 2^28 for an eviction)
+ * and a layer's pages start on 16-byte boundaries (HKV_E_ALIGN for a packed
+ * layout where they do not; an eviction takes those too).  What the host plans
+ * and the workspaces follow max_blocks, since it does not know the lengths:
+ * tables not much wider than the sequences are faster.
  * ------------------------------------------------------------------------ */
 
 #define HKV_BF16 0
@@ -419,7 +425,8 @@ typedef struct hkv_mla_attend_args {
   int32_t value_width;       /* a multiple of 16, at most 512 and at most mla_width */
   int32_t dtype;             /* of q and out: HKV_BF16 or HKV_FP16 */
   int32_t cache_dtype;       /* mla_bytes = 2: the same as dtype; 1: HKV_E4M3 */
-  int32_t max_blocks;        /* entries of a block_table row, >= 1 */
+  int32_t max_blocks;        /* entries of a block_table row, >= 1; n_seqs x max_blocks x N at
+                                most 2^36 - 32 tokens */
   float scale;               /* softmax scale */
   float cache_scale;         /* what a cached 1.0 stands for (1 unless e4m3); both and their
                                 product are finite */
@@ -490,7 +497,7 @@ typedef struct hkv_mla_evict_args {
   int32_t n_layers;          /* 1..64 */
   const int32_t* layers;     /* HOST [n_layers] distinct MLA layers of one KV group (they
                                 share the block table) */
-  int32_t n_seqs;            /* 0..65535; 0 is a no-op */
+  int32_t n_seqs;            /* 0..65535, n_layers x n_seqs too; 0 is a no-op */
   int32_t max_blocks;        /* entries of a block_table row, >= 1 */
   int32_t budget;            /* tokens to keep, >= 1 */
   int32_t sinks;             /* >= 0, sinks + recent <= budget */
