@@ -17,7 +17,7 @@
 // one rounding of P to 16 bits would be as large as the rounding of the
 // output itself.  An e4m3 cache's rows are widened to the query's type as they
 // are staged, which is exact.  (For a bf16 query fp16 products with one term of
-// P took 108 us for 118 on the e4m3 case below, but P then has 11 bits, and a
+// P took 103 us for 113 on the e4m3 case below, but P then has 11 bits, and a
 // query scaled by a power of two to fit fp16 loses what is 2^31 below its
 // largest value.)
 //
@@ -29,20 +29,25 @@
 // and i + 3 are on their way in the carriers' registers.  (1 sequence of 10^6
 // tokens, 32 heads: 273 us when all waves loaded, scored and summed in turn, 220
 // with roles; a round is 1.5 us now.)  LDS rows are padded to an odd multiple
-// of 32 bytes: eight rows at the same column, and four rows of the transposing
-// loads, then fall into different banks.
+// of 32 bytes, so that eight rows at the same column, and four rows of the
+// transposing loads, start in different banks; counters still show a quarter of
+// the LDS's active cycles lost to conflicts, a third with e4m3 rows.
 //
 // The batch's tiles, all sequences after one another, are cut into equal
-// runs, one per worker (workgroup), whatever the lengths are: a million-token
-// sequence and a ragged batch both fill the card, and no length is needed on
-// the host.  A worker whose run covers part of a sequence leaves a partial
+// runs, one per worker (workgroup): a million-token sequence and a ragged batch
+// both fill the card, and no length is needed on the host.  Null blocks count in
+// the cut and are skipped only then, so that runs over dropped blocks end early
+// and the others carry the call (24 sequences of up to 40000, 64 heads, e4m3: 161
+// us whole, 93 with two blocks of every three null, 128 with the oldest two
+// thirds null).  A worker whose run covers part of a sequence leaves a partial
 // result (m, l, unnormalised O) that hkv_mla_attend_join adds up.
 //
 // Measured: 64 ragged sequences of up to 14001 tokens, 32 heads, bf16 (648 MB)
-// 126 us, 5.1 TB/s; 1 of 10^6 tokens (1.15 GB) 190 us, 6.1 TB/s, what a large
+// 126 us, 5.1 TB/s; 1 of 10^6 tokens (1.15 GB) 192 us, 6.0 TB/s, what a large
 // read reaches; 24 of up to 40000, 64 heads, e4m3, a third of the blocks null
-// (229 MB, 55 GFLOP) 118 us; 1
-// of 333 tokens 12 us, two launches and one round.
+// (229 MB, 55 GFLOP) 113 us, where no unit is full (LDS active 54% of the time,
+// matrix units 40%) and a round waits for its chain of widening, score, softmax
+// and sum; 1 of 333 tokens 12 us, two launches and one round.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -798,6 +803,8 @@ __device__ __forceinline__ void join(const hkv::AttendArgs& a) {
 
 }  // namespace
 
+// The 64-head kernels for 2-byte rows are 16 registers over what 12 waves leave
+// each (60 bytes of scratch a lane); no other spills any but scalar ones.
 #define HKV_ATTEND(name, T, fp8, heads)                                                     \
   extern "C" __global__ __launch_bounds__(attend_threads(heads)) void name(hkv::AttendArgs a) { \
     __shared__ __align__(16) Attend<T, fp8, heads>::Lds lds;                                \

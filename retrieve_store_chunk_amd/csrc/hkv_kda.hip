@@ -198,9 +198,11 @@ __device__ __forceinline__ void step(const hkv::KdaArgs& a) {
 
 // Threads by head dim, so that a thread holds up to 16 rows of 4 columns and its
 // state stays in registers (256 sequences, 32 heads: d = 64 67 us with 256
-// threads, 70 with 512, 625 with 128, which spill; d = 128 203 us with 512, 202
-// with 256, 304 with 1024; 16 sequences 12.1, 12.9, 18.1; 16 heads of d = 256 386
-// us with 1024, 666 with 512; d = 32 23 us with 64, 22 with 128, 29 with 256).
+// threads, 70 with 512, 625 with 128, which spill; d = 128 210 us with 512, 212
+// with 256, 311 with 1024, with a fifth of them without a state 183, 187, 259; 61
+// sequences 54, 51, 75; 16 sequences 13.7, 14.6, 19.5; 4 7.5, 8.2, 8.8; 16 heads of
+// d = 256 386 us with 1024, 666 with 512; d = 32 23 us with 64, 22 with 128, 29
+// with 256).
 #define HKV_KDA(name, T, d, threads)                                                        \
   extern "C" __global__ __launch_bounds__(threads, 4) void name(                            \
       hkv::KdaArgs a) {                                                                     \

@@ -105,9 +105,10 @@ hkv_status check_table(const hkv::Plan& p, int32_t n_seqs, int32_t max_blocks,
 }
 
 // ---------------------------------------------------------------- attention
-// One workgroup (9 to 12 waves, about 120 KB of LDS) fits a CU.  The head tiles
+// One workgroup (9 to 12 waves, 116 to 132 KB of LDS) fits a CU.  The head tiles
 // of a batch run at once, those of one run of tokens on the same XCD (a
-// multiple of 8 apart), so that only the first reads from HBM.
+// multiple of 8 apart, but in calls of fewer tiles than workers), so that only
+// the first reads from HBM.
 hkv_status plan_attend(const hkv_layout* layout, const hkv_mla_attend_args* a, bool weights,
                        hkv::AttendArgs* k, hkv::AttendWorkspace* ws) {
   const hkv::Plan& p = layout->plan;

@@ -18,9 +18,13 @@ constexpr uint32_t kAttendMaxWorkers = 256; // one workgroup per CU
 // Rows of a call whose tables can hold more than the last-level cache are read
 // past the caches (nontemporal): they cannot be there from the call before, and
 // should not evict what is (1 sequence of 10^6 tokens, 32 heads: 191 us, 213
-// without; 64 of up to 14001: 126, 140).  Smaller calls keep them, where a layer
-// that is read again finds them (16 of up to 9000, 32 heads: 36 us, 39 past the
-// caches; 16 of up to 2400, 64 heads: 27, 29.5).
+// without; 64 of up to 14001: 128, 140; 64 of up to 4000, 418 MB of tables: 53,
+// 56).  Smaller calls are no slower, or faster, through the caches, with seven
+// layers read in turn as in a decode loop (16 of up to 9000, 32 heads: 38.7 us,
+// 38.2 past the caches; 16 of up to 2400, 64 heads: 27.6, 29.7; 4 of up to 9000,
+// 32 heads: 23.6, 25.2; one layer again and again gains 3 us more).  With two
+// head tiles both ways meet at the limit (16 of up to 20000, 64 heads, 383 MB:
+// 73.9 us, 73.5; 64 of up to 4000: 70.5, 72.2).
 constexpr uint64_t kAttendStreamBytes = uint64_t(256) << 20;
 
 // One call's geometry as the host plans it and the kernels follow it.
