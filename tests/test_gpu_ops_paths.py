@@ -1,12 +1,16 @@
 """Paths of the decode-step operators that only large calls take: weights in
 several pieces, and the eviction of rows that many workgroups share, captured,
-repeated, in place and on two streams."""
+repeated, in place and on two streams; and calls from several threads."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
+import retrieve_store_chunk_amd as hkv
 from tests import test_gpu_attend as attend
 from tests import test_gpu_evict as evict
+from tests import test_gpu_kda as kda
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +116,70 @@ def test_a_row_of_more_chunks_than_threads():
     ws = c.workspace()
     c.enqueue(ws)
     c.compare((after, w_out, pos_out, np.array([budget], np.int32)))
+
+
+def test_calls_from_several_threads_on_one_layout():
+    """Each thread has its own stream, buffers and workspace; the layout and the
+    pool are shared (the KDA steps write blocks of their own)."""
+    shared = attend.Case([900, 33, 0, 2100], heads=32, seed=10, block_size=32, weights=True)
+    cases = []
+    for i in range(4):
+        c = attend.Case([900, 33, 0, 2100], heads=32, seed=10, block_size=32, weights=True)
+        c.pool = shared.pool
+        c.q = (c.q.float() * (1 + i)).to(c.dt)
+        cases.append(c)
+    steps = [kda.Case([2 * i, -1], [2 * i, 2 * i + 1], heads=4, d=64, seed=11, blocks=8) for i in range(4)]
+    for k in steps[1:]:
+        k.pool = steps[0].pool
+    want = [k.expect() for k in steps]
+    evicts = [evict.Case([700, 90], 200, seed=20 + i) for i in range(4)]
+    want_evict = [e.expect() for e in evicts]
+    ws = [(c.workspace(), e.workspace(), torch.cuda.Stream()) for c, e in zip(cases, evicts)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            wa, we, s = ws[i]
+            for _ in range(20):
+                cases[i].pool.layout.mla_attend(cases[i].pool.ptr, cases[i].args(), wa.data_ptr(),
+                                                wa.numel(), s.cuda_stream)
+            steps[i].enqueue(s.cuda_stream)
+            evicts[i].enqueue(we, s.cuda_stream)
+        except Exception as e:  # noqa: BLE001 (reported by the test's thread)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for c in cases:
+        grown = c.weights - c.weights_in
+        c.weights = None
+        c.check()
+        for s, n in enumerate(c.lens):  # 20 times a sum of 1 a head
+            assert grown[s].double().sum().item() == pytest.approx(20 * 32 * (n > 0), rel=1e-4)
+    before = want[0][1]
+    for k, (res, _) in zip(steps, want):
+        for s in range(2):
+            assert (k.out[s].cpu().double() - res["out"][s]).abs().le(res["out_tol"][s]).all()
+        for b, new in res["rec"].items():
+            assert (k.rec()[b].cpu().double() - new).abs().le(res["tol"][b]).all()
+            assert torch.equal(k.conv()[b].cpu(), res["conv"][b])
+    assert not torch.equal(before, steps[0].pool.bytes)
+    for e, x in zip(evicts, want_evict):
+        e.compare(x)
+
+
+def test_the_kda_step_of_a_layout_with_the_codec():
+    """The codec is the objects' form: the pool's pages are the same."""
+    a, b = (kda.Case([0, -1, 2], [3, 1, 2], heads=2, d=64, seed=12) for _ in range(2))
+    b.pool.layout = hkv.Layout(dict(b.pool.desc, kda_codec=1))
+    assert b.pool.layout.info["kda_codec"] == 1 and b.pool.layout.layers[b.layer]["stride"] == \
+        a.pool.layers[a.layer]["stride"]
+    a.run()
+    b.run()
+    assert torch.equal(a.out, b.out) and torch.equal(a.pool.bytes, b.pool.bytes)
