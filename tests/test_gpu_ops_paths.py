@@ -183,3 +183,13 @@ def test_the_kda_step_of_a_layout_with_the_codec():
     a.run()
     b.run()
     assert torch.equal(a.out, b.out) and torch.equal(a.pool.bytes, b.pool.bytes)
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("block_size", [16, 48, 768])
+def test_sequences_whose_older_blocks_are_all_null(dtype, cache, block_size):
+    """Most workers' runs then hold nothing, and a few hold everything."""
+    lens = [9001, 4000, 31, 6000]
+    holes = [(s, j) for s, n in enumerate(lens) for j in range(2 * -(-n // block_size) // 3)]
+    attend.Case(lens, heads=32, dtype=dtype, cache=cache, seed=13, block_size=block_size,
+                holes=holes, weights=True).run().check()
