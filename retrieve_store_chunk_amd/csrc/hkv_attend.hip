@@ -44,10 +44,11 @@
 //
 // Measured: 64 ragged sequences of up to 14001 tokens, 32 heads, bf16 (648 MB)
 // 126 us, 5.1 TB/s; 1 of 10^6 tokens (1.15 GB) 192 us, 6.0 TB/s, what a torch
-// sum of 4 GiB reaches (the best reading kernel here 7.4); 24 of up to 40000, 64 heads, e4m3, a third of the blocks null
-// (229 MB, 55 GFLOP) 113 us, where no unit is full (LDS active 54% of the time,
-// matrix units 40%) and a round waits for its chain of widening, score, softmax
-// and sum; 1 of 333 tokens 12 us, two launches and one round.
+// sum of 4 GiB reaches (the best reading kernel here 7.4); 24 of up to 40000, 64
+// heads, e4m3, a third of the blocks null (229 MB, 55 GFLOP) 113 us, where no unit
+// is full (LDS active 54% of the time, matrix units 40%) and a round waits for its
+// chain of widening, score, softmax and sum; 1 of 333 tokens 12 us, two launches
+// and one round.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
