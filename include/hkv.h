@@ -582,6 +582,146 @@ hkv_status hkv_kda_step(const hkv_layout* layout, void* pool, const hkv_kda_step
                         void* stream);
 
 /* ------------------------------------------------------------------------
+ * New tokens into the pool: what fills the pages that the decode step reads.
+ * A prompt (or what is left of it after a retrieve) runs through
+ * hkv_mla_append and hkv_kda_prefill layer by layer; the pages that they leave
+ * are what hkv_mla_attend and hkv_kda_step go on from and hkv_store_chunks
+ * stores.  The rules of the decode step hold here too: tables, ids and lengths
+ * are DEVICE arrays, everything else is checked on the host, the calls only
+ * enqueue kernel launches and may be captured.
+ *
+ * The tokens of a call's sequences lie one after another in its rows:
+ * sequence s has rows seq_starts[s] .. seq_starts[s+1] - 1.  The starts must
+ * not decrease.  Rows before the first sequence and behind the last (a padded
+ * batch) are not written, and what they hold does not matter.
+ * ------------------------------------------------------------------------ */
+
+/* Appends tokens to one layer's paged latent cache, and rotates their queries.
+ * Of a token's new row c (mla_width values, an MLA layer's joint projection of
+ * latent and rotary part):
+ *   columns w < latent_width:  c_w / sqrt(mean_{w < latent_width} c_w^2 + eps)
+ *                              x norm_weight_w   (norm_weight NULL: c_w itself)
+ *   the last rotary_dim columns, by pairs (a, b):  (a cos - b sin, a sin + b cos)
+ *   columns between them: c_w itself
+ * in fp32, each divided by cache_scale and rounded once to the cache's type.
+ * Pair j is columns (2j, 2j+1) of the rotary part, or (j, j + rotary_dim/2)
+ * with rotary_halves; its cos and sin are cos_sin[position][j] and
+ * cos_sin[position][rotary_dim/2 + j].  Token i of sequence s, counted from 0,
+ * goes to slot t = seq_lens[s] - (its new tokens) + i, i.e. row t % N of block
+ * block_table[s][t / N], where hkv_mla_attend reads it; its position is its own
+ * (after an eviction slots and positions differ).  A token whose block is
+ * HKV_NULL_BLOCK is not stored.
+ * Queries: the rotary parts q_in go to q_out (fp32, rounded once to dtype),
+ * which may be q_in itself or the last columns of hkv_mla_attend's q. */
+typedef struct hkv_mla_append_args {
+  int32_t layer;             /* an MLA layer */
+  int32_t n_seqs;            /* 0..65535; 0 is a no-op */
+  int32_t n_tokens;          /* rows of kv, 0..2^20 */
+  int32_t n_heads;           /* 0..128 query heads; 0: no queries */
+  int32_t dtype;             /* of kv, norm_weight and the queries: HKV_BF16 or HKV_FP16 */
+  int32_t cache_dtype;       /* mla_bytes = 2: the same as dtype; 1: HKV_E4M3 */
+  int32_t latent_width;      /* a multiple of 8, 0..mla_width - rotary_dim */
+  int32_t rotary_dim;        /* a multiple of 16, 0..mla_width; 0: no rotation */
+  int32_t rotary_halves;     /* 0 or 1: which columns are pairs (above) */
+  int32_t n_positions;       /* rows of cos_sin */
+  int32_t max_blocks;        /* entries of a block_table row, >= 1 */
+  float eps;                 /* >= 0 */
+  float cache_scale;         /* what a cached 1.0 stands for (1 unless e4m3); finite, > 0 */
+  const void* kv;            /* DEVICE [n_tokens][mla_width] */
+  int64_t kv_stride;         /* elements, a multiple of 8, >= 0 */
+  const void* norm_weight;   /* DEVICE [latent_width], or NULL */
+  const float* cos_sin;      /* DEVICE [n_positions][rotary_dim] */
+  const int32_t* positions;  /* DEVICE [n_tokens] (may be NULL without rotation) */
+  const int32_t* seq_starts; /* DEVICE [n_seqs + 1], or NULL: one token per sequence
+                                (n_tokens = n_seqs) */
+  const int32_t* seq_lens;   /* DEVICE [n_seqs] tokens in the cache, the new ones counted */
+  const int32_t* block_table; /* DEVICE [n_seqs][max_blocks], as for hkv_mla_attend; only the
+                                entries of the new tokens are read */
+  int64_t table_stride;      /* elements, >= 0 */
+  const void* q_in;          /* DEVICE [n_tokens][n_heads][rotary_dim] */
+  int64_t q_in_token_stride; /* elements, multiples of 8, >= 0, as the next three */
+  int64_t q_in_head_stride;
+  void* q_out;               /* DEVICE, same shape; == q_in with its strides, or disjoint */
+  int64_t q_out_token_stride;
+  int64_t q_out_head_stride;
+} hkv_mla_append_args;
+
+/* Enqueues the append as one kernel, without a workspace (see above).  pool:
+ * DEVICE as for hkv_store_chunks.  Needs mla_width a multiple of 16 of at most
+ * 1024 and mla_bytes 1 or 2.  pool, kv, norm_weight, cos_sin, q_in and q_out are
+ * 16-byte aligned, the other arrays by their element.  In an e4m3 cache a value
+ * beyond +-448 x cache_scale becomes +-448, NaN stays NaN.
+ * A token whose sequence's length is outside [its new tokens, max_blocks x N],
+ * or whose block id is not in [0, num_blocks), is not stored; one whose position
+ * is outside [0, n_positions) gets NaN in its rotary columns and queries.  No
+ * slot of the pool may be named by two tokens of a call: it would hold parts of
+ * either.
+ * Errors: HKV_E_ARG, HKV_E_ALIAS, HKV_E_ALIGN, HKV_E_HIP. */
+hkv_status hkv_mla_append(const hkv_layout* layout, void* pool, const hkv_mla_append_args* args,
+                          void* stream);
+
+/* hkv_kda_step for many tokens of each sequence: the same conv, norms and
+ * recurrence (above), token after token, from the state page of block
+ * src_blocks[s], which covers the sequence's first positions[s] tokens, to the
+ * pages of the sequence's own blocks: the state after a token of position p goes
+ * to block block_table[s][p / N] if p is the last position of its block
+ * ((p + 1) % N = 0, a snapshot of the block boundary as a store wants it: vLLM
+ * hybrid KV-cache blog, section 7, mamba_cache_mode=align) or the sequence's
+ * last new token.  A source of HKV_NULL_BLOCK is a state of zeros; an entry of
+ * HKV_NULL_BLOCK is not written (snapshots that are not kept).  The source may
+ * be one of the sequence's own blocks.  A sequence without new tokens reads and
+ * writes nothing.
+ * Sums, norms, decays and states are fp32.  Long runs are computed in chunks of
+ * up to 64 tokens whose products take each operand as two fp16 terms (22 bits),
+ * so a state differs from the token-by-token one by about 1e-6 of its column's
+ * size; there, a NaN or an infinity may also reach outputs of its head up to 63
+ * rows before it. */
+typedef struct hkv_kda_prefill_args {
+  int32_t layer;             /* a KDA layer */
+  int32_t n_seqs;            /* 0..4096; 0 is a no-op */
+  int32_t n_tokens;          /* rows of x and out, 0..2^20 */
+  int32_t max_seq_tokens;    /* no sequence has more new tokens; plans the call */
+  int32_t max_blocks;        /* entries of a block_table row, >= 1 */
+  int32_t dtype;             /* as for hkv_kda_step */
+  float scale;               /* of q, e.g. d^-1/2 */
+  float eps;                 /* >= 0 */
+  const void* x;             /* DEVICE [n_tokens][conv_dim] */
+  int64_t x_stride;          /* elements, >= 0 */
+  const void* conv_weight;   /* DEVICE [conv_dim][conv_kernel] */
+  const float* log_decay;    /* DEVICE [n_tokens][heads x d] natural logs, <= 0 (a positive one
+                                counts as 0); -infinity forgets */
+  int64_t decay_stride;      /* elements, >= 0 */
+  const float* beta;         /* DEVICE [n_tokens][heads], in [0, 2] */
+  int64_t beta_stride;       /* elements, >= 0 */
+  const int32_t* seq_starts; /* DEVICE [n_seqs + 1] */
+  const int32_t* positions;  /* DEVICE [n_seqs] position of the sequence's first new token */
+  const int32_t* src_blocks; /* DEVICE [n_seqs] */
+  const int32_t* block_table; /* DEVICE [n_seqs][max_blocks] block ids of the layer's KV group;
+                                only the entries of the new tokens are read */
+  int64_t table_stride;      /* elements, >= 0 */
+  void* out;                 /* DEVICE [n_tokens][heads x d] */
+  int64_t out_stride;        /* elements, a multiple of 4, >= heads x d */
+} hkv_kda_prefill_args;
+
+/* Device workspace bytes of a call with these shapes (n_seqs, n_tokens,
+ * max_seq_tokens, dtype; pointers are not read).  Errors: HKV_E_ARG. */
+hkv_status hkv_kda_prefill_workspace(const hkv_layout* layout, const hkv_kda_prefill_args* args,
+                                     size_t* bytes);
+
+/* Enqueues the prefill (see above).  Needs of the layout what hkv_kda_step
+ * needs; pool, out and workspace are 16-byte aligned, the other arrays by their
+ * element.  The result of a call depends on its inputs alone (no atomics).
+ * A sequence whose position is negative, that has more tokens than
+ * max_seq_tokens or than its table's max_blocks x N - positions[s], that names
+ * a block id which is neither HKV_NULL_BLOCK nor in [0, num_blocks), or a block
+ * to be written that its table names twice or another sequence of the call
+ * reads or writes, gets NaN in its rows of out and writes no page.  One whose
+ * starts decrease or leave [0, n_tokens] is left as it was.
+ * Errors: HKV_E_ARG, HKV_E_ALIAS, HKV_E_ALIGN, HKV_E_WORKSPACE, HKV_E_HIP. */
+hkv_status hkv_kda_prefill(const hkv_layout* layout, void* pool, const hkv_kda_prefill_args* args,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Object identity.  Cached pages are byte-opaque, so an entry must never be
  * read back by an engine whose object format differs: other attention
  * backends or kernel block sizes ("Kimi-Linear", "Kimi K3" recipes and

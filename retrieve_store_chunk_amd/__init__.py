@@ -122,6 +122,28 @@ class hkv_kda_step_args(ctypes.Structure):
                 ("dst_blocks", vp), ("out", vp), ("out_stride", i64)]
 
 
+class hkv_mla_append_args(ctypes.Structure):
+    """Pointers are integer device addresses (0 = NULL)."""
+    _fields_ = [("layer", i32), ("n_seqs", i32), ("n_tokens", i32), ("n_heads", i32),
+                ("dtype", i32), ("cache_dtype", i32), ("latent_width", i32), ("rotary_dim", i32),
+                ("rotary_halves", i32), ("n_positions", i32), ("max_blocks", i32), ("eps", f32),
+                ("cache_scale", f32), ("kv", vp), ("kv_stride", i64), ("norm_weight", vp),
+                ("cos_sin", vp), ("positions", vp), ("seq_starts", vp), ("seq_lens", vp),
+                ("block_table", vp), ("table_stride", i64), ("q_in", vp),
+                ("q_in_token_stride", i64), ("q_in_head_stride", i64), ("q_out", vp),
+                ("q_out_token_stride", i64), ("q_out_head_stride", i64)]
+
+
+class hkv_kda_prefill_args(ctypes.Structure):
+    """Pointers are integer device addresses (0 = NULL)."""
+    _fields_ = [("layer", i32), ("n_seqs", i32), ("n_tokens", i32), ("max_seq_tokens", i32),
+                ("max_blocks", i32), ("dtype", i32), ("scale", f32), ("eps", f32), ("x", vp),
+                ("x_stride", i64), ("conv_weight", vp), ("log_decay", vp), ("decay_stride", i64),
+                ("beta", vp), ("beta_stride", i64), ("seq_starts", vp), ("positions", vp),
+                ("src_blocks", vp), ("block_table", vp), ("table_stride", i64), ("out", vp),
+                ("out_stride", i64)]
+
+
 def one_hip_runtime() -> None:
     """A process must hold one HIP runtime.  PyTorch-ROCm ships its own copy,
     which its libraries load by file name; if libhkv.so were loaded first it
@@ -181,6 +203,14 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
                                 ctypes.c_size_t, vp]
     L.hkv_kda_step.restype = i32
     L.hkv_kda_step.argtypes = [vp, vp, ctypes.POINTER(hkv_kda_step_args), vp]
+    L.hkv_mla_append.restype = i32
+    L.hkv_mla_append.argtypes = [vp, vp, ctypes.POINTER(hkv_mla_append_args), vp]
+    L.hkv_kda_prefill_workspace.restype = i32
+    L.hkv_kda_prefill_workspace.argtypes = [vp, ctypes.POINTER(hkv_kda_prefill_args),
+                                            ctypes.POINTER(ctypes.c_size_t)]
+    L.hkv_kda_prefill.restype = i32
+    L.hkv_kda_prefill.argtypes = [vp, vp, ctypes.POINTER(hkv_kda_prefill_args), vp,
+                                  ctypes.c_size_t, vp]
     L.hkv_last_error.restype = ctypes.c_char_p
     L.hkv_last_error.argtypes = []
     return L
@@ -388,6 +418,23 @@ def hkv_kda_step(handle: int, pool_ptr: int, args: hkv_kda_step_args, stream: in
     _check(lib.hkv_kda_step(handle, pool_ptr, ctypes.byref(args), stream), "hkv_kda_step")
 
 
+def hkv_mla_append(handle: int, pool_ptr: int, args: hkv_mla_append_args, stream: int = 0) -> None:
+    _check(lib.hkv_mla_append(handle, pool_ptr, ctypes.byref(args), stream), "hkv_mla_append")
+
+
+def hkv_kda_prefill_workspace(handle: int, args: hkv_kda_prefill_args) -> int:
+    out = ctypes.c_size_t()
+    _check(lib.hkv_kda_prefill_workspace(handle, ctypes.byref(args), ctypes.byref(out)),
+           "hkv_kda_prefill_workspace")
+    return out.value
+
+
+def hkv_kda_prefill(handle: int, pool_ptr: int, args: hkv_kda_prefill_args, workspace_ptr: int,
+                    ws_bytes: int, stream: int = 0) -> None:
+    _check(lib.hkv_kda_prefill(handle, pool_ptr, ctypes.byref(args), workspace_ptr, ws_bytes,
+                               stream), "hkv_kda_prefill")
+
+
 def status_of(fn, *args) -> int:
     """Calls one of the wrappers above and returns its status instead of
     raising (for tests of error paths)."""
@@ -463,3 +510,12 @@ class Layout:
 
     def kda_step(self, pool_ptr, args: hkv_kda_step_args, stream=0):
         hkv_kda_step(self.handle, pool_ptr, args, stream)
+
+    def mla_append(self, pool_ptr, args: hkv_mla_append_args, stream=0):
+        hkv_mla_append(self.handle, pool_ptr, args, stream)
+
+    def kda_prefill_workspace(self, args: hkv_kda_prefill_args) -> int:
+        return hkv_kda_prefill_workspace(self.handle, args)
+
+    def kda_prefill(self, pool_ptr, args: hkv_kda_prefill_args, ws_ptr, ws_bytes, stream=0):
+        hkv_kda_prefill(self.handle, pool_ptr, args, ws_ptr, ws_bytes, stream)

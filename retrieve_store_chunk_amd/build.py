@@ -7,8 +7,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libhkv.so")
 
-SOURCES = ["hkv_plan.cpp", "hkv_groups.cpp", "hkv_keys.cpp", "hkv_api.cpp", "hkv_ops.cpp", "hkv_copy.hip",
-           "hkv_attend.hip", "hkv_evict.hip", "hkv_kda.hip"]
+SOURCES = ["hkv_plan.cpp", "hkv_groups.cpp", "hkv_keys.cpp", "hkv_api.cpp", "hkv_ops.cpp", "hkv_prompt.cpp",
+           "hkv_copy.hip", "hkv_attend.hip", "hkv_evict.hip", "hkv_kda.hip", "hkv_append.hip",
+           "hkv_prefill.hip"]
 # The INT8 codec takes integer decisions in fp32 on both the GPU and the CPU
 # oracle: keep IEEE division and fp32 denormals explicit.
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-Wall",

@@ -195,4 +195,73 @@ struct KdaArgs {
 
 int launch_kda(const KdaArgs& a, int32_t dtype, void* stream);
 
+// ---------------------------------------------------------------- append
+constexpr uint32_t kAppendMaxWidth = 1024;          // a wave holds a row: 16 values a lane
+constexpr int32_t kPromptMaxTokens = 1 << 20;       // rows of a call
+
+struct AppendArgs {
+  uint8_t* pages;        // the layer's page of block 0
+  uint64_t stride;       // bytes between block ids
+  const void* kv;        // [n_tokens][width]
+  int64_t kv_stride;     // elements, as the other strides
+  const void* norm;      // [latent] or nullptr
+  const float* cos_sin;  // [n_positions][rotary]
+  const int32_t* positions;  // [n_tokens]
+  const int32_t* starts;     // [n_seqs + 1] or nullptr
+  const int32_t* lens;       // [n_seqs]
+  const int32_t* table;      // [n_seqs][max_blocks]
+  int64_t table_stride;
+  const void* q_in;          // [n_tokens][n_heads][rotary]
+  int64_t q_in_token, q_in_head;
+  void* q_out;
+  int64_t q_out_token, q_out_head;
+  float eps, cache_scale;
+  uint32_t num_blocks, block_tokens, max_blocks, n_seqs, n_tokens, n_positions;
+  uint32_t n_heads, width, latent, rotary, halves, cache_bytes;
+};
+
+int launch_append(const AppendArgs& a, int32_t dtype, void* stream);
+
+// ---------------------------------------------------------------- KDA prefill
+struct PrefillArgs {
+  uint8_t* pages;        // the layer's page of block 0
+  uint64_t stride;       // bytes between block ids
+  uint64_t conv_bytes;   // the recurrent state's offset in a page
+  const void* x;         // [n_tokens][conv_dim]
+  int64_t x_stride;      // elements, as the other strides
+  const void* conv_weight;  // [conv_dim][taps]
+  const float* log_decay;   // [n_tokens][heads * d]
+  int64_t decay_stride;
+  const float* beta;        // [n_tokens][heads]
+  int64_t beta_stride;
+  const int32_t* starts;    // [n_seqs + 1]
+  const int32_t* positions; // [n_seqs]
+  const int32_t* src;       // [n_seqs]
+  const int32_t* table;     // [n_seqs][max_blocks]
+  int64_t table_stride;
+  void* out;                // [n_tokens][heads * d]
+  int64_t out_stride;
+  float scale, eps;
+  uint32_t num_blocks, block_tokens, max_blocks, n_seqs, n_tokens, max_seq_tokens;
+  uint32_t heads, head_dim, taps;
+  // workspace
+  int32_t* status;          // [n_seqs]: kPrefill* below
+};
+
+// What becomes of a sequence.
+constexpr int32_t kPrefillRuns = 0;
+constexpr int32_t kPrefillRefused = 1;  // NaN in its rows, no page
+constexpr int32_t kPrefillNoRows = 2;   // nothing to do, or its rows are not known
+
+struct PrefillWorkspace {
+  uint64_t status, total;
+};
+inline PrefillWorkspace prefill_workspace(uint64_t n_seqs) {
+  PrefillWorkspace w{};
+  w.total = w.status + align256(n_seqs * 4);
+  return w;
+}
+
+int launch_prefill(const PrefillArgs& a, int32_t dtype, void* stream);
+
 }  // namespace hkv
