@@ -223,6 +223,18 @@ struct AppendArgs {
 int launch_append(const AppendArgs& a, int32_t dtype, void* stream);
 
 // ---------------------------------------------------------------- KDA prefill
+constexpr uint32_t kPrefillChunk = 64;       // tokens
+constexpr uint32_t kPrefillChunkDim = 128;   // the head dim that is computed in chunks
+constexpr uint32_t kPrefillRecord = 3 * 32768 + 12288 + 32768 + 512;  // bytes of a chunk and head
+
+// Runs of up to so many tokens go token by token (a call of one sequence has no
+// launch for them where it has chunks).
+constexpr uint32_t kPrefillShort = 8;
+
+struct PrefillChunk {
+  int32_t seq, row, len, off;  // its first token: row of the call, token of the sequence
+};
+
 struct PrefillArgs {
   uint8_t* pages;        // the layer's page of block 0
   uint64_t stride;       // bytes between block ids
@@ -244,8 +256,14 @@ struct PrefillArgs {
   float scale, eps;
   uint32_t num_blocks, block_tokens, max_blocks, n_seqs, n_tokens, max_seq_tokens;
   uint32_t heads, head_dim, taps;
+  uint32_t chunked;         // sequences of more than short_tokens are computed in chunks
+  uint32_t short_tokens;
+  uint32_t max_chunks;
   // workspace
   int32_t* status;          // [n_seqs]: kPrefill* below
+  int32_t* first_chunk;     // [2][n_seqs], [1]: each sequence's first, how many; all of them
+  PrefillChunk* chunks;     // [max_chunks]
+  uint8_t* records;         // [max_chunks][heads][kPrefillRecord]
 };
 
 // What becomes of a sequence.
@@ -254,11 +272,14 @@ constexpr int32_t kPrefillRefused = 1;  // NaN in its rows, no page
 constexpr int32_t kPrefillNoRows = 2;   // nothing to do, or its rows are not known
 
 struct PrefillWorkspace {
-  uint64_t status, total;
+  uint64_t status, first_chunk, chunks, records, total;
 };
-inline PrefillWorkspace prefill_workspace(uint64_t n_seqs) {
+inline PrefillWorkspace prefill_workspace(uint64_t n_seqs, uint64_t max_chunks, uint64_t heads) {
   PrefillWorkspace w{};
-  w.total = w.status + align256(n_seqs * 4);
+  w.first_chunk = w.status + align256(n_seqs * 4);
+  w.chunks = w.first_chunk + (max_chunks ? align256((2 * n_seqs + 1) * 4) : 0);
+  w.records = w.chunks + align256(max_chunks * sizeof(PrefillChunk));
+  w.total = w.records + max_chunks * heads * kPrefillRecord;
   return w;
 }
 

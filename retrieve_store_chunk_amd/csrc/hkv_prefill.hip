@@ -35,6 +35,7 @@ struct Fp32 {
 
 // ---------------------------------------------------------------- plan
 constexpr uint32_t kPlanThreads = 256;
+constexpr uint32_t kC = hkv::kPrefillChunk;
 
 // A sequence's rows of the call and the blocks that its tokens lie in.  `known`:
 // the rows lie in [0, n_tokens); `blocks`: its positions lie in its table.
@@ -61,15 +62,29 @@ __device__ __forceinline__ bool outside(int32_t id, uint32_t num_blocks) {
   return id != HKV_NULL_BLOCK && (id < 0 || (uint32_t)id >= num_blocks);
 }
 
+// Tokens up to the first block's end.
+__device__ __forceinline__ uint32_t chunk_lead(const hkv::PrefillArgs& a, const Span& p) {
+  if (!p.blocks) return 0;
+  return min((uint32_t)p.tokens,
+             a.block_tokens - (uint32_t)p.position % a.block_tokens);
+}
+__device__ __forceinline__ uint32_t chunks_of(const hkv::PrefillArgs& a, const Span& p) {
+  if (!p.blocks || p.tokens <= (int32_t)a.short_tokens || p.tokens > (int32_t)a.max_seq_tokens)
+    return 0;
+  const uint32_t lead = chunk_lead(a, p), rest = (uint32_t)p.tokens - lead;
+  return (lead + kC - 1) / kC + rest / a.block_tokens * ((a.block_tokens + kC - 1) / kC) +
+         (rest % a.block_tokens + kC - 1) / kC;
+}
+
 // What becomes of each sequence (hkv.h), one workgroup each.  Blocks are compared
 // with those of all sequences: entries are few (a block holds hundreds of tokens).
 __device__ __forceinline__ void plan(const hkv::PrefillArgs& a) {
   __shared__ int32_t most;
-  __shared__ uint32_t refused;
+  __shared__ uint32_t refused, before;
   const uint32_t s = blockIdx.x, t = threadIdx.x;
   if (t == 0) {
     most = INT32_MIN;
-    refused = 0;
+    refused = before = 0;
   }
   __syncthreads();
   const Span me = span_of(a, s);
@@ -101,36 +116,74 @@ __device__ __forceinline__ void plan(const hkv::PrefillArgs& a) {
     }
   }
   if (bad) atomicOr(&refused, 1u);
+  uint32_t mine = 0;  // chunks of the sequences before
+  if (a.chunked)
+    for (uint32_t r = t; r < s; r += kPlanThreads) mine += chunks_of(a, span_of(a, r));
+  if (mine) atomicAdd(&before, mine);
   __syncthreads();
+  const bool rows = me.known && me.tokens > 0 && most <= me.row;
   if (t == 0)
-    a.status[s] = !me.known || me.tokens == 0 || most > me.row ? hkv::kPrefillNoRows
-                  : refused                                    ? hkv::kPrefillRefused
-                                                               : hkv::kPrefillRuns;
+    a.status[s] = !rows ? hkv::kPrefillNoRows : refused ? hkv::kPrefillRefused : hkv::kPrefillRuns;
+  if (!a.chunked) return;
+  // Starts that go backwards can give more chunks than the workspace has records
+  // for: the first sequence that does not fit leaves its part of them empty.
+  const uint32_t all = chunks_of(a, me);
+  const uint32_t first = min(before, a.max_chunks), room = a.max_chunks - first;
+  const uint32_t count = all <= room ? all : 0;
+  if (t == 0) {
+    if (all > room && rows) a.status[s] = hkv::kPrefillNoRows;
+    a.first_chunk[s] = (int32_t)first;
+    a.first_chunk[s + a.n_seqs] = (int32_t)count;
+    if (s == a.n_seqs - 1) a.first_chunk[2 * a.n_seqs] = (int32_t)(first + count);
+  }
+  if (all > room)
+    for (uint32_t c = first + t; c < a.max_chunks; c += kPlanThreads)
+      a.chunks[c] = hkv::PrefillChunk{};
+  // A chunk of a sequence that does not run is empty.
+  const bool runs = rows && !refused;
+  const uint32_t lead = chunk_lead(a, me), lead_chunks = (lead + kC - 1) / kC;
+  const uint32_t per = (a.block_tokens + kC - 1) / kC;
+  for (uint32_t c = t; c < count; c += kPlanThreads) {
+    uint32_t off = c * kC, end = lead;
+    if (c >= lead_chunks) {
+      const uint32_t k = c - lead_chunks;
+      end = lead + (k / per + 1) * a.block_tokens;
+      off = lead + k / per * a.block_tokens + k % per * kC;
+    }
+    end = min(end, (uint32_t)me.tokens);
+    hkv::PrefillChunk ck;
+    ck.seq = (int32_t)s;
+    ck.row = me.row + (int32_t)off;
+    ck.len = runs ? (int32_t)min(kC, end - off) : 0;
+    ck.off = (int32_t)off;
+    a.chunks[first + c] = ck;
+  }
 }
 
 // ---------------------------------------------------------------- token by token
 // hkv_kda_step's arithmetic with the state and the conv's taps kept in registers
 // from token to token: one workgroup per (head, sequence).
-template <class T, uint32_t kD, uint32_t kThreads>
+template <class T, uint32_t kDim, uint32_t kThreads>
 __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
   using E = typename T::type;
-  constexpr uint32_t kRowThreads = kD / 4;               // threads that hold a row
+  constexpr uint32_t kRowThreads = kDim / 4;               // threads that hold a row
   constexpr uint32_t kGroups = kThreads / kRowThreads;   // rows held at a time
-  constexpr uint32_t kRows = kD / kGroups;               // rows per thread
+  constexpr uint32_t kRows = kDim / kGroups;               // rows per thread
   constexpr uint32_t kWaves = kThreads / 64;
-  constexpr uint32_t kChannels = (3 * kD + kThreads - 1) / kThreads;  // conv rows per thread
-  static_assert(kGroups * kRows == kD && kRowThreads <= 64, "a head splits into whole rows");
+  constexpr uint32_t kChannels = (3 * kDim + kThreads - 1) / kThreads;  // conv rows per thread
+  static_assert(kGroups * kRows == kDim && kRowThreads <= 64, "a head splits into whole rows");
   // two of each, by the token's parity: the next token's are written while slower
   // waves still read this one's
-  __shared__ float y[2][3][kD];  // q, k, v after the conv
-  __shared__ float decay[2][kD];
+  __shared__ float y[2][3][kDim];  // q, k, v after the conv
+  __shared__ float decay[2][kDim];
   __shared__ v4f sums[2][kWaves][kRowThreads];
   const uint32_t h = blockIdx.x, s = blockIdx.y, t = threadIdx.x, lane = t & 63;
   const uint32_t c = t % kRowThreads, r0 = t / kRowThreads;
   const int32_t status = a.status[s];
   if (status == hkv::kPrefillNoRows) return;
   const int32_t row0 = a.starts[s], n = a.starts[s + 1] - row0;
-  E* const out = static_cast<E*>(a.out) + (int64_t)row0 * a.out_stride + (int64_t)h * kD + c * 4;
+  if (a.chunked && n > (int32_t)a.short_tokens) return;
+  E* const out = static_cast<E*>(a.out) + (int64_t)row0 * a.out_stride + (int64_t)h * kDim + c * 4;
   if (status == hkv::kPrefillRefused) {
     for (uint32_t i = r0; i < (uint32_t)n; i += kGroups)
       T::store4(out + (int64_t)i * a.out_stride, v4f{NAN, NAN, NAN, NAN});
@@ -138,7 +191,7 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
   }
   const int32_t src = a.src[s], position = a.positions[s];
   const int32_t* const table = a.table + (int64_t)s * a.table_stride;
-  const uint64_t state_off = a.conv_bytes + (uint64_t)h * kD * kD * 4;
+  const uint64_t state_off = a.conv_bytes + (uint64_t)h * kDim * kDim * 4;
   const uint32_t state_at = r0 * kRowThreads + c;  // in units of four values
   const uint32_t keep = a.taps - 1;
 
@@ -159,8 +212,8 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
 #pragma unroll
   for (uint32_t i = 0; i < kChannels; ++i) {
     const uint32_t w = t + i * kThreads;
-    if (w >= 3 * kD) break;
-    const uint64_t ch = ((uint64_t)(w / kD) * a.heads + h) * kD + w % kD;
+    if (w >= 3 * kDim) break;
+    const uint64_t ch = ((uint64_t)(w / kDim) * a.heads + h) * kDim + w % kDim;
     const E* wt = static_cast<const E*>(a.conv_weight) + ch * a.taps;
     const E* old = reinterpret_cast<const E*>(a.pages + (uint64_t)(src < 0 ? 0 : src) * a.stride) +
                    ch * keep;
@@ -177,8 +230,8 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
 #pragma unroll
     for (uint32_t i = 0; i < kChannels; ++i) {
       const uint32_t w = t + i * kThreads;
-      if (w >= 3 * kD) break;
-      const uint64_t ch = ((uint64_t)(w / kD) * a.heads + h) * kD + w % kD;
+      if (w >= 3 * kDim) break;
+      const uint64_t ch = ((uint64_t)(w / kDim) * a.heads + h) * kDim + w % kDim;
       const E x = static_cast<const E*>(a.x)[row * a.x_stride + (int64_t)ch];
       float sum = 0.0f;
 #pragma unroll
@@ -192,10 +245,10 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
         if (j + 1 < keep) taps[i][j] = taps[i][j + 1 < hkv::kKdaMaxKernel - 1 ? j + 1 : j];
         if (j + 1 == keep) taps[i][j] = x;
       }
-      y[b][w / kD][w % kD] = sum / (1.0f + expf(-sum));
+      y[b][w / kDim][w % kDim] = sum / (1.0f + expf(-sum));
     }
-    for (uint32_t i = t; i < kD; i += kThreads) {
-      const float g = a.log_decay[row * a.decay_stride + (int64_t)h * kD + i];
+    for (uint32_t i = t; i < kDim; i += kThreads) {
+      const float g = a.log_decay[row * a.decay_stride + (int64_t)h * kDim + i];
       decay[b][i] = expf(g > 0.0f ? 0.0f : g);
     }
     const float beta = a.beta[row * a.beta_stride + h];
@@ -203,7 +256,7 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
 
     // |q|^2, |k|^2 and q.k, by every wave for itself.
     float qq = 0.0f, kk = 0.0f, qk = 0.0f;
-    for (uint32_t i = lane; i < kD; i += 64) {
+    for (uint32_t i = lane; i < kDim; i += 64) {
       const float q = y[b][0][i], k = y[b][1][i];
       qq += q * q;
       kk += k * k;
@@ -264,12 +317,849 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
 #pragma unroll
     for (uint32_t i = 0; i < kChannels; ++i) {
       const uint32_t w = t + i * kThreads;
-      if (w >= 3 * kD) break;
-      const uint64_t ch = ((uint64_t)(w / kD) * a.heads + h) * kD + w % kD;
+      if (w >= 3 * kDim) break;
+      const uint64_t ch = ((uint64_t)(w / kDim) * a.heads + h) * kDim + w % kDim;
       E* to = reinterpret_cast<E*>(a.pages + (uint64_t)dst * a.stride) + ch * keep;
 #pragma unroll
       for (uint32_t j = 0; j + 1 < hkv::kKdaMaxKernel; ++j)
         if (j < keep) to[j] = taps[i][j];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- chunks
+// A chunk is up to 64 tokens of one sequence that end no later than their block.
+// With a_t the token's decays, R_t = a_1 .. a_t and D_ts = a_{s+1} .. a_t (products
+// per channel, all <= 1):
+//   A_ts = beta_t sum_c k_tc k_sc D_tsc (s < t),  P_ts = sum_c q_tc k_sc D_tsc (s <= t)
+//   T = (1 + A)^-1 diag(beta),  W = T (k R),  U0 = T V
+// do not depend on the state, so `form` computes them for all chunks and heads at
+// once; `scan` then goes through a sequence's chunks in order:
+//   U = U0 - W S,  O = (q R) S + P U,  S <- diag(R_64) S + (k D_64)^T U.
+// Decays are multiplied up, never divided: for blocks of 16 tokens and halves of
+// 32, D_ts is (decays since the half's start) x (decays up to it), both <= 1, so
+// that no factor overflows; within a block of 16 the pairs are summed one by one
+// in fp32.  Products of matrices run in fp16 with each operand as two terms, hi +
+// lo (22 bits), and three products (lo lo is below 2^-22); what is scaled by a
+// power of two to lie well inside fp16's range says so.  V's and S's columns never
+// mix, so each has a power of two of its own.
+constexpr uint32_t kD = hkv::kPrefillChunkDim;
+constexpr uint32_t kFormThreads = 256;
+constexpr float kUnit = 64.0f;  // scale of k and q operands (each at most 1 in size)
+
+typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+__device__ __forceinline__ float real(uint32_t x) { return __builtin_bit_cast(float, x); }
+
+// x = hi + lo, to 2^-22 of x.
+struct Terms2 {
+  v2h hi, lo;
+};
+__device__ __forceinline__ Terms2 terms(float x, float y) {
+  Terms2 t;
+  t.hi = __builtin_convertvector(v2f{x, y}, v2h);
+  t.lo = __builtin_convertvector(v2f{x - (float)t.hi[0], y - (float)t.hi[1]}, v2h);
+  return t;
+}
+struct Terms8 {
+  v8h hi, lo;
+};
+__device__ __forceinline__ Terms8 terms(v4f x, v4f y) {
+  const Terms2 a = terms(x[0], x[1]), b = terms(x[2], x[3]);
+  const Terms2 c = terms(y[0], y[1]), d = terms(y[2], y[3]);
+  Terms8 t;
+  t.hi = v8h{a.hi[0], a.hi[1], b.hi[0], b.hi[1], c.hi[0], c.hi[1], d.hi[0], d.hi[1]};
+  t.lo = v8h{a.lo[0], a.lo[1], b.lo[0], b.lo[1], c.lo[0], c.lo[1], d.lo[0], d.lo[1]};
+  return t;
+}
+
+__device__ __forceinline__ v4f mfma(v8h a, v8h b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v4f mfma3(const Terms8& a, const Terms8& b, v4f c) {
+  c = mfma(a.lo, b.hi, c);
+  c = mfma(a.hi, b.lo, c);
+  return mfma(a.hi, b.hi, c);
+}
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float x) {
+  return real((uint32_t)__builtin_amdgcn_update_dpp(0, (int)bits(x), kCtrl, 0xf, 0xf, true));
+}
+
+// Sums 32 values over the wave: lane l gets the sum of value l / 2.
+__device__ __forceinline__ float sum32(float (&v)[32], uint32_t lane) {
+  float a[16], b[8], c[4], d[2];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const auto r = __builtin_amdgcn_permlane32_swap(bits(v[i]), bits(v[i + 16]), false, false);
+    const uint32_t x = r[0], y = r[1];
+    a[i] = real(x) + real(y);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const auto r = __builtin_amdgcn_permlane16_swap(bits(a[i]), bits(a[i + 8]), false, false);
+    const uint32_t x = r[0], y = r[1];
+    b[i] = real(x) + real(y);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool up = lane & 8;
+    c[i] = (up ? b[i + 4] : b[i]) + dpp<0x128>(up ? b[i] : b[i + 4]);  // row_ror:8
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool up = lane & 4;
+    d[i] = (up ? c[i + 2] : c[i]) + dpp<0x141>(up ? c[i] : c[i + 2]);  // row_half_mirror
+  }
+  const bool up = lane & 2;
+  float r = (up ? d[1] : d[0]) + dpp<0x4e>(up ? d[0] : d[1]);  // quad_perm [2,3,0,1]
+  return r + dpp<0xb1>(r);                                     // quad_perm [1,0,3,2]
+}
+
+// Orders a wave's own LDS accesses (its instructions run in order).
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// LDS of `form`, bytes.  Planes: rows of 128 channels (`row`) or of 64 tokens.
+constexpr uint32_t kRowPlane = 16 * (kD * 2 + 16);   // 16 tokens
+constexpr uint32_t kRowStride = kD * 2 + 16;
+constexpr uint32_t kTokStride = kC * 2 + 16;
+constexpr uint32_t kTokPlane = kD * kTokStride;      // 128 channels x 64 tokens
+constexpr uint32_t kTPlane = kC * kTokStride;        // T: 64 x 64
+constexpr uint32_t kMStride = 68;                    // floats
+constexpr uint32_t kTmpStride = 36;
+constexpr uint32_t kOffM = 2 * kTPlane + 2 * kTokPlane;
+constexpr uint32_t kOffTmp = kOffM + kC * kMStride * 4;
+constexpr uint32_t kOffBeta = kOffTmp + 32 * kTmpStride * 4;
+constexpr uint32_t kOffTotal = kOffBeta + kC * 4;
+constexpr uint32_t kOffMost = kOffTotal + 4 * kD * 4;
+constexpr uint32_t kOffExps = kOffTotal;  // the totals are in registers by then
+constexpr uint32_t kFormLds = kOffMost + 4 * kD * 4;
+static_assert(12 * kRowPlane <= kOffM && 8 * kRowPlane <= kOffM && kFormLds <= 80 * 1024,
+              "two workgroups of `form` fit a CU");
+
+// One chunk's result in the workspace, as the scan's lanes load it (1 KiB for 64
+// lanes of 16 bytes; lane l: row or column l % 16, group g = l / 16).
+//   W, Q   [token tile][32 channels][hi, lo]: 8 channels 4 g + 0..3 and 16 + 4 g + 0..3
+//   K      [channel tile][32 tokens][hi, lo]: 8 tokens in the same order
+//   P      [tile of 16 x 32 tokens][hi, lo]
+//   U0     [channel tile][token tile]: 4 tokens 4 g + 0..3, fp32
+//   decay  [channel], fp32
+constexpr uint32_t kRecW = 0;
+constexpr uint32_t kRecQ = kRecW + 4 * (kD / 32) * 2048;
+constexpr uint32_t kRecK = kRecQ + 4 * (kD / 32) * 2048;
+constexpr uint32_t kRecP = kRecK + (kD / 16) * 2 * 2048;
+constexpr uint32_t kRecU = kRecP + 6 * 2048;
+constexpr uint32_t kRecDecay = kRecU + (kD / 16) * 4 * 1024;
+static_assert(kRecDecay + kD * 4 == hkv::kPrefillRecord, "the workspace holds a record");
+
+// Two channels of one row.
+struct __attribute__((packed, aligned(2))) Pair16 {
+  uint32_t v;
+};
+struct __attribute__((packed, aligned(4))) Pair32 {
+  float x, y;
+};
+
+template <class E>
+__device__ __forceinline__ v2f widen(uint32_t x) {
+  typedef E pair __attribute__((ext_vector_type(2)));
+  return __builtin_convertvector(__builtin_bit_cast(pair, x), v2f);
+}
+
+// The scan's order of a 32-row block's rows: lane group g's eight are 4 g + 0..3 and
+// 16 + 4 g + 0..3, since that is where a 16x16 product leaves two tiles.
+__device__ __forceinline__ v8h join(v4h a, v4h b) {
+  return v8h{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+template <class T>
+__device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, uint32_t h,
+                                     uint8_t* lds) {
+  using E = typename T::type;
+  const uint32_t t = threadIdx.x, w = t >> 6, lane = t & 63, lr = lane & 15, lg = lane >> 4;
+  const hkv::PrefillChunk ck = a.chunks[slot];
+  const int32_t len = ck.len;
+  const int32_t src = a.src[ck.seq];
+  uint8_t* const rec = a.records + ((uint64_t)slot * a.heads + h) * hkv::kPrefillRecord;
+  float* const M = reinterpret_cast<float*>(lds + kOffM);
+  float* const tmp = reinterpret_cast<float*>(lds + kOffTmp);
+  float* const beta = reinterpret_cast<float*>(lds + kOffBeta);
+  float* const total = reinterpret_cast<float*>(lds + kOffTotal);
+  float* const most = reinterpret_cast<float*>(lds + kOffMost);
+  int32_t* const exps = reinterpret_cast<int32_t*>(lds + kOffExps);
+  const int32_t t0 = (int32_t)w * 16;  // the wave's first token of the chunk
+  const uint32_t ch = lane * 2;        // the lane's channels: ch, ch + 1
+
+  // Loads: the wave's 16 tokens and the three before them; tokens behind the
+  // chunk's last read the last one's row and are blanked below.
+  uint32_t raw[3][19];
+  float g0[16], g1[16];
+#pragma unroll
+  for (int r = 0; r < 19; ++r) {
+    const int32_t o = min(t0 + r - 3, len - 1);
+    const int64_t row = (int64_t)ck.row + (ck.off + o < 0 ? 0 : o);
+    const E* x = static_cast<const E*>(a.x) + row * a.x_stride;
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      raw[p][r] = reinterpret_cast<const Pair16*>(
+          x + ((uint64_t)p * a.heads + h) * kD + ch)->v;
+    if (r >= 3) {
+      const Pair32 g = *reinterpret_cast<const Pair32*>(
+          a.log_decay + row * a.decay_stride + (uint64_t)h * kD + ch);
+      g0[r - 3] = g.x;
+      g1[r - 3] = g.y;
+    }
+  }
+  float b_t = 0.0f;  // lane i: token i's beta
+  if (t0 + (int32_t)lr < len)
+    b_t = a.beta[((int64_t)ck.row + t0 + lr) * a.beta_stride + h];
+  if (ck.off + t0 < 3) {  // taps from before the sequence's first row
+#pragma unroll
+    for (int r = 0; r < 3; ++r) {
+      const int32_t o = ck.off + t0 + r - 3;
+      if (o >= 0) continue;
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        uint32_t v = 0;
+        if (src >= 0) {
+          const uint16_t* old = reinterpret_cast<const uint16_t*>(
+              a.pages + (uint64_t)src * a.stride) +
+              (((uint64_t)p * a.heads + h) * kD + ch) * 3 + (3 + o);
+          v = (uint32_t)old[0] | ((uint32_t)old[3] << 16);
+        }
+        raw[p][r] = v;
+      }
+    }
+  }
+
+  // y = silu(conv), two channels of 16 tokens a lane.
+  v2f y[3][16];
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    const E* wt = static_cast<const E*>(a.conv_weight) +
+                  (((uint64_t)p * a.heads + h) * kD + ch) * 4;
+    v2f w4[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w4[j] = v2f{(float)wt[j], (float)wt[j + 4]};
+    v2f x[19];
+#pragma unroll
+    for (int r = 0; r < 19; ++r) x[r] = widen<E>(raw[p][r]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v2f s = w4[0] * x[i];
+#pragma unroll
+      for (int j = 1; j < 4; ++j) s += w4[j] * x[i + j];
+      const bool live = t0 + i < len;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float e = __builtin_amdgcn_exp2f(s[c] * -1.44269504f);
+        y[p][i][c] = live ? s[c] * __builtin_amdgcn_rcpf(1.0f + e) : 0.0f;
+      }
+    }
+  }
+
+  // q and k over their norms: 32 sums at once, each lane's root goes to all.
+  {
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v[i] = y[0][i][0] * y[0][i][0] + y[0][i][1] * y[0][i][1];
+      v[16 + i] = y[1][i][0] * y[1][i][0] + y[1][i][1] * y[1][i][1];
+    }
+    const float by = 1.0f / sqrtf(sum32(v, lane) + a.eps);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float nq = real((uint32_t)__builtin_amdgcn_readlane((int)bits(by), 2 * i));
+      const float nk = real((uint32_t)__builtin_amdgcn_readlane((int)bits(by), 32 + 2 * i));
+      y[0][i] *= nq;
+      y[1][i] *= nk;
+    }
+  }
+
+  // The block's decays, and their products from its start (with the token) and
+  // to its end (without).
+  v2f up[16], down[16];
+  {
+    v2f av[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const bool live = t0 + i < len;
+      const float x0 = g0[i] > 0.0f ? 0.0f : g0[i], x1 = g1[i] > 0.0f ? 0.0f : g1[i];
+      av[i][0] = live ? __builtin_amdgcn_exp2f(x0 * 1.44269504f) : 1.0f;
+      av[i][1] = live ? __builtin_amdgcn_exp2f(x1 * 1.44269504f) : 1.0f;
+    }
+    up[0] = av[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) up[i] = up[i - 1] * av[i];
+    down[15] = v2f{1.0f, 1.0f};
+#pragma unroll
+    for (int i = 14; i >= 0; --i) down[i] = down[i + 1] * av[i + 1];
+
+    // Pairs within the block.  Columns s = b and 15 - b together give 32 sums; lane
+    // 2 n gets sum n.  M holds A below its diagonal and P's transpose above: P_ts
+    // at [s][t + 1].
+    const uint32_t n = lane >> 1, m = n & 15;
+    float* const block = M + t0 * kMStride + t0;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      float v[32];
+      v2f p = y[1][b];
+#pragma unroll
+      for (int i = b; i < 16; ++i) {
+        if (i > b) {
+          p *= av[i];
+          v[i] = y[1][i][0] * p[0] + y[1][i][1] * p[1];
+          v[16 + i] = y[0][i][0] * p[0] + y[0][i][1] * p[1];
+        } else {
+          v[b] = y[0][b][0] * p[0] + y[0][b][1] * p[1];
+        }
+      }
+      p = y[1][15 - b];
+#pragma unroll
+      for (int i = 15 - b; i < 16; ++i) {
+        const int k = i - (15 - b);
+        if (i > 15 - b) {
+          p *= av[i];
+          v[k - 1] = y[1][i][0] * p[0] + y[1][i][1] * p[1];
+        }
+        v[16 + k] = y[0][i][0] * p[0] + y[0][i][1] * p[1];
+      }
+      const float sum = sum32(v, lane);
+      // n < b: A(16 - b + n, 15 - b); n = b: P(b, b); b < n < 16: A(n, b);
+      // 16 <= n <= 16 + b: P(15 - b + m, 15 - b); n > 16 + b: P(m, b)
+      const bool first = n < 16 ? m >= (uint32_t)b : m > (uint32_t)b;
+      const uint32_t col = first ? b : 15 - b;
+      const uint32_t row = first ? m : n < 16 ? 16 - b + m : 15 - b + m;
+      const bool is_p = n >= 16 || m == (uint32_t)b;
+      block[is_p ? col * kMStride + row + 1 : row * kMStride + col] = sum;
+    }
+  }
+  if (lane < 16) beta[t0 + lane] = b_t;
+  wave_fence();
+
+  // (1 + A)^-1 of the block: lane j solves for column j.
+  {
+    const float* const block = M + t0 * kMStride + t0;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) s += block[i * kMStride + j] * x[j];
+      x[i] = (lr == (uint32_t)i ? 1.0f : 0.0f) - beta[t0 + i] * s;
+    }
+    wave_fence();
+    if (lane < 16) {
+      float* const out = M + t0 * kMStride + t0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i >= (int)lane) out[i * kMStride + lane] = x[i];
+    }
+  }
+
+  // Totals of the block's decays, the largest values of its V.
+  {
+    *reinterpret_cast<v2f*>(total + w * kD + ch) = up[15];
+    v2f big = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      big[0] = fmaxf(big[0], fabsf(y[2][i][0]));
+      big[1] = fmaxf(big[1], fabsf(y[2][i][1]));
+    }
+    *reinterpret_cast<v2f*>(most + w * kD + ch) = big;
+  }
+
+  // A row plane holds 16 tokens' channels of one term.
+  auto put_row = [&](uint32_t plane, const v2f (&x)[16], const v2f (&by)[16], v2f scale) {
+    uint8_t* const to = lds + plane * kRowPlane + ch * 2;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const v2f z = x[i] * by[i] * scale;
+      const Terms2 s = terms(z[0], z[1]);
+      *reinterpret_cast<v2h*>(to + i * kRowStride) = s.hi;
+      *reinterpret_cast<v2h*>(to + kRowPlane + i * kRowStride) = s.lo;
+    }
+  };
+  auto get_row = [&](uint32_t plane, uint32_t kb) {
+    const uint8_t* const from = lds + plane * kRowPlane + lr * kRowStride + kb * 64 + lg * 16;
+    Terms8 s;
+    s.hi = *reinterpret_cast<const v8h*>(from);
+    s.lo = *reinterpret_cast<const v8h*>(from + kRowPlane);
+    return s;
+  };
+  const v2f unit = {kUnit, kUnit};
+  constexpr float kUnits = 1.0f / (kUnit * kUnit);
+  // A 16x16 tile of A (unscaled by beta) or of P's transpose goes to M.
+  auto put_m = [&](bool is_p, uint32_t row_block, uint32_t col_block, v4f x) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t row = row_block * 16 + lg * 4 + j, col = col_block * 16 + lr;
+      M[is_p ? col * kMStride + row + 1 : row * kMStride + col] = x[j] * kUnits;
+    }
+  };
+
+  // Blocks 1 x 0 and 3 x 2: decays meet at the later block's start.
+  {
+    const uint32_t pair = (w >> 1) * 6;
+    if (w & 1) {
+      put_row(pair + 2, y[1], up, unit);
+      put_row(pair + 4, y[0], up, unit);
+    } else {
+      put_row(pair, y[1], down, unit);
+    }
+  }
+  __syncthreads();
+  {
+    const uint32_t pair = w & 1, is_p = w >> 1;
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (uint32_t kb = 0; kb < kD / 32; ++kb)
+      acc = mfma3(get_row(pair * 6 + 2 + 2 * is_p, kb), get_row(pair * 6, kb), acc);
+    put_m(is_p, 2 * pair + 1, 2 * pair, acc);
+    wave_fence();
+    // T_10 = -T_11 (beta A_10 T_00), in fp32.
+    if (!is_p) {
+      const uint32_t r0 = pair * 32 + 16, c0 = pair * 32;
+      float* const x = tmp + pair * 16 * kTmpStride;
+      v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (uint32_t kk = 0; kk < 4; ++kk) {
+        const uint32_t k = kk * 4 + lg;
+        const float p = M[(r0 + lr) * kMStride + c0 + k];
+        const float q = k >= lr ? M[(c0 + k) * kMStride + c0 + lr] : 0.0f;
+        z = __builtin_amdgcn_mfma_f32_16x16x4f32(p, q, z, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[(lg * 4 + j) * kTmpStride + lr] = z[j] * beta[r0 + lg * 4 + j];
+      wave_fence();
+      z = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (uint32_t kk = 0; kk < 4; ++kk) {
+        const uint32_t k = kk * 4 + lg;
+        const float p = k <= lr ? M[(r0 + lr) * kMStride + r0 + k] : 0.0f;
+        z = __builtin_amdgcn_mfma_f32_16x16x4f32(p, x[k * kTmpStride + lr], z, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) M[(r0 + lg * 4 + j) * kMStride + c0 + lr] = -z[j];
+    }
+  }
+  // All blocks' totals, this lane's channels.
+  v2f tot[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) tot[b] = *reinterpret_cast<const v2f*>(total + b * kD + ch);
+  __syncthreads();
+
+  // Halves 1 x 0: decays meet at token 32.  Planes 0..3 hold the columns' blocks,
+  // 4..11 the rows'.
+  if (w >= 2) {
+    const v2f by = w == 3 ? tot[2] * unit : unit;
+    put_row(4 + (w - 2) * 4, y[1], up, by);
+    put_row(6 + (w - 2) * 4, y[0], up, by);
+  } else {
+    put_row(w * 2, y[1], down, w == 0 ? tot[1] * unit : unit);
+  }
+  __syncthreads();
+  {
+    const uint32_t i = w >> 1, j = w & 1;
+    v4f ka = {0.0f, 0.0f, 0.0f, 0.0f}, qa = ka;
+#pragma unroll
+    for (uint32_t kb = 0; kb < kD / 32; ++kb) {
+      const Terms8 c = get_row(j * 2, kb);
+      ka = mfma3(get_row(4 + i * 4, kb), c, ka);
+      qa = mfma3(get_row(6 + i * 4, kb), c, qa);
+    }
+    put_m(false, 2 + i, j, ka);
+    put_m(true, 2 + i, j, qa);
+  }
+  __syncthreads();
+
+  // T_10 = -T_11 (beta A_10 T_00) of the halves, in fp32; meanwhile q R goes out.
+  const v2f before = w == 0   ? v2f{1.0f, 1.0f}
+                     : w == 1 ? tot[0]
+                     : w == 2 ? tot[0] * tot[1]
+                              : tot[0] * tot[1] * tot[2];
+  const v2f after = w == 3   ? v2f{1.0f, 1.0f}
+                    : w == 2 ? tot[3]
+                    : w == 1 ? tot[3] * tot[2]
+                             : tot[3] * tot[2] * tot[1];
+  {
+    const uint32_t i = w >> 1, j = w & 1;
+    v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (uint32_t kk = 0; kk < 8; ++kk) {
+      const uint32_t k = kk * 4 + lg, col = j * 16 + lr;
+      const float p = M[(32 + i * 16 + lr) * kMStride + k];
+      const float q = k >= col ? M[k * kMStride + col] : 0.0f;
+      z = __builtin_amdgcn_mfma_f32_16x16x4f32(p, q, z, 0, 0, 0);
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const uint32_t row = i * 16 + lg * 4 + n;
+      tmp[row * kTmpStride + j * 16 + lr] = z[n] * beta[32 + row];
+    }
+    const v2f by = before * v2f{16.0f, 16.0f};
+    put_row(w * 2, y[0], up, by);
+  }
+  __syncthreads();
+  {
+    const uint32_t i = w >> 1, j = w & 1;
+    v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (uint32_t kk = 0; kk < 8; ++kk) {
+      const uint32_t k = kk * 4 + lg, row = i * 16 + lr;
+      const float p = k <= row ? M[(32 + row) * kMStride + 32 + k] : 0.0f;
+      z = __builtin_amdgcn_mfma_f32_16x16x4f32(p, tmp[k * kTmpStride + j * 16 + lr], z, 0, 0, 0);
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) M[(32 + i * 16 + lg * 4 + n) * kMStride + j * 16 + lr] = -z[n];
+    // q R (16 times itself), in the scan's order: wave w's token tile is w.
+#pragma unroll
+    for (uint32_t kb = 0; kb < kD / 32; ++kb) {
+      const uint8_t* const from = lds + w * 2 * kRowPlane + lr * kRowStride + kb * 64 + lg * 8;
+      uint8_t* const to = rec + kRecQ + (w * (kD / 32) + kb) * 2048 + lane * 16;
+#pragma unroll
+      for (uint32_t x = 0; x < 2; ++x) {
+        const v4h lo = *reinterpret_cast<const v4h*>(from + x * kRowPlane);
+        const v4h hi = *reinterpret_cast<const v4h*>(from + x * kRowPlane + 32);
+        *reinterpret_cast<v8h*>(to + x * 1024) = join(lo, hi);
+      }
+    }
+    // P (4096 times itself): tiles (0,0) (1,0) (2,0) (2,1) (3,0) (3,1) of 16 x 32.
+    for (uint32_t e = t; e < 6 * 64; e += kFormThreads) {
+      const uint32_t tile = e >> 6, ti = tile < 2 ? tile : 1 + (tile >> 1), kb = tile < 2 ? 0 : tile & 1;
+      const uint32_t l = e & 63, row = ti * 16 + (l & 15), s0 = kb * 32 + (l >> 4) * 4;
+      v4f x[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t s = s0 + half * 16 + n;
+          x[half][n] = s <= row ? M[s * kMStride + row + 1] * 4096.0f : 0.0f;
+        }
+      const Terms8 z = terms(x[0], x[1]);
+      uint8_t* const to = rec + kRecP + tile * 2048 + l * 16;
+      *reinterpret_cast<v8h*>(to) = z.hi;
+      *reinterpret_cast<v8h*>(to + 1024) = z.lo;
+    }
+  }
+  __syncthreads();
+
+  // T's terms (256 times itself) and k R, transposed: rows of 64 tokens.
+  uint8_t* const tok = lds + 2 * kTPlane;
+  auto put_tokens = [&](uint8_t* to, const v2f (&x)[16], const v2f* by, v2f scale) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        v4f z[2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = half * 8 + i;
+          z[i >> 2][i & 3] = x[k][c] * (by ? by[k][c] : 1.0f) * scale[c];
+        }
+        const Terms8 s = terms(z[0], z[1]);
+        uint8_t* const at = to + (ch + c) * kTokStride + t0 * 2 + half * 16;
+        *reinterpret_cast<v8h*>(at) = s.hi;
+        *reinterpret_cast<v8h*>(at + kTokPlane) = s.lo;
+      }
+  };
+  {
+    const uint32_t row = t >> 2, c0 = (t & 3) * 16;
+#pragma unroll
+    for (uint32_t part = 0; part < 2; ++part) {
+      v4f z[2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t col = c0 + part * 8 + i;
+        z[i >> 2][i & 3] = col <= row ? M[row * kMStride + col] * beta[col] * 256.0f : 0.0f;
+      }
+      const Terms8 s = terms(z[0], z[1]);
+      uint8_t* const at = lds + row * kTokStride + c0 * 2 + part * 16;
+      *reinterpret_cast<v8h*>(at) = s.hi;
+      *reinterpret_cast<v8h*>(at + kTPlane) = s.lo;
+    }
+    put_tokens(tok, y[1], up, before * unit);
+  }
+  __syncthreads();
+  auto get_t = [&](uint32_t ti, uint32_t kb) {
+    const uint8_t* const from = lds + (ti * 16 + lr) * kTokStride + kb * 64 + lg * 16;
+    Terms8 s;
+    s.hi = *reinterpret_cast<const v8h*>(from);
+    s.lo = *reinterpret_cast<const v8h*>(from + kTPlane);
+    return s;
+  };
+  auto get_tok = [&](uint32_t tile, uint32_t kb) {
+    const uint8_t* const from = tok + (tile * 16 + lr) * kTokStride + kb * 64 + lg * 16;
+    Terms8 s;
+    s.hi = *reinterpret_cast<const v8h*>(from);
+    s.lo = *reinterpret_cast<const v8h*>(from + kTokPlane);
+    return s;
+  };
+  {
+    // -W (256 times itself): its transpose's tiles, channels 32 w .. 32 w + 31.
+    Terms8 k[2][2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) k[c][kb] = get_tok(w * 2 + c, kb);
+#pragma unroll
+    for (uint32_t ti = 0; ti < 4; ++ti) {
+      v4f z[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+      for (uint32_t kb = 0; kb <= ti / 2; ++kb) {
+        const Terms8 x = get_t(ti, kb);
+        z[0] = mfma3(k[0][kb], x, z[0]);
+        z[1] = mfma3(k[1][kb], x, z[1]);
+      }
+      const Terms8 s = terms(z[0] * (-1.0f / kUnit), z[1] * (-1.0f / kUnit));
+      uint8_t* const to = rec + kRecW + (ti * (kD / 32) + w) * 2048 + lane * 16;
+      *reinterpret_cast<v8h*>(to) = s.hi;
+      *reinterpret_cast<v8h*>(to + 1024) = s.lo;
+    }
+  }
+  __syncthreads();
+  // V, each column scaled by 2^e to have its largest value in [2^8, 2^9).
+  {
+    int32_t e[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float big = most[ch + c];
+#pragma unroll
+      for (uint32_t b = 1; b < 4; ++b) big = fmaxf(big, most[b * kD + ch + c]);
+      e[c] = big > 0.0f ? 9 - __builtin_amdgcn_frexp_expf(big) : 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[2][i][c] = __builtin_ldexpf(y[2][i][c], e[c]);
+    }
+    put_tokens(tok, y[2], nullptr, v2f{1.0f, 1.0f});
+    if (w == 0) {
+      *reinterpret_cast<v2f*>(rec + kRecDecay + ch * 4) = tot[0] * tot[1] * tot[2] * tot[3];
+      exps[ch] = e[0];
+      exps[ch + 1] = e[1];
+    }
+  }
+  __syncthreads();
+  {
+#pragma unroll
+    for (uint32_t c = 0; c < 2; ++c) {
+      const uint32_t tile = w * 2 + c;
+      const Terms8 v0 = get_tok(tile, 0), v1 = get_tok(tile, 1);
+      const int32_t back = -8 - exps[tile * 16 + lr];  // T is 256 times itself
+#pragma unroll
+      for (uint32_t ti = 0; ti < 4; ++ti) {
+        v4f z = mfma3(get_t(ti, 0), v0, v4f{0.0f, 0.0f, 0.0f, 0.0f});
+        if (ti >= 2) z = mfma3(get_t(ti, 1), v1, z);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) z[n] = __builtin_ldexpf(z[n], back);
+        *reinterpret_cast<v4f*>(rec + kRecU + (tile * 4 + ti) * 1024 + lane * 16) = z;
+      }
+    }
+  }
+  __syncthreads();
+  // k D_64, over T's planes too.
+  put_tokens(lds, y[1], down, after * unit * v2f{4.0f, 4.0f});
+  __syncthreads();
+#pragma unroll
+  for (uint32_t c = 0; c < 2; ++c)
+#pragma unroll
+    for (uint32_t kb = 0; kb < 2; ++kb) {
+      const uint32_t tile = w * 2 + c;
+      const uint8_t* const from = lds + (tile * 16 + lr) * kTokStride + kb * 64 + lg * 8;
+      uint8_t* const to = rec + kRecK + (tile * 2 + kb) * 2048 + lane * 16;
+#pragma unroll
+      for (uint32_t x = 0; x < 2; ++x) {
+        const v4h lo = *reinterpret_cast<const v4h*>(from + x * kTokPlane);
+        const v4h hi = *reinterpret_cast<const v4h*>(from + x * kTokPlane + 32);
+        *reinterpret_cast<v8h*>(to + x * 1024) = join(lo, hi);
+      }
+    }
+}
+
+__device__ __forceinline__ v8h read8(const uint8_t* p) { return *(const HKV_GLOBAL v8h*)p; }
+__device__ __forceinline__ Terms8 read_terms(const uint8_t* p) {
+  Terms8 t;
+  t.hi = read8(p);
+  t.lo = read8(p + 1024);
+  return t;
+}
+
+// One wave goes through a sequence's chunks with 16 columns of a head's state in
+// registers (tile i: rows 16 i + 4 g + 0..3 of column lane % 16), which is the order
+// in which products take them again.
+template <class T>
+__device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint32_t h,
+                                     uint32_t cg, uint32_t lane) {
+  using E = typename T::type;
+  constexpr uint32_t kTiles = kD / 16;
+  const uint32_t lr = lane & 15, lg = lane >> 4;
+  const int32_t status = a.status[s];
+  const int32_t row0 = a.starts[s];
+  if (status == hkv::kPrefillNoRows) return;
+  const int32_t n = a.starts[s + 1] - row0;
+  if (n <= (int32_t)a.short_tokens) return;
+  E* const out = static_cast<E*>(a.out) + (int64_t)h * kD + cg * 16 + lg * 4;
+  if (status == hkv::kPrefillRefused) {
+    for (int32_t i = (int32_t)lr; i < n; i += 16)
+      T::store4(out + (int64_t)(row0 + i) * a.out_stride, v4f{NAN, NAN, NAN, NAN});
+    return;
+  }
+  const int32_t src = a.src[s], position = a.positions[s];
+  const int32_t* const table = a.table + (int64_t)s * a.table_stride;
+  const uint64_t state_off =
+      a.conv_bytes + (((uint64_t)h * kD + lg * 4) * kD + cg * 16 + lr) * 4;
+  v4f st[kTiles];
+#pragma unroll
+  for (uint32_t i = 0; i < kTiles; ++i) {
+    st[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (src < 0) continue;
+    const HKV_GLOBAL float* p =
+        (const HKV_GLOBAL float*)(a.pages + (uint64_t)src * a.stride + state_off) + i * 16 * kD;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) st[i][j] = p[j * kD];
+  }
+  // The source's conv taps of the head's channels: one of the head's waves writes
+  // the blocks' conv states.
+  constexpr uint32_t kConv = 3 * kD / 64;
+  uint16_t old[kConv][3];
+  if (cg == 0 && src >= 0) {
+#pragma unroll
+    for (uint32_t i = 0; i < kConv; ++i) {
+      const uint32_t c = lane + i * 64;
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(a.pages + (uint64_t)src * a.stride) +
+                          (((uint64_t)(c / kD) * a.heads + h) * kD + c % kD) * 3;
+#pragma unroll
+      for (int j = 0; j < 3; ++j) old[i][j] = p[j];
+    }
+  } else {
+#pragma unroll
+    for (uint32_t i = 0; i < kConv; ++i)
+#pragma unroll
+      for (int j = 0; j < 3; ++j) old[i][j] = 0;
+  }
+
+  int e = 0;  // the column is held 2^e times itself
+  const uint32_t slot0 = (uint32_t)a.first_chunk[s], count = (uint32_t)a.first_chunk[s + a.n_seqs];
+  for (uint32_t c = 0; c < count; ++c) {
+    const hkv::PrefillChunk ck = a.chunks[slot0 + c];
+    const uint8_t* const rec =
+        a.records + ((uint64_t)(slot0 + c) * a.heads + h) * hkv::kPrefillRecord + lane * 16;
+    v4f u[4];
+#pragma unroll
+    for (uint32_t ti = 0; ti < 4; ++ti)
+      u[ti] = *(const HKV_GLOBAL v4f*)(rec + kRecU + (cg * 4 + ti) * 1024);
+    // The column's scale follows its largest value, when that leaves [2^6, 2^12).
+    {
+      float big = 0.0f;
+#pragma unroll
+      for (uint32_t i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) big = fmaxf(big, fabsf(st[i][j]));
+      float fresh = 0.0f;
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fresh = fmaxf(fresh, fabsf(u[i][j]));
+      int top = max(big > 0.0f ? __builtin_amdgcn_frexp_expf(big) - e : -1000,
+                    fresh > 0.0f ? __builtin_amdgcn_frexp_expf(fresh) : -1000);
+      top = max(top, __shfl_xor(top, 16, 64));
+      top = max(top, __shfl_xor(top, 32, 64));
+      const bool off = top > -1000 && (top + e < 7 || top + e > 12);
+      if (__any(off)) {
+        const int to = off ? min(max(10 - top, -250), 250) : e;
+#pragma unroll
+        for (uint32_t i = 0; i < kTiles; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) st[i][j] = __builtin_ldexpf(st[i][j], to - e);
+        e = to;
+      }
+    }
+    Terms8 sf[kTiles / 2];
+#pragma unroll
+    for (uint32_t kb = 0; kb < kTiles / 2; ++kb) sf[kb] = terms(st[2 * kb], st[2 * kb + 1]);
+#pragma unroll
+    for (uint32_t ti = 0; ti < 4; ++ti)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[ti][j] = __builtin_ldexpf(u[ti][j], e + 8);
+    // U (256 times itself) and O's part from the state (16 times)
+#pragma unroll
+    for (uint32_t kb = 0; kb < kTiles / 2; ++kb)
+#pragma unroll
+      for (uint32_t ti = 0; ti < 4; ++ti)
+        u[ti] = mfma3(read_terms(rec + kRecW + (ti * (kD / 32) + kb) * 2048), sf[kb], u[ti]);
+    v4f o[4];
+#pragma unroll
+    for (uint32_t ti = 0; ti < 4; ++ti) o[ti] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (uint32_t kb = 0; kb < kTiles / 2; ++kb)
+#pragma unroll
+      for (uint32_t ti = 0; ti < 4; ++ti)
+        o[ti] = mfma3(sf[kb], read_terms(rec + kRecQ + (ti * (kD / 32) + kb) * 2048), o[ti]);
+    // U over 256: P U comes to 16 times itself, (256 k D)^T U to itself.
+    Terms8 uf[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+      uf[kb] = terms(u[2 * kb] * (1.0f / 65536.0f), u[2 * kb + 1] * (1.0f / 65536.0f));
+#pragma unroll
+    for (uint32_t i = 0; i < kTiles; ++i) {
+      const v4f d = *(const HKV_GLOBAL v4f*)(rec - lane * 16 + kRecDecay + (i * 16 + lg * 4) * 4);
+      st[i] *= d;
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (uint32_t i = 0; i < kTiles; ++i)
+        st[i] = mfma3(read_terms(rec + kRecK + (i * 2 + kb) * 2048), uf[kb], st[i]);
+#pragma unroll
+    for (uint32_t ti = 0; ti < 4; ++ti)
+#pragma unroll
+      for (uint32_t kb = 0; kb <= ti / 2; ++kb)
+        o[ti] = mfma3(uf[kb], read_terms(rec + kRecP + (ti + (ti == 3) + kb) * 2048), o[ti]);
+    // O's transpose: lane's token is lane % 16 of a tile, its columns 4 g + 0..3,
+    // whose scales are those columns' lanes'.
+    v4f back;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      back[j] = __builtin_ldexpf(a.scale, -4 - __shfl(e, (int)(lg * 4 + j), 64));
+#pragma unroll
+    for (uint32_t ti = 0; ti < 4; ++ti) {
+      const int32_t i = (int32_t)(ti * 16 + lr);
+      if (i < ck.len) T::store4(out + (int64_t)(ck.row + i) * a.out_stride, o[ti] * back);
+    }
+
+    const int32_t done = ck.off + ck.len;
+    const uint32_t last = (uint32_t)(position + done - 1);
+    if ((last + 1) % a.block_tokens != 0 && done != n) continue;
+    const int32_t dst = table[last / a.block_tokens];
+    if (dst < 0) continue;
+    HKV_GLOBAL float* p = (HKV_GLOBAL float*)(a.pages + (uint64_t)dst * a.stride + state_off);
+#pragma unroll
+    for (uint32_t i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[(i * 16 + j) * kD] = __builtin_ldexpf(st[i][j], -e);
+    if (cg != 0) continue;
+#pragma unroll
+    for (uint32_t i = 0; i < kConv; ++i) {
+      const uint32_t m = lane + i * 64;
+      const uint64_t chn = ((uint64_t)(m / kD) * a.heads + h) * kD + m % kD;
+      uint16_t* const to =
+          reinterpret_cast<uint16_t*>(a.pages + (uint64_t)dst * a.stride) + chn * 3;
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const int32_t at = done - 3 + j;  // of the sequence's tokens
+        uint16_t v;
+        if (at >= 0)
+          v = static_cast<const uint16_t*>(a.x)[(int64_t)(row0 + at) * a.x_stride + (int64_t)chn];
+        else
+          v = at == -3 ? old[i][0] : at == -2 ? old[i][1] : old[i][2];
+        to[j] = v;
+      }
     }
   }
 }
@@ -299,6 +1189,26 @@ HKV_TOKENS_DIMS(fp32, Fp32)
 #undef HKV_TOKENS
 #undef HKV_TOKENS_DIMS
 
+#define HKV_CHUNKS(suffix, T)                                                               \
+  extern "C" __global__ __launch_bounds__(kFormThreads, 2) void hkv_kda_form_##suffix(      \
+      hkv::PrefillArgs a) {                                                                 \
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kFormLds];                          \
+    const uint32_t slot = blockIdx.x / a.heads;                                             \
+    if (slot >= (uint32_t)a.first_chunk[2 * a.n_seqs] || a.chunks[slot].len == 0) return;   \
+    form<T>(a, slot, blockIdx.x % a.heads, lds);                                            \
+  }                                                                                         \
+  extern "C" __global__ __launch_bounds__(64) void hkv_kda_scan_##suffix(                   \
+      hkv::PrefillArgs a) {                                                                 \
+    /* the head's column groups on one XCD, which reads its records once */                 \
+    const uint32_t group = blockIdx.x / (8 * (kD / 16)), in = blockIdx.x % (8 * (kD / 16)); \
+    const uint32_t pair = group * 8 + in % 8;                                               \
+    if (pair < a.n_seqs * a.heads)                                                          \
+      scan<T>(a, pair / a.heads, pair % a.heads, in / 8, threadIdx.x);                      \
+  }
+HKV_CHUNKS(bf16, Bf16)
+HKV_CHUNKS(fp16, Fp16)
+#undef HKV_CHUNKS
+
 namespace hkv {
 
 int launch_prefill(const PrefillArgs& a, int32_t dtype, void* stream) {
@@ -318,6 +1228,16 @@ int launch_prefill(const PrefillArgs& a, int32_t dtype, void* stream) {
   hipError_t e = hipLaunchKernel(HKV_FN(hkv_kda_prefill_plan), dim3(a.n_seqs), dim3(kPlanThreads),
                                  params, 0, st);
   if (e != hipSuccess) return (int)e;
+  if (a.chunked) {
+    static const void* const kForm[2] = {HKV_FN(hkv_kda_form_bf16), HKV_FN(hkv_kda_form_fp16)};
+    static const void* const kScan[2] = {HKV_FN(hkv_kda_scan_bf16), HKV_FN(hkv_kda_scan_fp16)};
+    const uint32_t pairs = (a.n_seqs * a.heads + 7) / 8 * 8;
+    e = hipLaunchKernel(kForm[dtype], dim3(a.max_chunks * a.heads), dim3(kFormThreads), params, 0,
+                        st);
+    if (e != hipSuccess) return (int)e;
+    e = hipLaunchKernel(kScan[dtype], dim3(pairs * (kD / 16)), dim3(64), params, 0, st);
+    if (e != hipSuccess || a.short_tokens == 0) return (int)e;
+  }
   return (int)hipLaunchKernel(kTokens[dtype][i], dim3(a.heads, a.n_seqs), dim3(kThreads[i]),
                               params, 0, st);
 #undef HKV_FN

@@ -207,7 +207,15 @@ hkv_status plan_prefill(const hkv_layout* layout, const hkv_kda_prefill_args* a,
   k->heads = (uint32_t)heads;
   k->head_dim = (uint32_t)d;
   k->taps = (uint32_t)taps;
-  *w = hkv::prefill_workspace(k->n_seqs);
+  // In chunks where that pays (and is built): not for runs of a few tokens.
+  k->short_tokens = k->n_seqs > 1 ? hkv::kPrefillShort : 0;
+  k->chunked = d == (int64_t)hkv::kPrefillChunkDim && taps == 4 && es == 2 &&
+               k->max_seq_tokens > hkv::kPrefillShort;
+  // A sequence's blocks are cut each on its own: the last chunk of the first, of
+  // the last and of every whole block may be short.
+  if (k->chunked)
+    k->max_chunks = k->n_tokens / hkv::kPrefillChunk + k->n_tokens / k->block_tokens + 2 * k->n_seqs;
+  *w = hkv::prefill_workspace(k->n_seqs, k->max_chunks, k->heads);
   return HKV_OK;
 }
 
@@ -291,7 +299,11 @@ hkv_status prefill(const hkv_layout* layout, void* pool, const hkv_kda_prefill_a
   k.out_stride = a->out_stride;
   k.scale = a->scale;
   k.eps = a->eps;
-  k.status = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + w.status);
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  k.status = reinterpret_cast<int32_t*>(wsb + w.status);
+  k.first_chunk = reinterpret_cast<int32_t*>(wsb + w.first_chunk);
+  k.chunks = reinterpret_cast<hkv::PrefillChunk*>(wsb + w.chunks);
+  k.records = wsb + w.records;
   int dev = 0;
   st = stream_device(reinterpret_cast<hipStream_t>(stream), &dev);
   if (st != HKV_OK) return st;
