@@ -225,7 +225,7 @@ int launch_append(const AppendArgs& a, int32_t dtype, void* stream);
 // ---------------------------------------------------------------- KDA prefill
 constexpr uint32_t kPrefillChunk = 64;       // tokens
 constexpr uint32_t kPrefillChunkDim = 128;   // the head dim that is computed in chunks
-constexpr uint32_t kPrefillRecord = 3 * 32768 + 12288 + 32768 + 512;  // bytes of a chunk and head
+constexpr uint32_t kPrefillRecord = 3 * 32768 + 12288 + 32768 + 1024;  // bytes of a chunk and head
 
 // Runs of up to so many tokens go token by token (a call of one sequence has no
 // launch for them where it has chunks).
@@ -233,6 +233,8 @@ constexpr uint32_t kPrefillShort = 8;
 
 struct PrefillChunk {
   int32_t seq, row, len, off;  // its first token: row of the call, token of the sequence
+  int32_t dst;                 // the block that its last token's state goes to, or none
+  int32_t pad[3];
 };
 
 struct PrefillArgs {

@@ -156,6 +156,8 @@ __device__ __forceinline__ void plan(const hkv::PrefillArgs& a) {
     ck.row = me.row + (int32_t)off;
     ck.len = runs ? (int32_t)min(kC, end - off) : 0;
     ck.off = (int32_t)off;
+    ck.dst = HKV_NULL_BLOCK;
+    if (runs && off + kC >= end) ck.dst = own[(uint32_t)(me.position + (int32_t)off) / a.block_tokens];
     a.chunks[first + c] = ck;
   }
 }
@@ -350,6 +352,7 @@ constexpr float kUnit = 64.0f;  // scale of k and q operands (each at most 1 in 
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v2f __attribute__((ext_vector_type(2)));
+typedef int32_t v2i __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
@@ -360,9 +363,13 @@ struct Terms2 {
   v2h hi, lo;
 };
 __device__ __forceinline__ Terms2 terms(float x, float y) {
+  // one v_fma_mix a remainder: the compiler makes two instructions of a difference
+  float minus = -1.0f;
+  __asm__("" : "+s"(minus));
   Terms2 t;
   t.hi = __builtin_convertvector(v2f{x, y}, v2h);
-  t.lo = __builtin_convertvector(v2f{x - (float)t.hi[0], y - (float)t.hi[1]}, v2h);
+  t.lo = __builtin_convertvector(v2f{__builtin_fmaf((float)t.hi[0], minus, x),
+                                     __builtin_fmaf((float)t.hi[1], minus, y)}, v2h);
   return t;
 }
 struct Terms8 {
@@ -421,6 +428,11 @@ __device__ __forceinline__ float sum32(float (&v)[32], uint32_t lane) {
   return r + dpp<0xb1>(r);                                     // quad_perm [1,0,3,2]
 }
 
+// The wave's place in its workgroup, as a scalar.
+__device__ __forceinline__ uint32_t wave_index() {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+}
+
 // Orders a wave's own LDS accesses (its instructions run in order).
 __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -451,13 +463,15 @@ static_assert(12 * kRowPlane <= kOffM && 8 * kRowPlane <= kOffM && kFormLds <= 8
 //   P      [tile of 16 x 32 tokens][hi, lo]
 //   U0     [channel tile][token tile]: 4 tokens 4 g + 0..3, fp32
 //   decay  [channel], fp32
+//   exps   [channel]: V's largest value is below 2^exps; -1000: V is zero
 constexpr uint32_t kRecW = 0;
 constexpr uint32_t kRecQ = kRecW + 4 * (kD / 32) * 2048;
 constexpr uint32_t kRecK = kRecQ + 4 * (kD / 32) * 2048;
 constexpr uint32_t kRecP = kRecK + (kD / 16) * 2 * 2048;
 constexpr uint32_t kRecU = kRecP + 6 * 2048;
 constexpr uint32_t kRecDecay = kRecU + (kD / 16) * 4 * 1024;
-static_assert(kRecDecay + kD * 4 == hkv::kPrefillRecord, "the workspace holds a record");
+constexpr uint32_t kRecExps = kRecDecay + kD * 4;
+static_assert(kRecExps + kD * 4 == hkv::kPrefillRecord, "the workspace holds a record");
 
 // Two channels of one row.
 struct __attribute__((packed, aligned(2))) Pair16 {
@@ -479,12 +493,26 @@ __device__ __forceinline__ v8h join(v4h a, v4h b) {
   return v8h{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
+// A chunk as scalars, through the constant address space: a vector load would have to
+// wait for the operands that are under way.
+__device__ __forceinline__ hkv::PrefillChunk read_chunk(const hkv::PrefillArgs& a, uint32_t slot) {
+  typedef __attribute__((address_space(4))) const int32_t word;
+  word* const p = (word*)(uintptr_t)(a.chunks + slot);
+  hkv::PrefillChunk ck;
+  ck.seq = p[0];
+  ck.row = p[1];
+  ck.len = p[2];
+  ck.off = p[3];
+  ck.dst = p[4];
+  return ck;
+}
+
 template <class T>
 __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, uint32_t h,
                                      uint8_t* lds) {
   using E = typename T::type;
-  const uint32_t t = threadIdx.x, w = t >> 6, lane = t & 63, lr = lane & 15, lg = lane >> 4;
-  const hkv::PrefillChunk ck = a.chunks[slot];
+  const uint32_t t = threadIdx.x, w = wave_index(), lane = t & 63, lr = lane & 15, lg = lane >> 4;
+  const hkv::PrefillChunk ck = read_chunk(a, slot);
   const int32_t len = ck.len;
   const int32_t src = a.src[ck.seq];
   uint8_t* const rec = a.records + ((uint64_t)slot * a.heads + h) * hkv::kPrefillRecord;
@@ -805,7 +833,7 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
       const uint32_t row = i * 16 + lg * 4 + n;
       tmp[row * kTmpStride + j * 16 + lr] = z[n] * beta[32 + row];
     }
-    const v2f by = before * v2f{16.0f, 16.0f};
+    const v2f by = before * v2f{256.0f, 256.0f};
     put_row(w * 2, y[0], up, by);
   }
   __syncthreads();
@@ -820,7 +848,7 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n) M[(32 + i * 16 + lg * 4 + n) * kMStride + j * 16 + lr] = -z[n];
-    // q R (16 times itself), in the scan's order: wave w's token tile is w.
+    // q R (256 times itself), in the scan's order: wave w's token tile is w.
 #pragma unroll
     for (uint32_t kb = 0; kb < kD / 32; ++kb) {
       const uint8_t* const from = lds + w * 2 * kRowPlane + lr * kRowStride + kb * 64 + lg * 8;
@@ -929,12 +957,14 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
   // V, each column scaled by 2^e to have its largest value in [2^8, 2^9).
   {
     int32_t e[2];
+    v2i top;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       float big = most[ch + c];
 #pragma unroll
       for (uint32_t b = 1; b < 4; ++b) big = fmaxf(big, most[b * kD + ch + c]);
-      e[c] = big > 0.0f ? 9 - __builtin_amdgcn_frexp_expf(big) : 0;
+      top[c] = big > 0.0f ? __builtin_amdgcn_frexp_expf(big) : -1000;
+      e[c] = big > 0.0f ? 9 - top[c] : 0;
 #pragma unroll
       for (int i = 0; i < 16; ++i) y[2][i][c] = __builtin_ldexpf(y[2][i][c], e[c]);
     }
@@ -943,6 +973,7 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
       *reinterpret_cast<v2f*>(rec + kRecDecay + ch * 4) = tot[0] * tot[1] * tot[2] * tot[3];
       exps[ch] = e[0];
       exps[ch + 1] = e[1];
+      *reinterpret_cast<v2i*>(rec + kRecExps + ch * 4) = top;
     }
   }
   __syncthreads();
@@ -963,8 +994,8 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     }
   }
   __syncthreads();
-  // k D_64, over T's planes too.
-  put_tokens(lds, y[1], down, after * unit * v2f{4.0f, 4.0f});
+  // k D_64 (16 times itself), over T's planes too.
+  put_tokens(lds, y[1], down, after * v2f{16.0f, 16.0f});
   __syncthreads();
 #pragma unroll
   for (uint32_t c = 0; c < 2; ++c)
@@ -982,182 +1013,341 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     }
 }
 
-__device__ __forceinline__ v8h read8(const uint8_t* p) { return *(const HKV_GLOBAL v8h*)p; }
-__device__ __forceinline__ Terms8 read_terms(const uint8_t* p) {
+// A sequence's chunks in order, kCt x 16 columns of a head's state a workgroup of four
+// waves.  Wave w has rows 32 w .. 32 w + 31 of the state in registers (tile i: rows
+// 16 i + 4 g + 0..3 of column lane % 16) and computes tokens 16 w .. 16 w + 15 of U and
+// O, so that every operand that comes from memory is read by one wave alone: it
+// goes straight to that wave's registers, a chunk ahead.  What the waves need of each
+// other, the state's and U's terms, goes through LDS, in the order in which
+// products take them: two barriers a chunk.
+constexpr uint32_t kScanThreads = 256;
+
+// The state's terms by 32 rows, U's by 32 tokens, the columns' largest values by wave.
+template <uint32_t kCt>
+struct ScanShared {
+  v8h s[kCt][kD / 32][2][64];
+  v8h u[kCt][2][2][64];
+  float most[kCt][16][4];
+};
+
+// At a uniform address and a lane's offset.
+__device__ __forceinline__ Terms8 read_terms(const uint8_t* p, uint32_t at) {
   Terms8 t;
-  t.hi = read8(p);
-  t.lo = read8(p + 1024);
+  t.hi = *(const HKV_GLOBAL v8h*)(p + at);
+  t.lo = *(const HKV_GLOBAL v8h*)(p + 1024 + at);
   return t;
 }
 
-// One wave goes through a sequence's chunks with 16 columns of a head's state in
-// registers (tile i: rows 16 i + 4 g + 0..3 of column lane % 16), which is the order
-// in which products take them again.
-template <class T>
+template <class T, uint32_t kCt>
 __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint32_t h,
-                                     uint32_t cg, uint32_t lane) {
+                                     uint32_t group, ScanShared<kCt>& lds) {
   using E = typename T::type;
-  constexpr uint32_t kTiles = kD / 16;
-  const uint32_t lr = lane & 15, lg = lane >> 4;
+  const uint32_t w = wave_index(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int32_t status = a.status[s];
-  const int32_t row0 = a.starts[s];
   if (status == hkv::kPrefillNoRows) return;
-  const int32_t n = a.starts[s + 1] - row0;
+  const int32_t row0 = a.starts[s], n = a.starts[s + 1] - row0;
   if (n <= (int32_t)a.short_tokens) return;
-  E* const out = static_cast<E*>(a.out) + (int64_t)h * kD + cg * 16 + lg * 4;
+  const uint32_t col0 = group * kCt * 16;
+  E* const out = static_cast<E*>(a.out) + (int64_t)h * kD + col0 + lg * 4;
   if (status == hkv::kPrefillRefused) {
-    for (int32_t i = (int32_t)lr; i < n; i += 16)
-      T::store4(out + (int64_t)(row0 + i) * a.out_stride, v4f{NAN, NAN, NAN, NAN});
+    for (int32_t i = (int32_t)(lr + w * 16); i < n; i += 64)
+#pragma unroll
+      for (uint32_t ct = 0; ct < kCt; ++ct)
+        T::store4(out + (int64_t)(row0 + i) * a.out_stride + ct * 16, v4f{NAN, NAN, NAN, NAN});
     return;
   }
-  const int32_t src = a.src[s], position = a.positions[s];
-  const int32_t* const table = a.table + (int64_t)s * a.table_stride;
-  const uint64_t state_off =
-      a.conv_bytes + (((uint64_t)h * kD + lg * 4) * kD + cg * 16 + lr) * 4;
-  v4f st[kTiles];
-#pragma unroll
-  for (uint32_t i = 0; i < kTiles; ++i) {
-    st[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    if (src < 0) continue;
-    const HKV_GLOBAL float* p =
-        (const HKV_GLOBAL float*)(a.pages + (uint64_t)src * a.stride + state_off) + i * 16 * kD;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) st[i][j] = p[j * kD];
-  }
-  // The source's conv taps of the head's channels: one of the head's waves writes
-  // the blocks' conv states.
-  constexpr uint32_t kConv = 3 * kD / 64;
-  uint16_t old[kConv][3];
-  if (cg == 0 && src >= 0) {
-#pragma unroll
-    for (uint32_t i = 0; i < kConv; ++i) {
-      const uint32_t c = lane + i * 64;
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(a.pages + (uint64_t)src * a.stride) +
-                          (((uint64_t)(c / kD) * a.heads + h) * kD + c % kD) * 3;
-#pragma unroll
-      for (int j = 0; j < 3; ++j) old[i][j] = p[j];
-    }
-  } else {
-#pragma unroll
-    for (uint32_t i = 0; i < kConv; ++i)
-#pragma unroll
-      for (int j = 0; j < 3; ++j) old[i][j] = 0;
-  }
-
-  int e = 0;  // the column is held 2^e times itself
+  const int32_t src = a.src[s];
   const uint32_t slot0 = (uint32_t)a.first_chunk[s], count = (uint32_t)a.first_chunk[s + a.n_seqs];
-  for (uint32_t c = 0; c < count; ++c) {
-    const hkv::PrefillChunk ck = a.chunks[slot0 + c];
-    const uint8_t* const rec =
-        a.records + ((uint64_t)(slot0 + c) * a.heads + h) * hkv::kPrefillRecord + lane * 16;
-    v4f u[4];
+  const uint8_t* rec = a.records + ((uint64_t)slot0 * a.heads + h) * hkv::kPrefillRecord;
+  const uint64_t step = (uint64_t)a.heads * hkv::kPrefillRecord;
+  const uint64_t state_off =
+      a.conv_bytes + (((uint64_t)h * kD + w * 32 + lg * 4) * kD + col0 + lr) * 4;
+  v4f st[2][kCt];
 #pragma unroll
-    for (uint32_t ti = 0; ti < 4; ++ti)
-      u[ti] = *(const HKV_GLOBAL v4f*)(rec + kRecU + (cg * 4 + ti) * 1024);
-    // The column's scale follows its largest value, when that leaves [2^6, 2^12).
-    {
-      float big = 0.0f;
+  for (uint32_t i = 0; i < 2; ++i)
 #pragma unroll
-      for (uint32_t i = 0; i < kTiles; ++i)
+    for (uint32_t ct = 0; ct < kCt; ++ct) {
+      st[i][ct] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      if (src < 0) continue;
+      const HKV_GLOBAL float* p =
+          (const HKV_GLOBAL float*)(a.pages + (uint64_t)src * a.stride + state_off);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) big = fmaxf(big, fabsf(st[i][j]));
-      float fresh = 0.0f;
-#pragma unroll
-      for (uint32_t i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) fresh = fmaxf(fresh, fabsf(u[i][j]));
-      int top = max(big > 0.0f ? __builtin_amdgcn_frexp_expf(big) - e : -1000,
-                    fresh > 0.0f ? __builtin_amdgcn_frexp_expf(fresh) : -1000);
-      top = max(top, __shfl_xor(top, 16, 64));
-      top = max(top, __shfl_xor(top, 32, 64));
-      const bool off = top > -1000 && (top + e < 7 || top + e > 12);
-      if (__any(off)) {
-        const int to = off ? min(max(10 - top, -250), 250) : e;
-#pragma unroll
-        for (uint32_t i = 0; i < kTiles; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) st[i][j] = __builtin_ldexpf(st[i][j], to - e);
-        e = to;
-      }
+      for (int j = 0; j < 4; ++j) st[i][ct][j] = p[(i * 16 + j) * kD + ct * 16];
     }
-    Terms8 sf[kTiles / 2];
+  // A chunk's operands of this wave.
+  Terms8 wf[kD / 32], qf[kD / 32], pf[2], kf[2][2];
+  v4f u0[kCt], decay[2];
+  int32_t ve[kCt];  // exponents of V's columns, of the chunk after
+  const uint32_t p_first = w < 2 ? w : 2 * w - 2;
+  const uint32_t at = lane * 16;
+  auto fetch_wq = [&](const uint8_t* r, uint32_t kb) {
+    wf[kb] = read_terms(r + kRecW + (w * (kD / 32) + kb) * 2048, at);
+    qf[kb] = read_terms(r + kRecQ + (w * (kD / 32) + kb) * 2048, at);
+  };
+  auto fetch_u = [&](const uint8_t* r) {
 #pragma unroll
-    for (uint32_t kb = 0; kb < kTiles / 2; ++kb) sf[kb] = terms(st[2 * kb], st[2 * kb + 1]);
+    for (uint32_t ct = 0; ct < kCt; ++ct)
+      u0[ct] = *(const HKV_GLOBAL v4f*)(r + kRecU + ((group * kCt + ct) * 4 + w) * 1024 + at);
+  };
+  auto fetch_k = [&](const uint8_t* r, uint32_t i, uint32_t kb) {
+    kf[i][kb] = read_terms(r + kRecK + ((w * 2 + i) * 2 + kb) * 2048, at);
+  };
+  auto fetch_d = [&](const uint8_t* r) {
 #pragma unroll
-    for (uint32_t ti = 0; ti < 4; ++ti)
+    for (uint32_t i = 0; i < 2; ++i)
+      decay[i] = *(const HKV_GLOBAL v4f*)(r + kRecDecay + (w * 32 + i * 16) * 4 + lg * 16);
+  };
+  auto fetch_p = [&](const uint8_t* r) {
+    pf[0] = read_terms(r + kRecP + p_first * 2048, at);
+    if (w >= 2) pf[1] = read_terms(r + kRecP + (p_first + 1) * 2048, at);
+  };
+  auto fetch_e = [&](const uint8_t* r) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u[ti][j] = __builtin_ldexpf(u[ti][j], e + 8);
-    // U (256 times itself) and O's part from the state (16 times)
-#pragma unroll
-    for (uint32_t kb = 0; kb < kTiles / 2; ++kb)
-#pragma unroll
-      for (uint32_t ti = 0; ti < 4; ++ti)
-        u[ti] = mfma3(read_terms(rec + kRecW + (ti * (kD / 32) + kb) * 2048), sf[kb], u[ti]);
-    v4f o[4];
-#pragma unroll
-    for (uint32_t ti = 0; ti < 4; ++ti) o[ti] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (uint32_t kb = 0; kb < kTiles / 2; ++kb)
-#pragma unroll
-      for (uint32_t ti = 0; ti < 4; ++ti)
-        o[ti] = mfma3(sf[kb], read_terms(rec + kRecQ + (ti * (kD / 32) + kb) * 2048), o[ti]);
-    // U over 256: P U comes to 16 times itself, (256 k D)^T U to itself.
-    Terms8 uf[2];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-      uf[kb] = terms(u[2 * kb] * (1.0f / 65536.0f), u[2 * kb + 1] * (1.0f / 65536.0f));
-#pragma unroll
-    for (uint32_t i = 0; i < kTiles; ++i) {
-      const v4f d = *(const HKV_GLOBAL v4f*)(rec - lane * 16 + kRecDecay + (i * 16 + lg * 4) * 4);
-      st[i] *= d;
-    }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (uint32_t i = 0; i < kTiles; ++i)
-        st[i] = mfma3(read_terms(rec + kRecK + (i * 2 + kb) * 2048), uf[kb], st[i]);
-#pragma unroll
-    for (uint32_t ti = 0; ti < 4; ++ti)
-#pragma unroll
-      for (uint32_t kb = 0; kb <= ti / 2; ++kb)
-        o[ti] = mfma3(uf[kb], read_terms(rec + kRecP + (ti + (ti == 3) + kb) * 2048), o[ti]);
-    // O's transpose: lane's token is lane % 16 of a tile, its columns 4 g + 0..3,
-    // whose scales are those columns' lanes'.
-    v4f back;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      back[j] = __builtin_ldexpf(a.scale, -4 - __shfl(e, (int)(lg * 4 + j), 64));
-#pragma unroll
-    for (uint32_t ti = 0; ti < 4; ++ti) {
-      const int32_t i = (int32_t)(ti * 16 + lr);
-      if (i < ck.len) T::store4(out + (int64_t)(ck.row + i) * a.out_stride, o[ti] * back);
-    }
+    for (uint32_t ct = 0; ct < kCt; ++ct)
+      ve[ct] = *(const HKV_GLOBAL int32_t*)(r + kRecExps + (col0 + ct * 16) * 4 + lr * 4);
+  };
 
+  // Columns are held 2^e times themselves.  The state's terms for the products of the
+  // next chunk, scaled so that the largest value that the column's state, U and the
+  // next chunk's V have lies in [2^3, 2^8): a state after a chunk is at most 65 times
+  // the larger of the state before it and U, below fp16's limit of 2^16, and U at most
+  // 23 times the state and 256 times V, below 16 times that.
+  int e[kCt];
+#pragma unroll
+  for (uint32_t ct = 0; ct < kCt; ++ct) e[ct] = 0;
+  auto put_most = [&](const v4f (&u)[kCt], float by) {
+    float m[kCt];
+#pragma unroll
+    for (uint32_t ct = 0; ct < kCt; ++ct) {
+      float x = 0.0f, y = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x = fmaxf(x, fmaxf(fabsf(st[0][ct][j]), fabsf(st[1][ct][j])));
+        y = fmaxf(y, fabsf(u[ct][j]));
+      }
+      x = fmaxf(x, y * by);
+      const auto r = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
+      const uint32_t r0 = r[0], r1 = r[1];
+      x = fmaxf(real(r0), real(r1));
+      const auto q = __builtin_amdgcn_permlane16_swap(bits(x), bits(x), false, false);
+      const uint32_t q0 = q[0], q1 = q[1];
+      m[ct] = fmaxf(real(q0), real(q1));
+    }
+#pragma unroll
+    for (uint32_t ct = 0; ct < kCt; ++ct)
+      if (lg == ct) lds.most[ct][lr][w] = m[ct];
+  };
+  int to[kCt];  // the columns' next exponents
+  auto get_most = [&]() {
+#pragma unroll
+    for (uint32_t ct = 0; ct < kCt; ++ct) {
+      const v4f m = *reinterpret_cast<const v4f*>(lds.most[ct][lr]);
+      const float big = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+      const int top = max(big > 0.0f ? __builtin_amdgcn_frexp_expf(big) : -1000,
+                          ve[ct] > -1000 ? ve[ct] + e[ct] : -1000);
+      to[ct] = top > -1000 && (top < 4 || top > 8) ? e[ct] + 6 - top : e[ct];
+    }
+  };
+  auto put_state = [&]() {
+#pragma unroll
+    for (uint32_t ct = 0; ct < kCt; ++ct) {
+      if (__any(to[ct] != e[ct])) {
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            st[i][ct][j] = __builtin_ldexpf(st[i][ct][j], to[ct] - e[ct]);
+        e[ct] = to[ct];
+      }
+      const Terms8 x = terms(st[0][ct], st[1][ct]);
+      lds.s[ct][w][0][lane] = x.hi;
+      lds.s[ct][w][1][lane] = x.lo;
+    }
+  };
+  fetch_e(rec);
+  fetch_u(rec);
+#pragma unroll
+  for (uint32_t kb = 0; kb < kD / 32; ++kb) fetch_wq(rec, kb);
+  fetch_d(rec);
+#pragma unroll
+  for (uint32_t x = 0; x < 4; ++x) fetch_k(rec, x & 1, x >> 1);
+  fetch_p(rec);
+  {
+    v4f none[kCt];
+#pragma unroll
+    for (uint32_t ct = 0; ct < kCt; ++ct) none[ct] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    put_most(none, 0.0f);
+  }
+  __syncthreads();
+  get_most();
+  put_state();
+  __syncthreads();
+  hkv::PrefillChunk ck = read_chunk(a, slot0);
+  for (uint32_t c = 0; c < count; ++c) {
+    const hkv::PrefillChunk ck_next = read_chunk(a, slot0 + (c + 1 < count ? c + 1 : c));
+    // the last chunk's operands are fetched once more instead of none
+    const uint8_t* const next = c + 1 < count ? rec + step : rec;
+    fetch_e(next);
+    Terms8 sf[2][kCt];
+    auto get_state = [&](uint32_t kb) {
+#pragma unroll
+      for (uint32_t ct = 0; ct < kCt; ++ct) {
+        sf[kb & 1][ct].hi = lds.s[ct][kb][0][lane];
+        sf[kb & 1][ct].lo = lds.s[ct][kb][1][lane];
+      }
+    };
+    get_state(0);
+    // U = U0 - W S, 256 2^e times itself.
+    v4f u[kCt], o[kCt];
+#pragma unroll
+    for (uint32_t ct = 0; ct < kCt; ++ct)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u[ct][j] = __builtin_ldexpf(u0[ct][j], e[ct] + 8);
+        o[ct][j] = 0.0f;
+      }
+    // O's part from the state, 256 2^e times itself and transposed (a lane's token is
+    // lane % 16 of its tile, its columns 4 g + 0..3), side by side with U: the products
+    // of one sum lie 2 kCt apart.
+    fetch_u(next);
+#pragma unroll
+    for (uint32_t kb = 0; kb < kD / 32; ++kb) {
+      if (kb + 1 < kD / 32) get_state(kb + 1);
+#pragma unroll
+      for (int term = 0; term < 3; ++term)
+#pragma unroll
+        for (uint32_t ct = 0; ct < kCt; ++ct) {
+          const v8h x = term == 1 ? sf[kb & 1][ct].lo : sf[kb & 1][ct].hi;
+          u[ct] = mfma(term == 0 ? wf[kb].lo : wf[kb].hi, x, u[ct]);
+          o[ct] = mfma(x, term == 0 ? qf[kb].lo : qf[kb].hi, o[ct]);
+        }
+      // operands of the next chunk as their registers become free: a CU takes 64
+      // bytes a cycle, so that all of them in a row would hold up the products
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_wq(next, kb);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // U over 16: P U, 4096 times itself, comes to 256 times, 16 (k D)^T U to itself.
+#pragma unroll
+    for (uint32_t ct = 0; ct < kCt; ++ct) {
+      u[ct] *= 1.0f / 4096.0f;
+      const Terms2 x = terms(u[ct][0], u[ct][1]), y = terms(u[ct][2], u[ct][3]);
+      v4h* const hi = reinterpret_cast<v4h*>(&lds.u[ct][w >> 1][0][lane]) + (w & 1);
+      v4h* const lo = reinterpret_cast<v4h*>(&lds.u[ct][w >> 1][1][lane]) + (w & 1);
+      *hi = v4h{x.hi[0], x.hi[1], y.hi[0], y.hi[1]};
+      *lo = v4h{x.lo[0], x.lo[1], y.lo[0], y.lo[1]};
+    }
+    put_most(u, 16.0f);
+    __syncthreads();
+    // S <- D S + (k D)^T U.
+    Terms8 uf[kCt][2];
+#pragma unroll
+    for (uint32_t kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (uint32_t ct = 0; ct < kCt; ++ct) {
+        uf[ct][kb].hi = lds.u[ct][kb][0][lane];
+        uf[ct][kb].lo = lds.u[ct][kb][1][lane];
+      }
+    get_most();
+    int back[kCt][4];  // the scales of the columns that the lane has of O
+#pragma unroll
+    for (uint32_t ct = 0; ct < kCt; ++ct)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) back[ct][j] = -8 - __shfl(e[ct], (int)(lg * 4 + j), 64);
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i)
+#pragma unroll
+      for (uint32_t ct = 0; ct < kCt; ++ct) st[i][ct] *= decay[i];
+    fetch_d(next);
+#pragma unroll
+    for (uint32_t kb = 0; kb < 2; ++kb) {
+#pragma unroll
+      for (int term = 0; term < 3; ++term)
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i)
+#pragma unroll
+          for (uint32_t ct = 0; ct < kCt; ++ct)
+            st[i][ct] = mfma(term == 0 ? kf[i][kb].lo : kf[i][kb].hi,
+                             term == 1 ? uf[ct][kb].lo : uf[ct][kb].hi, st[i][ct]);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_k(next, 0, kb);
+      fetch_k(next, 1, kb);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (ck.dst >= 0) {
+      HKV_GLOBAL float* p = (HKV_GLOBAL float*)(a.pages + (uint64_t)ck.dst * a.stride + state_off);
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i)
+#pragma unroll
+        for (uint32_t ct = 0; ct < kCt; ++ct)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            p[(i * 16 + j) * kD + ct * 16] = __builtin_ldexpf(st[i][ct][j], -e[ct]);
+    }
+    put_state();
+    // O's part from U.
+#pragma unroll
+    for (int term = 0; term < 3; ++term)
+#pragma unroll
+      for (uint32_t ct = 0; ct < kCt; ++ct)
+        o[ct] = mfma(term == 1 ? uf[ct][0].lo : uf[ct][0].hi,
+                     term == 0 ? pf[0].lo : pf[0].hi, o[ct]);
+    if (w >= 2)
+#pragma unroll
+      for (int term = 0; term < 3; ++term)
+#pragma unroll
+        for (uint32_t ct = 0; ct < kCt; ++ct)
+          o[ct] = mfma(term == 1 ? uf[ct][1].lo : uf[ct][1].hi,
+                       term == 0 ? pf[1].lo : pf[1].hi, o[ct]);
+    fetch_p(next);
+    const int32_t i = (int32_t)(w * 16 + lr);
+#pragma unroll
+    for (uint32_t ct = 0; ct < kCt; ++ct) {
+      v4f x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = __builtin_ldexpf(o[ct][j], back[ct][j]) * a.scale;
+      if (i < ck.len) T::store4(out + (int64_t)(ck.row + i) * a.out_stride + ct * 16, x);
+    }
+    rec = next;
+    ck = ck_next;
+    __syncthreads();
+  }
+}
+
+// The conv states of a sequence's blocks, a head's channels by one workgroup: it reads the
+// source's before it writes any, since the source may be one of the blocks.
+__device__ __forceinline__ void conv_states(const hkv::PrefillArgs& a, uint32_t s, uint32_t h) {
+  if (a.status[s] != hkv::kPrefillRuns) return;
+  const int32_t src = a.src[s], row0 = a.starts[s];
+  const uint32_t slot0 = (uint32_t)a.first_chunk[s], count = (uint32_t)a.first_chunk[s + a.n_seqs];
+  constexpr uint32_t kEach = (3 * kD + kScanThreads - 1) / kScanThreads;
+  uint16_t old[kEach][3];
+#pragma unroll
+  for (uint32_t i = 0; i < kEach; ++i) {
+    const uint32_t m = threadIdx.x + i * kScanThreads;
+    const uint64_t ch = ((uint64_t)(m / kD) * a.heads + h) * kD + m % kD;
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      old[i][j] = src < 0 || m >= 3 * kD
+                      ? 0
+                      : reinterpret_cast<const uint16_t*>(a.pages + (uint64_t)src * a.stride)[ch * 3 + j];
+  }
+  for (uint32_t c = 0; c < count; ++c) {
+    const hkv::PrefillChunk ck = read_chunk(a, slot0 + c);
+    if (ck.dst < 0) continue;
     const int32_t done = ck.off + ck.len;
-    const uint32_t last = (uint32_t)(position + done - 1);
-    if ((last + 1) % a.block_tokens != 0 && done != n) continue;
-    const int32_t dst = table[last / a.block_tokens];
-    if (dst < 0) continue;
-    HKV_GLOBAL float* p = (HKV_GLOBAL float*)(a.pages + (uint64_t)dst * a.stride + state_off);
 #pragma unroll
-    for (uint32_t i = 0; i < kTiles; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) p[(i * 16 + j) * kD] = __builtin_ldexpf(st[i][j], -e);
-    if (cg != 0) continue;
-#pragma unroll
-    for (uint32_t i = 0; i < kConv; ++i) {
-      const uint32_t m = lane + i * 64;
-      const uint64_t chn = ((uint64_t)(m / kD) * a.heads + h) * kD + m % kD;
-      uint16_t* const to =
-          reinterpret_cast<uint16_t*>(a.pages + (uint64_t)dst * a.stride) + chn * 3;
+    for (uint32_t i = 0; i < kEach; ++i) {
+      const uint32_t m = threadIdx.x + i * kScanThreads;
+      if (m >= 3 * kD) break;
+      const uint64_t ch = ((uint64_t)(m / kD) * a.heads + h) * kD + m % kD;
+      uint16_t* const to = reinterpret_cast<uint16_t*>(a.pages + (uint64_t)ck.dst * a.stride) + ch * 3;
 #pragma unroll
       for (int j = 0; j < 3; ++j) {
-        const int32_t at = done - 3 + j;  // of the sequence's tokens
-        uint16_t v;
-        if (at >= 0)
-          v = static_cast<const uint16_t*>(a.x)[(int64_t)(row0 + at) * a.x_stride + (int64_t)chn];
-        else
-          v = at == -3 ? old[i][0] : at == -2 ? old[i][1] : old[i][2];
+        const int32_t k = done - 3 + j;  // of the sequence's tokens
+        uint16_t v = k == -3 ? old[i][0] : k == -2 ? old[i][1] : old[i][2];
+        if (k >= 0)
+          v = static_cast<const uint16_t*>(a.x)[(int64_t)(row0 + k) * a.x_stride + (int64_t)ch];
         to[j] = v;
       }
     }
@@ -1189,6 +1379,21 @@ HKV_TOKENS_DIMS(fp32, Fp32)
 #undef HKV_TOKENS
 #undef HKV_TOKENS_DIMS
 
+#define HKV_SCAN(name, T, tiles)                                                            \
+  extern "C" __global__ __launch_bounds__(kScanThreads, 2) void name(hkv::PrefillArgs a) {  \
+    __shared__ ScanShared<tiles> lds;                                                       \
+    /* a head's column groups on one XCD, which reads its records once */                   \
+    constexpr uint32_t kGroups = kD / 16 / tiles;                                           \
+    const uint32_t pairs = a.n_seqs * a.heads, scans = (pairs + 7) / 8 * 8 * kGroups;       \
+    if (blockIdx.x >= scans) {                                                              \
+      const uint32_t pair = blockIdx.x - scans;                                             \
+      conv_states(a, pair / a.heads, pair % a.heads);                                       \
+      return;                                                                               \
+    }                                                                                       \
+    const uint32_t pair = blockIdx.x / (8 * kGroups) * 8 + blockIdx.x % 8;                  \
+    if (pair < pairs)                                                                       \
+      scan<T, tiles>(a, pair / a.heads, pair % a.heads, blockIdx.x / 8 % kGroups, lds);     \
+  }
 #define HKV_CHUNKS(suffix, T)                                                               \
   extern "C" __global__ __launch_bounds__(kFormThreads, 2) void hkv_kda_form_##suffix(      \
       hkv::PrefillArgs a) {                                                                 \
@@ -1197,17 +1402,12 @@ HKV_TOKENS_DIMS(fp32, Fp32)
     if (slot >= (uint32_t)a.first_chunk[2 * a.n_seqs] || a.chunks[slot].len == 0) return;   \
     form<T>(a, slot, blockIdx.x % a.heads, lds);                                            \
   }                                                                                         \
-  extern "C" __global__ __launch_bounds__(64) void hkv_kda_scan_##suffix(                   \
-      hkv::PrefillArgs a) {                                                                 \
-    /* the head's column groups on one XCD, which reads its records once */                 \
-    const uint32_t group = blockIdx.x / (8 * (kD / 16)), in = blockIdx.x % (8 * (kD / 16)); \
-    const uint32_t pair = group * 8 + in % 8;                                               \
-    if (pair < a.n_seqs * a.heads)                                                          \
-      scan<T>(a, pair / a.heads, pair % a.heads, in / 8, threadIdx.x);                      \
-  }
+  HKV_SCAN(hkv_kda_scan_##suffix##_16, T, 1)                                                \
+  HKV_SCAN(hkv_kda_scan_##suffix##_32, T, 2)
 HKV_CHUNKS(bf16, Bf16)
 HKV_CHUNKS(fp16, Fp16)
 #undef HKV_CHUNKS
+#undef HKV_SCAN
 
 namespace hkv {
 
@@ -1230,12 +1430,16 @@ int launch_prefill(const PrefillArgs& a, int32_t dtype, void* stream) {
   if (e != hipSuccess) return (int)e;
   if (a.chunked) {
     static const void* const kForm[2] = {HKV_FN(hkv_kda_form_bf16), HKV_FN(hkv_kda_form_fp16)};
-    static const void* const kScan[2] = {HKV_FN(hkv_kda_scan_bf16), HKV_FN(hkv_kda_scan_fp16)};
-    const uint32_t pairs = (a.n_seqs * a.heads + 7) / 8 * 8;
+    static const void* const kScan[2][2] = {
+        {HKV_FN(hkv_kda_scan_bf16_16), HKV_FN(hkv_kda_scan_bf16_32)},
+        {HKV_FN(hkv_kda_scan_fp16_16), HKV_FN(hkv_kda_scan_fp16_32)}};
+    const uint32_t tiles = a.n_seqs * a.heads * (kD / 16) > 256 ? 2 : 1;
+    const uint32_t pairs = a.n_seqs * a.heads;
     e = hipLaunchKernel(kForm[dtype], dim3(a.max_chunks * a.heads), dim3(kFormThreads), params, 0,
                         st);
     if (e != hipSuccess) return (int)e;
-    e = hipLaunchKernel(kScan[dtype], dim3(pairs * (kD / 16)), dim3(64), params, 0, st);
+    e = hipLaunchKernel(kScan[dtype][tiles - 1], dim3((pairs + 7) / 8 * 8 * (kD / 16 / tiles) + pairs),
+                        dim3(kScanThreads), params, 0, st);
     if (e != hipSuccess || a.short_tokens == 0) return (int)e;
   }
   return (int)hipLaunchKernel(kTokens[dtype][i], dim3(a.heads, a.n_seqs), dim3(kThreads[i]),
