@@ -393,6 +393,12 @@ __device__ __forceinline__ v4f mfma3(const Terms8& a, const Terms8& b, v4f c) {
   return mfma(a.hi, b.hi, c);
 }
 
+__device__ __forceinline__ void mfma3(const Terms8& a, const Terms8& b, v4f (&c)[3]) {
+  c[0] = mfma(a.lo, b.hi, c[0]);
+  c[1] = mfma(a.hi, b.lo, c[1]);
+  c[2] = mfma(a.hi, b.hi, c[2]);
+}
+
 template <int kCtrl>
 __device__ __forceinline__ float dpp(float x) {
   return real((uint32_t)__builtin_amdgcn_update_dpp(0, (int)bits(x), kCtrl, 0xf, 0xf, true));
@@ -635,6 +641,10 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     // at [s][t + 1].
     const uint32_t n = lane >> 1, m = n & 15;
     float* const block = M + t0 * kMStride + t0;
+    float acc[16];  // lane j: column j of sum_s A(i, s) x_s
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+    float sums[8];
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
       float v[32];
@@ -666,29 +676,30 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
       const uint32_t col = first ? b : 15 - b;
       const uint32_t row = first ? m : n < 16 ? 16 - b + m : 15 - b + m;
       const bool is_p = n >= 16 || m == (uint32_t)b;
-      block[is_p ? col * kMStride + row + 1 : row * kMStride + col] = sum;
+      if (is_p) block[col * kMStride + row + 1] = sum;
+      sums[b] = sum;
     }
-  }
-  if (lane < 16) beta[t0 + lane] = b_t;
-  wave_fence();
-
-  // (1 + A)^-1 of the block: lane j solves for column j.
-  {
-    const float* const block = M + t0 * kMStride + t0;
+    // (1 + A)^-1 of the block: lane j solves for column j, with A's values as scalars
+    // from the lanes that have them.
     float x[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float s = 0.0f;
+    for (int s = 0; s < 16; ++s) {
+      const float b_s = real((uint32_t)__builtin_amdgcn_readlane((int)bits(b_t), s));
+      x[s] = (lr == (uint32_t)s ? 1.0f : 0.0f) - b_s * acc[s];
 #pragma unroll
-      for (int j = 0; j < i; ++j) s += block[i * kMStride + j] * x[j];
-      x[i] = (lr == (uint32_t)i ? 1.0f : 0.0f) - beta[t0 + i] * s;
+      for (int i = s + 1; i < 16; ++i) {
+        // A(i, s): in sums[s] at i for s < 8, in sums[15 - s] at i - s - 1 otherwise
+        const int from = s < 8 ? i : i - s - 1;
+        const float as = real(
+            (uint32_t)__builtin_amdgcn_readlane((int)bits(sums[s < 8 ? s : 15 - s]), 2 * from));
+        acc[i] += as * x[s];
+      }
     }
-    wave_fence();
     if (lane < 16) {
-      float* const out = M + t0 * kMStride + t0;
+      beta[t0 + lane] = b_t;
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (i >= (int)lane) out[i * kMStride + lane] = x[i];
+        if (i >= (int)lane) block[i * kMStride + lane] = x[i];
     }
   }
 
@@ -746,35 +757,38 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
   __syncthreads();
   {
     const uint32_t pair = w & 1, is_p = w >> 1;
-    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    v4f acc[3] = {};  // by term: a sum waits for the one before
 #pragma unroll
     for (uint32_t kb = 0; kb < kD / 32; ++kb)
-      acc = mfma3(get_row(pair * 6 + 2 + 2 * is_p, kb), get_row(pair * 6, kb), acc);
-    put_m(is_p, 2 * pair + 1, 2 * pair, acc);
+      mfma3(get_row(pair * 6 + 2 + 2 * is_p, kb), get_row(pair * 6, kb), acc);
+    put_m(is_p, 2 * pair + 1, 2 * pair, acc[0] + acc[1] + acc[2]);
     wave_fence();
     // T_10 = -T_11 (beta A_10 T_00), in fp32.
     if (!is_p) {
       const uint32_t r0 = pair * 32 + 16, c0 = pair * 32;
       float* const x = tmp + pair * 16 * kTmpStride;
-      v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+      v4f y2[2] = {};
 #pragma unroll
       for (uint32_t kk = 0; kk < 4; ++kk) {
         const uint32_t k = kk * 4 + lg;
         const float p = M[(r0 + lr) * kMStride + c0 + k];
         const float q = k >= lr ? M[(c0 + k) * kMStride + c0 + lr] : 0.0f;
-        z = __builtin_amdgcn_mfma_f32_16x16x4f32(p, q, z, 0, 0, 0);
+        y2[kk & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(p, q, y2[kk & 1], 0, 0, 0);
       }
+      v4f z = y2[0] + y2[1];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         x[(lg * 4 + j) * kTmpStride + lr] = z[j] * beta[r0 + lg * 4 + j];
       wave_fence();
-      z = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      y2[0] = y2[1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (uint32_t kk = 0; kk < 4; ++kk) {
         const uint32_t k = kk * 4 + lg;
         const float p = k <= lr ? M[(r0 + lr) * kMStride + r0 + k] : 0.0f;
-        z = __builtin_amdgcn_mfma_f32_16x16x4f32(p, x[k * kTmpStride + lr], z, 0, 0, 0);
+        y2[kk & 1] =
+            __builtin_amdgcn_mfma_f32_16x16x4f32(p, x[k * kTmpStride + lr], y2[kk & 1], 0, 0, 0);
       }
+      z = y2[0] + y2[1];
 #pragma unroll
       for (int j = 0; j < 4; ++j) M[(r0 + lg * 4 + j) * kMStride + c0 + lr] = -z[j];
     }
@@ -797,15 +811,15 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
   __syncthreads();
   {
     const uint32_t i = w >> 1, j = w & 1;
-    v4f ka = {0.0f, 0.0f, 0.0f, 0.0f}, qa = ka;
+    v4f ka[3] = {}, qa[3] = {};
 #pragma unroll
     for (uint32_t kb = 0; kb < kD / 32; ++kb) {
       const Terms8 c = get_row(j * 2, kb);
-      ka = mfma3(get_row(4 + i * 4, kb), c, ka);
-      qa = mfma3(get_row(6 + i * 4, kb), c, qa);
+      mfma3(get_row(4 + i * 4, kb), c, ka);
+      mfma3(get_row(6 + i * 4, kb), c, qa);
     }
-    put_m(false, 2 + i, j, ka);
-    put_m(true, 2 + i, j, qa);
+    put_m(false, 2 + i, j, ka[0] + ka[1] + ka[2]);
+    put_m(true, 2 + i, j, qa[0] + qa[1] + qa[2]);
   }
   __syncthreads();
 
@@ -820,14 +834,15 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
                              : tot[3] * tot[2] * tot[1];
   {
     const uint32_t i = w >> 1, j = w & 1;
-    v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+    v4f y2[2] = {};
 #pragma unroll
     for (uint32_t kk = 0; kk < 8; ++kk) {
       const uint32_t k = kk * 4 + lg, col = j * 16 + lr;
       const float p = M[(32 + i * 16 + lr) * kMStride + k];
       const float q = k >= col ? M[k * kMStride + col] : 0.0f;
-      z = __builtin_amdgcn_mfma_f32_16x16x4f32(p, q, z, 0, 0, 0);
+      y2[kk & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(p, q, y2[kk & 1], 0, 0, 0);
     }
+    const v4f z = y2[0] + y2[1];
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const uint32_t row = i * 16 + lg * 4 + n;
@@ -839,13 +854,15 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
   __syncthreads();
   {
     const uint32_t i = w >> 1, j = w & 1;
-    v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+    v4f y2[2] = {};
 #pragma unroll
     for (uint32_t kk = 0; kk < 8; ++kk) {
       const uint32_t k = kk * 4 + lg, row = i * 16 + lr;
       const float p = k <= row ? M[(32 + row) * kMStride + 32 + k] : 0.0f;
-      z = __builtin_amdgcn_mfma_f32_16x16x4f32(p, tmp[k * kTmpStride + j * 16 + lr], z, 0, 0, 0);
+      y2[kk & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(p, tmp[k * kTmpStride + j * 16 + lr],
+                                                        y2[kk & 1], 0, 0, 0);
     }
+    const v4f z = y2[0] + y2[1];
 #pragma unroll
     for (int n = 0; n < 4; ++n) M[(32 + i * 16 + lg * 4 + n) * kMStride + j * 16 + lr] = -z[n];
     // q R (256 times itself), in the scan's order: wave w's token tile is w.
@@ -938,16 +955,24 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) k[c][kb] = get_tok(w * 2 + c, kb);
+    v4f z[4][2] = {};
+#pragma unroll
+    for (uint32_t kb = 0; kb < 2; ++kb) {
+      Terms8 x[4];
+#pragma unroll
+      for (uint32_t ti = kb * 2; ti < 4; ++ti) x[ti] = get_t(ti, kb);
+#pragma unroll
+      for (int term = 0; term < 3; ++term)
+#pragma unroll
+        for (uint32_t ti = kb * 2; ti < 4; ++ti)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            z[ti][c] = mfma(term == 0 ? k[c][kb].lo : k[c][kb].hi,
+                            term == 1 ? x[ti].lo : x[ti].hi, z[ti][c]);
+    }
 #pragma unroll
     for (uint32_t ti = 0; ti < 4; ++ti) {
-      v4f z[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll
-      for (uint32_t kb = 0; kb <= ti / 2; ++kb) {
-        const Terms8 x = get_t(ti, kb);
-        z[0] = mfma3(k[0][kb], x, z[0]);
-        z[1] = mfma3(k[1][kb], x, z[1]);
-      }
-      const Terms8 s = terms(z[0] * (-1.0f / kUnit), z[1] * (-1.0f / kUnit));
+      const Terms8 s = terms(z[ti][0] * (-1.0f / kUnit), z[ti][1] * (-1.0f / kUnit));
       uint8_t* const to = rec + kRecW + (ti * (kD / 32) + w) * 2048 + lane * 16;
       *reinterpret_cast<v8h*>(to) = s.hi;
       *reinterpret_cast<v8h*>(to + 1024) = s.lo;
@@ -978,18 +1003,35 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
   }
   __syncthreads();
   {
+    Terms8 v[2][2];
+#pragma unroll
+    for (uint32_t c = 0; c < 2; ++c)
+#pragma unroll
+      for (uint32_t kb = 0; kb < 2; ++kb) v[c][kb] = get_tok(w * 2 + c, kb);
+    v4f z[4][2] = {};
+#pragma unroll
+    for (uint32_t kb = 0; kb < 2; ++kb) {
+      Terms8 x[4];
+#pragma unroll
+      for (uint32_t ti = kb * 2; ti < 4; ++ti) x[ti] = get_t(ti, kb);
+#pragma unroll
+      for (int term = 0; term < 3; ++term)
+#pragma unroll
+        for (uint32_t ti = kb * 2; ti < 4; ++ti)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            z[ti][c] = mfma(term == 0 ? x[ti].lo : x[ti].hi,
+                            term == 1 ? v[c][kb].lo : v[c][kb].hi, z[ti][c]);
+    }
 #pragma unroll
     for (uint32_t c = 0; c < 2; ++c) {
       const uint32_t tile = w * 2 + c;
-      const Terms8 v0 = get_tok(tile, 0), v1 = get_tok(tile, 1);
       const int32_t back = -8 - exps[tile * 16 + lr];  // T is 256 times itself
 #pragma unroll
       for (uint32_t ti = 0; ti < 4; ++ti) {
-        v4f z = mfma3(get_t(ti, 0), v0, v4f{0.0f, 0.0f, 0.0f, 0.0f});
-        if (ti >= 2) z = mfma3(get_t(ti, 1), v1, z);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) z[n] = __builtin_ldexpf(z[n], back);
-        *reinterpret_cast<v4f*>(rec + kRecU + (tile * 4 + ti) * 1024 + lane * 16) = z;
+        for (int n = 0; n < 4; ++n) z[ti][c][n] = __builtin_ldexpf(z[ti][c][n], back);
+        *reinterpret_cast<v4f*>(rec + kRecU + (tile * 4 + ti) * 1024 + lane * 16) = z[ti][c];
       }
     }
   }
