@@ -387,11 +387,6 @@ __device__ __forceinline__ Terms8 terms(v4f x, v4f y) {
 __device__ __forceinline__ v4f mfma(v8h a, v8h b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ v4f mfma3(const Terms8& a, const Terms8& b, v4f c) {
-  c = mfma(a.lo, b.hi, c);
-  c = mfma(a.hi, b.lo, c);
-  return mfma(a.hi, b.hi, c);
-}
 
 __device__ __forceinline__ void mfma3(const Terms8& a, const Terms8& b, v4f (&c)[3]) {
   c[0] = mfma(a.lo, b.hi, c[0]);
@@ -641,6 +636,7 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     // at [s][t + 1].
     const uint32_t n = lane >> 1, m = n & 15;
     float* const block = M + t0 * kMStride + t0;
+    float* const waste = tmp + w * 8;
     float acc[16];  // lane j: column j of sum_s A(i, s) x_s
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
@@ -671,13 +667,12 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
       }
       const float sum = sum32(v, lane);
       // n < b: A(16 - b + n, 15 - b); n = b: P(b, b); b < n < 16: A(n, b);
-      // 16 <= n <= 16 + b: P(15 - b + m, 15 - b); n > 16 + b: P(m, b)
-      const bool first = n < 16 ? m >= (uint32_t)b : m > (uint32_t)b;
-      const uint32_t col = first ? b : 15 - b;
-      const uint32_t row = first ? m : n < 16 ? 16 - b + m : 15 - b + m;
-      const bool is_p = n >= 16 || m == (uint32_t)b;
-      if (is_p) block[col * kMStride + row + 1] = sum;
+      // 16 <= n <= 16 + b: P(15 - b + m, 15 - b); n > 16 + b: P(m, b).  Lanes with A write
+      // to where nobody reads.
       sums[b] = sum;
+      const uint32_t to = n >= 16 ? (m > (uint32_t)b ? b * kMStride : (15 - b) * (kMStride + 1))
+                                  : b * kMStride;
+      (n >= 16 || m == (uint32_t)b ? block : waste)[to + m + 1] = sum;
     }
     // (1 + A)^-1 of the block: lane j solves for column j, with A's values as scalars
     // from the lanes that have them.
@@ -694,6 +689,7 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
             (uint32_t)__builtin_amdgcn_readlane((int)bits(sums[s < 8 ? s : 15 - s]), 2 * from));
         acc[i] += as * x[s];
       }
+      __builtin_amdgcn_sched_barrier(0);  // a column's scalars at a time
     }
     if (lane < 16) {
       beta[t0 + lane] = b_t;
