@@ -338,15 +338,15 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
 // do not depend on the state, so `form` computes them for all chunks and heads at
 // once; `scan` then goes through a sequence's chunks in order:
 //   U = U0 - W S,  O = (q R) S + P U,  S <- diag(R_64) S + (k D_64)^T U.
-// Decays are multiplied up, never divided: for blocks of 16 tokens and halves of
-// 32, D_ts is (decays since the half's start) x (decays up to it), both <= 1, so
-// that no factor overflows; within a block of 16 the pairs are summed one by one
-// in fp32.  Products of matrices run in fp16 with each operand as two terms, hi +
+// Decays are multiplied up, never divided: where t lies in the later half of 16, 32 or
+// 64 tokens and s in the earlier, D_ts is (decays since the later half's start) x (decays
+// up to it), both <= 1, so that no factor overflows; within 8 tokens the pairs are
+// summed one by one in fp32.  Products of matrices run in fp16 with each operand as two terms, hi +
 // lo (22 bits), and three products (lo lo is below 2^-22); what is scaled by a
 // power of two to lie well inside fp16's range says so.  V's and S's columns never
 // mix, so each has a power of two of its own.
 constexpr uint32_t kD = hkv::kPrefillChunkDim;
-constexpr uint32_t kFormThreads = 256;
+constexpr uint32_t kFormThreads = 512;
 constexpr float kUnit = 64.0f;  // scale of k and q operands (each at most 1 in size)
 
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
@@ -399,34 +399,30 @@ __device__ __forceinline__ float dpp(float x) {
   return real((uint32_t)__builtin_amdgcn_update_dpp(0, (int)bits(x), kCtrl, 0xf, 0xf, true));
 }
 
-// Sums 32 values over the wave: lane l gets the sum of value l / 2.
-__device__ __forceinline__ float sum32(float (&v)[32], uint32_t lane) {
-  float a[16], b[8], c[4], d[2];
+// Sums 16 values over the wave: lane l gets the sum of value l / 4.
+__device__ __forceinline__ float sum16(const float (&v)[16], uint32_t lane) {
+  float a[8], b[4], c[2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const auto r = __builtin_amdgcn_permlane32_swap(bits(v[i]), bits(v[i + 16]), false, false);
+  for (int i = 0; i < 8; ++i) {
+    const auto r = __builtin_amdgcn_permlane32_swap(bits(v[i]), bits(v[i + 8]), false, false);
     const uint32_t x = r[0], y = r[1];
     a[i] = real(x) + real(y);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const auto r = __builtin_amdgcn_permlane16_swap(bits(a[i]), bits(a[i + 8]), false, false);
+  for (int i = 0; i < 4; ++i) {
+    const auto r = __builtin_amdgcn_permlane16_swap(bits(a[i]), bits(a[i + 4]), false, false);
     const uint32_t x = r[0], y = r[1];
     b[i] = real(x) + real(y);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool up = lane & 8;
-    c[i] = (up ? b[i + 4] : b[i]) + dpp<0x128>(up ? b[i] : b[i + 4]);  // row_ror:8
-  }
-#pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const bool up = lane & 4;
-    d[i] = (up ? c[i + 2] : c[i]) + dpp<0x141>(up ? c[i] : c[i + 2]);  // row_half_mirror
+    const bool up = lane & 8;
+    c[i] = (up ? b[i + 2] : b[i]) + dpp<0x128>(up ? b[i] : b[i + 2]);  // row_ror:8
   }
-  const bool up = lane & 2;
-  float r = (up ? d[1] : d[0]) + dpp<0x4e>(up ? d[0] : d[1]);  // quad_perm [2,3,0,1]
-  return r + dpp<0xb1>(r);                                     // quad_perm [1,0,3,2]
+  const bool up = lane & 4;
+  float r = (up ? c[1] : c[0]) + dpp<0x141>(up ? c[0] : c[1]);  // row_half_mirror
+  r += dpp<0x4e>(r);                                            // quad_perm [2,3,0,1]
+  return r + dpp<0xb1>(r);                                      // quad_perm [1,0,3,2]
 }
 
 // The wave's place in its workgroup, as a scalar.
@@ -451,11 +447,8 @@ constexpr uint32_t kOffM = 2 * kTPlane + 2 * kTokPlane;
 constexpr uint32_t kOffTmp = kOffM + kC * kMStride * 4;
 constexpr uint32_t kOffBeta = kOffTmp + 32 * kTmpStride * 4;
 constexpr uint32_t kOffTotal = kOffBeta + kC * 4;
-constexpr uint32_t kOffMost = kOffTotal + 4 * kD * 4;
-constexpr uint32_t kOffExps = kOffTotal;  // the totals are in registers by then
-constexpr uint32_t kFormLds = kOffMost + 4 * kD * 4;
-static_assert(12 * kRowPlane <= kOffM && 8 * kRowPlane <= kOffM && kFormLds <= 80 * 1024,
-              "two workgroups of `form` fit a CU");
+constexpr uint32_t kFormLds = kOffTotal + 8 * kD * 4;
+static_assert(12 * kRowPlane <= kOffM && kFormLds <= 80 * 1024, "two workgroups of `form` fit a CU");
 
 // One chunk's result in the workspace, as the scan's lanes load it (1 KiB for 64
 // lanes of 16 bytes; lane l: row or column l % 16, group g = l / 16).
@@ -521,24 +514,21 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
   float* const tmp = reinterpret_cast<float*>(lds + kOffTmp);
   float* const beta = reinterpret_cast<float*>(lds + kOffBeta);
   float* const total = reinterpret_cast<float*>(lds + kOffTotal);
-  float* const most = reinterpret_cast<float*>(lds + kOffMost);
-  int32_t* const exps = reinterpret_cast<int32_t*>(lds + kOffExps);
-  const int32_t t0 = (int32_t)w * 16;  // the wave's first token of the chunk
+  const int32_t t0 = (int32_t)w * 8;   // the wave's first token of the chunk
   const uint32_t ch = lane * 2;        // the lane's channels: ch, ch + 1
 
-  // Loads: the wave's 16 tokens and the three before them; tokens behind the
-  // chunk's last read the last one's row and are blanked below.
-  uint32_t raw[3][19];
-  float g0[16], g1[16];
+  // Loads: the wave's 8 tokens and the three before them; tokens behind the chunk's
+  // last read the last one's row and are blanked below.
+  uint32_t raw[3][11];
+  float g0[8], g1[8];
 #pragma unroll
-  for (int r = 0; r < 19; ++r) {
+  for (int r = 0; r < 11; ++r) {
     const int32_t o = min(t0 + r - 3, len - 1);
     const int64_t row = (int64_t)ck.row + (ck.off + o < 0 ? 0 : o);
     const E* x = static_cast<const E*>(a.x) + row * a.x_stride;
 #pragma unroll
     for (int p = 0; p < 3; ++p)
-      raw[p][r] = reinterpret_cast<const Pair16*>(
-          x + ((uint64_t)p * a.heads + h) * kD + ch)->v;
+      raw[p][r] = reinterpret_cast<const Pair16*>(x + ((uint64_t)p * a.heads + h) * kD + ch)->v;
     if (r >= 3) {
       const Pair32 g = *reinterpret_cast<const Pair32*>(
           a.log_decay + row * a.decay_stride + (uint64_t)h * kD + ch);
@@ -547,8 +537,8 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     }
   }
   float b_t = 0.0f;  // lane i: token i's beta
-  if (t0 + (int32_t)lr < len)
-    b_t = a.beta[((int64_t)ck.row + t0 + lr) * a.beta_stride + h];
+  if (t0 + (int32_t)(lane & 7) < len)
+    b_t = a.beta[((int64_t)ck.row + t0 + (lane & 7)) * a.beta_stride + h];
   if (ck.off + t0 < 3) {  // taps from before the sequence's first row
 #pragma unroll
     for (int r = 0; r < 3; ++r) {
@@ -568,8 +558,8 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     }
   }
 
-  // y = silu(conv), two channels of 16 tokens a lane.
-  v2f y[3][16];
+  // y = silu(conv), two channels of 8 tokens a lane.
+  v2f y[3][8];
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
     const E* wt = static_cast<const E*>(a.conv_weight) +
@@ -577,190 +567,266 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     v2f w4[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w4[j] = v2f{(float)wt[j], (float)wt[j + 4]};
-    v2f x[19];
+    v2f x[11];
 #pragma unroll
-    for (int r = 0; r < 19; ++r) x[r] = widen<E>(raw[p][r]);
+    for (int r = 0; r < 11; ++r) x[r] = widen<E>(raw[p][r]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
       v2f s = w4[0] * x[i];
 #pragma unroll
       for (int j = 1; j < 4; ++j) s += w4[j] * x[i + j];
-      const bool live = t0 + i < len;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float e = __builtin_amdgcn_exp2f(s[c] * -1.44269504f);
-        y[p][i][c] = live ? s[c] * __builtin_amdgcn_rcpf(1.0f + e) : 0.0f;
+        y[p][i][c] = s[c] * __builtin_amdgcn_rcpf(1.0f + e);
       }
     }
   }
+  v2f av[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x0 = g0[i] > 0.0f ? 0.0f : g0[i], x1 = g1[i] > 0.0f ? 0.0f : g1[i];
+    av[i] = v2f{__builtin_amdgcn_exp2f(x0 * 1.44269504f), __builtin_amdgcn_exp2f(x1 * 1.44269504f)};
+  }
+  if (t0 + 8 > len) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (t0 + i >= len) {
+        y[0][i] = y[1][i] = y[2][i] = v2f{0.0f, 0.0f};
+        av[i] = v2f{1.0f, 1.0f};
+      }
+  }
 
-  // q and k over their norms: 32 sums at once, each lane's root goes to all.
+  // q and k over their norms (16 sums at once, each lane's root goes to all), times
+  // kUnit.
   {
-    float v[32];
+    float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
       v[i] = y[0][i][0] * y[0][i][0] + y[0][i][1] * y[0][i][1];
-      v[16 + i] = y[1][i][0] * y[1][i][0] + y[1][i][1] * y[1][i][1];
+      v[8 + i] = y[1][i][0] * y[1][i][0] + y[1][i][1] * y[1][i][1];
     }
-    const float by = 1.0f / sqrtf(sum32(v, lane) + a.eps);
+    const float by = kUnit / sqrtf(sum16(v, lane) + a.eps);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float nq = real((uint32_t)__builtin_amdgcn_readlane((int)bits(by), 2 * i));
-      const float nk = real((uint32_t)__builtin_amdgcn_readlane((int)bits(by), 32 + 2 * i));
+    for (int i = 0; i < 8; ++i) {
+      const float nq = real((uint32_t)__builtin_amdgcn_readlane((int)bits(by), 4 * i));
+      const float nk = real((uint32_t)__builtin_amdgcn_readlane((int)bits(by), 32 + 4 * i));
       y[0][i] *= nq;
       y[1][i] *= nk;
     }
   }
+  constexpr float kUnits = 1.0f / (kUnit * kUnit);
 
-  // The block's decays, and their products from its start (with the token) and
-  // to its end (without).
-  v2f up[16], down[16];
+  // Pairs within the wave's 8 tokens.  Columns s = b and 7 - b together give 16 sums;
+  // lane 4 n gets sum n.  M holds A (without beta) below its diagonal and P's transpose
+  // above: P_ts at [s][t + 1].
   {
-    v2f av[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const bool live = t0 + i < len;
-      const float x0 = g0[i] > 0.0f ? 0.0f : g0[i], x1 = g1[i] > 0.0f ? 0.0f : g1[i];
-      av[i][0] = live ? __builtin_amdgcn_exp2f(x0 * 1.44269504f) : 1.0f;
-      av[i][1] = live ? __builtin_amdgcn_exp2f(x1 * 1.44269504f) : 1.0f;
-    }
-    up[0] = av[0];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) up[i] = up[i - 1] * av[i];
-    down[15] = v2f{1.0f, 1.0f};
-#pragma unroll
-    for (int i = 14; i >= 0; --i) down[i] = down[i + 1] * av[i + 1];
-
-    // Pairs within the block.  Columns s = b and 15 - b together give 32 sums; lane
-    // 2 n gets sum n.  M holds A below its diagonal and P's transpose above: P_ts
-    // at [s][t + 1].
-    const uint32_t n = lane >> 1, m = n & 15;
+    const uint32_t n = lane >> 2, m = n & 7;
     float* const block = M + t0 * kMStride + t0;
     float* const waste = tmp + w * 8;
-    float acc[16];  // lane j: column j of sum_s A(i, s) x_s
+    float sums[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    float sums[8];
-#pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      float v[32];
+    for (int b = 0; b < 4; ++b) {
+      float v[16];
       v2f p = y[1][b];
+      v[b] = y[0][b][0] * p[0] + y[0][b][1] * p[1];
 #pragma unroll
-      for (int i = b; i < 16; ++i) {
-        if (i > b) {
-          p *= av[i];
-          v[i] = y[1][i][0] * p[0] + y[1][i][1] * p[1];
-          v[16 + i] = y[0][i][0] * p[0] + y[0][i][1] * p[1];
-        } else {
-          v[b] = y[0][b][0] * p[0] + y[0][b][1] * p[1];
-        }
+      for (int i = b + 1; i < 8; ++i) {
+        p *= av[i];
+        v[i] = y[1][i][0] * p[0] + y[1][i][1] * p[1];
+        v[8 + i] = y[0][i][0] * p[0] + y[0][i][1] * p[1];
       }
-      p = y[1][15 - b];
+      p = y[1][7 - b];
 #pragma unroll
-      for (int i = 15 - b; i < 16; ++i) {
-        const int k = i - (15 - b);
-        if (i > 15 - b) {
+      for (int k = 0; k <= b; ++k) {
+        const int i = 7 - b + k;
+        if (k > 0) {
           p *= av[i];
           v[k - 1] = y[1][i][0] * p[0] + y[1][i][1] * p[1];
         }
-        v[16 + k] = y[0][i][0] * p[0] + y[0][i][1] * p[1];
+        v[8 + k] = y[0][i][0] * p[0] + y[0][i][1] * p[1];
       }
-      const float sum = sum32(v, lane);
-      // n < b: A(16 - b + n, 15 - b); n = b: P(b, b); b < n < 16: A(n, b);
-      // 16 <= n <= 16 + b: P(15 - b + m, 15 - b); n > 16 + b: P(m, b).  Lanes with A write
-      // to where nobody reads.
-      sums[b] = sum;
-      const uint32_t to = n >= 16 ? (m > (uint32_t)b ? b * kMStride : (15 - b) * (kMStride + 1))
-                                  : b * kMStride;
-      (n >= 16 || m == (uint32_t)b ? block : waste)[to + m + 1] = sum;
+      sums[b] = sum16(v, lane) * kUnits;
+      // n < b: A(8 - b + n, 7 - b); n = b: P(b, b); b < n < 8: A(n, b);
+      // 8 <= n <= 8 + b: P(7 - b + m, 7 - b); n > 8 + b: P(m, b).  Lanes with A write to
+      // where nobody reads.
+      const uint32_t to = n >= 8 && m <= (uint32_t)b ? (7 - b) * (kMStride + 1) : b * kMStride;
+      (n >= 8 || m == (uint32_t)b ? block : waste)[to + m + 1] = sums[b];
     }
-    // (1 + A)^-1 of the block: lane j solves for column j, with A's values as scalars
-    // from the lanes that have them.
-    float x[16];
+    // (1 + A)^-1: lane j solves for column j, with A's values as scalars from the lanes
+    // that have them.
+    float acc[8], x[8];  // acc: sum_s A(i, s) x_s
 #pragma unroll
-    for (int s = 0; s < 16; ++s) {
+    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
       const float b_s = real((uint32_t)__builtin_amdgcn_readlane((int)bits(b_t), s));
-      x[s] = (lr == (uint32_t)s ? 1.0f : 0.0f) - b_s * acc[s];
+      x[s] = (lane == (uint32_t)s ? 1.0f : 0.0f) - b_s * acc[s];
 #pragma unroll
-      for (int i = s + 1; i < 16; ++i) {
-        // A(i, s): in sums[s] at i for s < 8, in sums[15 - s] at i - s - 1 otherwise
-        const int from = s < 8 ? i : i - s - 1;
+      for (int i = s + 1; i < 8; ++i) {
+        // A(i, s): in sums[s] at i for s < 4, in sums[7 - s] at i - s - 1 otherwise
+        const int from = s < 4 ? i : i - s - 1;
         const float as = real(
-            (uint32_t)__builtin_amdgcn_readlane((int)bits(sums[s < 8 ? s : 15 - s]), 2 * from));
+            (uint32_t)__builtin_amdgcn_readlane((int)bits(sums[s < 4 ? s : 7 - s]), 4 * from));
         acc[i] += as * x[s];
       }
-      __builtin_amdgcn_sched_barrier(0);  // a column's scalars at a time
     }
-    if (lane < 16) {
+    if (lane < 8) {
       beta[t0 + lane] = b_t;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 8; ++i)
         if (i >= (int)lane) block[i * kMStride + lane] = x[i];
     }
   }
 
-  // Totals of the block's decays, the largest values of its V.
+  // Decays of the 8 tokens: up to a token with it go to k and q, behind it to k.
+  v2f kr[8], kd[8], qr[8];
   {
-    *reinterpret_cast<v2f*>(total + w * kD + ch) = up[15];
-    v2f big = {0.0f, 0.0f};
+    v2f r = av[0];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      big[0] = fmaxf(big[0], fabsf(y[2][i][0]));
-      big[1] = fmaxf(big[1], fabsf(y[2][i][1]));
+    for (int i = 0; i < 8; ++i) {
+      if (i > 0) r *= av[i];
+      kr[i] = y[1][i] * r;
+      qr[i] = y[0][i] * r;
     }
-    *reinterpret_cast<v2f*>(most + w * kD + ch) = big;
+    *reinterpret_cast<v2f*>(total + w * kD + ch) = r;
+    r = v2f{1.0f, 1.0f};
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+      kd[i] = y[1][i] * r;
+      r *= av[i];
+    }
   }
 
-  // A row plane holds 16 tokens' channels of one term.
-  auto put_row = [&](uint32_t plane, const v2f (&x)[16], const v2f (&by)[16], v2f scale) {
-    uint8_t* const to = lds + plane * kRowPlane + ch * 2;
+  // A row plane holds 16 tokens' channels of one term; a wave has half of its rows.
+  auto put_row = [&](uint32_t at, uint32_t lo, const v2f (&x)[8], v2f by) {
+    uint8_t* const to = lds + at + ch * 2;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const v2f z = x[i] * by[i] * scale;
+    for (int i = 0; i < 8; ++i) {
+      const v2f z = x[i] * by;
       const Terms2 s = terms(z[0], z[1]);
       *reinterpret_cast<v2h*>(to + i * kRowStride) = s.hi;
-      *reinterpret_cast<v2h*>(to + kRowPlane + i * kRowStride) = s.lo;
+      *reinterpret_cast<v2h*>(to + lo + i * kRowStride) = s.lo;
     }
   };
-  auto get_row = [&](uint32_t plane, uint32_t kb) {
-    const uint8_t* const from = lds + plane * kRowPlane + lr * kRowStride + kb * 64 + lg * 16;
+  auto get_row = [&](uint32_t at, uint32_t lo, uint32_t row, uint32_t kb) {
+    const uint8_t* const from = lds + at + row * kRowStride + kb * 64 + lg * 16;
     Terms8 s;
     s.hi = *reinterpret_cast<const v8h*>(from);
-    s.lo = *reinterpret_cast<const v8h*>(from + kRowPlane);
+    s.lo = *reinterpret_cast<const v8h*>(from + lo);
     return s;
   };
-  const v2f unit = {kUnit, kUnit};
-  constexpr float kUnits = 1.0f / (kUnit * kUnit);
-  // A 16x16 tile of A (unscaled by beta) or of P's transpose goes to M.
-  auto put_m = [&](bool is_p, uint32_t row_block, uint32_t col_block, v4f x) {
+  const v2f one = {1.0f, 1.0f};
+  const uint32_t tile = w >> 1, late = w & 1;  // of the chunk's four tiles of 16 tokens
+  constexpr uint32_t kHalf = kRowPlane / 2;
+  // A 16x16 tile of A or of P's transpose goes to M.
+  auto put_m = [&](bool is_p, uint32_t row_tile, uint32_t col_tile, v4f x) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t row = row_block * 16 + lg * 4 + j, col = col_block * 16 + lr;
+      const uint32_t row = row_tile * 16 + lg * 4 + j, col = col_tile * 16 + lr;
       M[is_p ? col * kMStride + row + 1 : row * kMStride + col] = x[j] * kUnits;
     }
   };
 
-  // Blocks 1 x 0 and 3 x 2: decays meet at the later block's start.
-  {
-    const uint32_t pair = (w >> 1) * 6;
-    if (w & 1) {
-      put_row(pair + 2, y[1], up, unit);
-      put_row(pair + 4, y[0], up, unit);
-    } else {
-      put_row(pair, y[1], down, unit);
-    }
+  // Halves of 16 tokens: a tile's plane of k has the earlier half's columns in rows 0..7
+  // and the later's in 8..15, which meet at the later half's start: its product with
+  // itself has A in one quarter.  Behind the four planes' terms those of the later
+  // halves' q.
+  constexpr uint32_t kQ8 = 8 * kRowPlane;
+  if (late) {
+    put_row(tile * 2 * kRowPlane + kHalf, kRowPlane, kr, one);
+    put_row(kQ8 + tile * kRowPlane, kHalf, qr, one);
+  } else {
+    put_row(tile * 2 * kRowPlane, kRowPlane, kd, one);
   }
   __syncthreads();
   {
-    const uint32_t pair = w & 1, is_p = w >> 1;
     v4f acc[3] = {};  // by term: a sum waits for the one before
 #pragma unroll
-    for (uint32_t kb = 0; kb < kD / 32; ++kb)
-      mfma3(get_row(pair * 6 + 2 + 2 * is_p, kb), get_row(pair * 6, kb), acc);
-    put_m(is_p, 2 * pair + 1, 2 * pair, acc[0] + acc[1] + acc[2]);
-    wave_fence();
+    for (uint32_t kb = 0; kb < kD / 32; ++kb) {
+      const Terms8 k = get_row(tile * 2 * kRowPlane, kRowPlane, lr, kb);
+      if (late)
+        mfma3(get_row(kQ8 + tile * kRowPlane, kHalf, lr & 7, kb), k, acc);
+      else
+        mfma3(k, k, acc);
+    }
+    const v4f z = acc[0] + acc[1] + acc[2];
+    if (lg >= 2 && lr < 8) put_m(late, tile, tile, z);
     // T_10 = -T_11 (beta A_10 T_00), in fp32.
+    if (!late) {
+      wave_fence();
+      const uint32_t r0 = tile * 16 + 8, c0 = tile * 16;
+      float* const x = tmp + tile * 8 * kTmpStride;
+      v4f y2 = {};
+#pragma unroll
+      for (uint32_t kk = 0; kk < 2; ++kk) {
+        const uint32_t k = kk * 4 + lg;
+        const float p = lr < 8 ? M[(r0 + lr) * kMStride + c0 + k] : 0.0f;
+        const float q = lr < 8 && k >= lr ? M[(c0 + k) * kMStride + c0 + lr] : 0.0f;
+        y2 = __builtin_amdgcn_mfma_f32_16x16x4f32(p, q, y2, 0, 0, 0);
+      }
+      if (lg < 2 && lr < 8)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[(lg * 4 + j) * kTmpStride + lr] = y2[j] * beta[r0 + lg * 4 + j];
+      wave_fence();
+      y2 = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (uint32_t kk = 0; kk < 2; ++kk) {
+        const uint32_t k = kk * 4 + lg;
+        const float p = lr < 8 && k <= lr ? M[(r0 + lr) * kMStride + r0 + k] : 0.0f;
+        const float q = lr < 8 ? x[k * kTmpStride + lr] : 0.0f;
+        y2 = __builtin_amdgcn_mfma_f32_16x16x4f32(p, q, y2, 0, 0, 0);
+      }
+      if (lg < 2 && lr < 8)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) M[(r0 + lg * 4 + j) * kMStride + c0 + lr] = -y2[j];
+    }
+  }
+  // The products of the other blocks' decays between a token's block and where it is
+  // met: by halves of 16, 32 and 64 tokens, from the chunk's start, to its end.
+  v2f by32, by64, before, after;
+  {
+    auto of = [&](uint32_t b) { return *reinterpret_cast<const v2f*>(total + b * kD + ch); };
+    v2f left = one, right = one;  // of the tiles before and behind the wave's
+    v2f near = one;               // of the half's other tile, where it lies between
+#pragma unroll
+    for (uint32_t b = 0; b < 4; ++b) {
+      const v2f x = of(2 * b) * of(2 * b + 1);
+      if (b < tile) left *= x;
+      if (b > tile) right *= x;
+      if ((tile == 3 && b == 2) || (tile == 0 && b == 1)) near = x;
+    }
+    const v2f up = late ? of(w - 1) : one, down = late ? one : of(w + 1);
+    by32 = tile & 1 ? up : down;
+    by64 = (w >= 4 ? up : down) * near;
+    before = up * left;
+    after = down * right;
+    if (w == 0) *reinterpret_cast<v2f*>(rec + kRecDecay + ch * 4) = after * of(0);
+  }
+  __syncthreads();
+
+  // Halves of 32: tiles 1 x 0 and 3 x 2.
+  {
+    const uint32_t at = (w >> 2) * 6 * kRowPlane + late * kHalf;
+    if (tile & 1) {
+      put_row(at + 2 * kRowPlane, kRowPlane, kr, by32);
+      put_row(at + 4 * kRowPlane, kRowPlane, qr, by32);
+    } else {
+      put_row(at, kRowPlane, kd, by32);
+    }
+  }
+  __syncthreads();
+  if (w < 4) {
+    const uint32_t pair = w & 1, is_p = w >> 1;
+    v4f acc[3] = {};
+#pragma unroll
+    for (uint32_t kb = 0; kb < kD / 32; ++kb)
+      mfma3(get_row((pair * 6 + 2 + 2 * is_p) * kRowPlane, kRowPlane, lr, kb),
+            get_row(pair * 6 * kRowPlane, kRowPlane, lr, kb), acc);
+    put_m(is_p, 2 * pair + 1, 2 * pair, acc[0] + acc[1] + acc[2]);
     if (!is_p) {
+      wave_fence();
       const uint32_t r0 = pair * 32 + 16, c0 = pair * 32;
       float* const x = tmp + pair * 16 * kTmpStride;
       v4f y2[2] = {};
@@ -789,46 +855,31 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
       for (int j = 0; j < 4; ++j) M[(r0 + lg * 4 + j) * kMStride + c0 + lr] = -z[j];
     }
   }
-  // All blocks' totals, this lane's channels.
-  v2f tot[4];
-#pragma unroll
-  for (int b = 0; b < 4; ++b) tot[b] = *reinterpret_cast<const v2f*>(total + b * kD + ch);
   __syncthreads();
 
-  // Halves 1 x 0: decays meet at token 32.  Planes 0..3 hold the columns' blocks,
-  // 4..11 the rows'.
-  if (w >= 2) {
-    const v2f by = w == 3 ? tot[2] * unit : unit;
-    put_row(4 + (w - 2) * 4, y[1], up, by);
-    put_row(6 + (w - 2) * 4, y[0], up, by);
+  // Halves of 64.  Planes 0..3 hold the columns' tiles, 4..11 the rows'.
+  if (w >= 4) {
+    const uint32_t at = (4 + (tile - 2) * 4) * kRowPlane + late * kHalf;
+    put_row(at, kRowPlane, kr, by64);
+    put_row(at + 2 * kRowPlane, kRowPlane, qr, by64);
   } else {
-    put_row(w * 2, y[1], down, w == 0 ? tot[1] * unit : unit);
+    put_row(tile * 2 * kRowPlane + late * kHalf, kRowPlane, kd, by64);
   }
   __syncthreads();
   {
-    const uint32_t i = w >> 1, j = w & 1;
-    v4f ka[3] = {}, qa[3] = {};
+    const uint32_t is_p = w >> 2, i = (w >> 1) & 1, j = w & 1;
+    v4f acc[3] = {};
 #pragma unroll
-    for (uint32_t kb = 0; kb < kD / 32; ++kb) {
-      const Terms8 c = get_row(j * 2, kb);
-      mfma3(get_row(4 + i * 4, kb), c, ka);
-      mfma3(get_row(6 + i * 4, kb), c, qa);
-    }
-    put_m(false, 2 + i, j, ka[0] + ka[1] + ka[2]);
-    put_m(true, 2 + i, j, qa[0] + qa[1] + qa[2]);
+    for (uint32_t kb = 0; kb < kD / 32; ++kb)
+      mfma3(get_row((4 + i * 4 + is_p * 2) * kRowPlane, kRowPlane, lr, kb),
+            get_row(j * 2 * kRowPlane, kRowPlane, lr, kb), acc);
+    put_m(is_p, 2 + i, j, acc[0] + acc[1] + acc[2]);
   }
   __syncthreads();
 
-  // T_10 = -T_11 (beta A_10 T_00) of the halves, in fp32; meanwhile q R goes out.
-  const v2f before = w == 0   ? v2f{1.0f, 1.0f}
-                     : w == 1 ? tot[0]
-                     : w == 2 ? tot[0] * tot[1]
-                              : tot[0] * tot[1] * tot[2];
-  const v2f after = w == 3   ? v2f{1.0f, 1.0f}
-                    : w == 2 ? tot[3]
-                    : w == 1 ? tot[3] * tot[2]
-                             : tot[3] * tot[2] * tot[1];
-  {
+  // T_10 of the halves, in fp32; meanwhile q R (256 times itself) goes out.
+  put_row(tile * 2 * kRowPlane + late * kHalf, kRowPlane, qr, before * v2f{256.0f / kUnit, 256.0f / kUnit});
+  if (w < 4) {
     const uint32_t i = w >> 1, j = w & 1;
     v4f y2[2] = {};
 #pragma unroll
@@ -844,11 +895,9 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
       const uint32_t row = i * 16 + lg * 4 + n;
       tmp[row * kTmpStride + j * 16 + lr] = z[n] * beta[32 + row];
     }
-    const v2f by = before * v2f{256.0f, 256.0f};
-    put_row(w * 2, y[0], up, by);
   }
   __syncthreads();
-  {
+  if (w < 4) {
     const uint32_t i = w >> 1, j = w & 1;
     v4f y2[2] = {};
 #pragma unroll
@@ -861,73 +910,74 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     const v4f z = y2[0] + y2[1];
 #pragma unroll
     for (int n = 0; n < 4; ++n) M[(32 + i * 16 + lg * 4 + n) * kMStride + j * 16 + lr] = -z[n];
-    // q R (256 times itself), in the scan's order: wave w's token tile is w.
+  }
+  // q R in the scan's order: a wave has half of its tile's channels.
 #pragma unroll
-    for (uint32_t kb = 0; kb < kD / 32; ++kb) {
-      const uint8_t* const from = lds + w * 2 * kRowPlane + lr * kRowStride + kb * 64 + lg * 8;
-      uint8_t* const to = rec + kRecQ + (w * (kD / 32) + kb) * 2048 + lane * 16;
+  for (uint32_t k2 = 0; k2 < kD / 64; ++k2) {
+    const uint32_t kb = late * (kD / 64) + k2;
+    const uint8_t* const from = lds + tile * 2 * kRowPlane + lr * kRowStride + kb * 64 + lg * 8;
+    uint8_t* const to = rec + kRecQ + (tile * (kD / 32) + kb) * 2048 + lane * 16;
 #pragma unroll
-      for (uint32_t x = 0; x < 2; ++x) {
-        const v4h lo = *reinterpret_cast<const v4h*>(from + x * kRowPlane);
-        const v4h hi = *reinterpret_cast<const v4h*>(from + x * kRowPlane + 32);
-        *reinterpret_cast<v8h*>(to + x * 1024) = join(lo, hi);
+    for (uint32_t x = 0; x < 2; ++x) {
+      const v4h lo = *reinterpret_cast<const v4h*>(from + x * kRowPlane);
+      const v4h hi = *reinterpret_cast<const v4h*>(from + x * kRowPlane + 32);
+      *reinterpret_cast<v8h*>(to + x * 1024) = join(lo, hi);
+    }
+  }
+  // P (4096 times itself): tiles (0,0) (1,0) (2,0) (2,1) (3,0) (3,1) of 16 x 32.
+  if (w >= 2) {
+    const uint32_t part = w - 2, ti = part < 2 ? part : 1 + (part >> 1), kb = part < 2 ? 0 : part & 1;
+    const uint32_t row = ti * 16 + lr, s0 = kb * 32 + lg * 4;
+    v4f x[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const uint32_t s = s0 + half * 16 + n;
+        x[half][n] = s <= row ? M[s * kMStride + row + 1] * 4096.0f : 0.0f;
       }
-    }
-    // P (4096 times itself): tiles (0,0) (1,0) (2,0) (2,1) (3,0) (3,1) of 16 x 32.
-    for (uint32_t e = t; e < 6 * 64; e += kFormThreads) {
-      const uint32_t tile = e >> 6, ti = tile < 2 ? tile : 1 + (tile >> 1), kb = tile < 2 ? 0 : tile & 1;
-      const uint32_t l = e & 63, row = ti * 16 + (l & 15), s0 = kb * 32 + (l >> 4) * 4;
-      v4f x[2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint32_t s = s0 + half * 16 + n;
-          x[half][n] = s <= row ? M[s * kMStride + row + 1] * 4096.0f : 0.0f;
-        }
-      const Terms8 z = terms(x[0], x[1]);
-      uint8_t* const to = rec + kRecP + tile * 2048 + l * 16;
-      *reinterpret_cast<v8h*>(to) = z.hi;
-      *reinterpret_cast<v8h*>(to + 1024) = z.lo;
-    }
+    const Terms8 z = terms(x[0], x[1]);
+    uint8_t* const to = rec + kRecP + part * 2048 + lane * 16;
+    *reinterpret_cast<v8h*>(to) = z.hi;
+    *reinterpret_cast<v8h*>(to + 1024) = z.lo;
   }
   __syncthreads();
 
-  // T's terms (256 times itself) and k R, transposed: rows of 64 tokens.
+  // T's terms (256 times itself) and k R (kUnit times), transposed: rows of 64 tokens.
   uint8_t* const tok = lds + 2 * kTPlane;
-  auto put_tokens = [&](uint8_t* to, const v2f (&x)[16], const v2f* by, v2f scale) {
+  auto put_tokens = [&](uint8_t* to, const v2f (&x)[8], v2f scale) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        v4f z[2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = half * 8 + i;
-          z[i >> 2][i & 3] = x[k][c] * (by ? by[k][c] : 1.0f) * scale[c];
-        }
-        const Terms8 s = terms(z[0], z[1]);
-        uint8_t* const at = to + (ch + c) * kTokStride + t0 * 2 + half * 16;
-        *reinterpret_cast<v8h*>(at) = s.hi;
-        *reinterpret_cast<v8h*>(at + kTokPlane) = s.lo;
-      }
-  };
-  {
-    const uint32_t row = t >> 2, c0 = (t & 3) * 16;
-#pragma unroll
-    for (uint32_t part = 0; part < 2; ++part) {
+    for (int c = 0; c < 2; ++c) {
       v4f z[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t col = c0 + part * 8 + i;
-        z[i >> 2][i & 3] = col <= row ? M[row * kMStride + col] * beta[col] * 256.0f : 0.0f;
-      }
+      for (int i = 0; i < 8; ++i) z[i >> 2][i & 3] = x[i][c] * scale[c];
       const Terms8 s = terms(z[0], z[1]);
-      uint8_t* const at = lds + row * kTokStride + c0 * 2 + part * 16;
+      uint8_t* const at = to + (ch + c) * kTokStride + t0 * 2;
       *reinterpret_cast<v8h*>(at) = s.hi;
-      *reinterpret_cast<v8h*>(at + kTPlane) = s.lo;
+      *reinterpret_cast<v8h*>(at + kTokPlane) = s.lo;
     }
-    put_tokens(tok, y[1], up, before * unit);
+  };
+  {
+    const uint32_t row = t >> 3, c0 = (t & 7) * 8;
+    v4f z[2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t col = c0 + i;
+      z[i >> 2][i & 3] = col <= row ? M[row * kMStride + col] * beta[col] * 256.0f : 0.0f;
+    }
+    const Terms8 s = terms(z[0], z[1]);
+    uint8_t* const at = lds + row * kTokStride + c0 * 2;
+    *reinterpret_cast<v8h*>(at) = s.hi;
+    *reinterpret_cast<v8h*>(at + kTPlane) = s.lo;
+    put_tokens(tok, kr, before);
+    // V's largest values by the wave, over the totals, which all have read
+    v2f big = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      big[0] = fmaxf(big[0], fabsf(y[2][i][0]));
+      big[1] = fmaxf(big[1], fabsf(y[2][i][1]));
+    }
+    *reinterpret_cast<v2f*>(total + w * kD + ch) = big;
   }
   __syncthreads();
   auto get_t = [&](uint32_t ti, uint32_t kb) {
@@ -944,111 +994,107 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     s.lo = *reinterpret_cast<const v8h*>(from + kTokPlane);
     return s;
   };
+  // Two channel tiles and two token tiles a wave: 0 and 3, or 1 and 2 (tiles 0 and 1
+  // have no tokens past 32 before them).
+  const uint32_t pair = w >> 1, ta = late, tb = 3 - late;
   {
-    // -W (256 times itself): its transpose's tiles, channels 32 w .. 32 w + 31.
-    Terms8 k[2][2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) k[c][kb] = get_tok(w * 2 + c, kb);
-    v4f z[4][2] = {};
+    // -W (256 times itself): its transpose's tiles.
+    v4f z[2][2] = {};
 #pragma unroll
     for (uint32_t kb = 0; kb < 2; ++kb) {
-      Terms8 x[4];
+      Terms8 k[2];
 #pragma unroll
-      for (uint32_t ti = kb * 2; ti < 4; ++ti) x[ti] = get_t(ti, kb);
+      for (uint32_t c = 0; c < 2; ++c) k[c] = get_tok(pair * 2 + c, kb);
+      const Terms8 xa = get_t(ta, 0), xb = get_t(tb, kb);
 #pragma unroll
       for (int term = 0; term < 3; ++term)
 #pragma unroll
-        for (uint32_t ti = kb * 2; ti < 4; ++ti)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            z[ti][c] = mfma(term == 0 ? k[c][kb].lo : k[c][kb].hi,
-                            term == 1 ? x[ti].lo : x[ti].hi, z[ti][c]);
+        for (int c = 0; c < 2; ++c) {
+          const v8h left = term == 0 ? k[c].lo : k[c].hi;
+          if (kb == 0) z[0][c] = mfma(left, term == 1 ? xa.lo : xa.hi, z[0][c]);
+          z[1][c] = mfma(left, term == 1 ? xb.lo : xb.hi, z[1][c]);
+        }
     }
 #pragma unroll
-    for (uint32_t ti = 0; ti < 4; ++ti) {
-      const Terms8 s = terms(z[ti][0] * (-1.0f / kUnit), z[ti][1] * (-1.0f / kUnit));
-      uint8_t* const to = rec + kRecW + (ti * (kD / 32) + w) * 2048 + lane * 16;
+    for (uint32_t x = 0; x < 2; ++x) {
+      const Terms8 s = terms(z[x][0] * (-1.0f / kUnit), z[x][1] * (-1.0f / kUnit));
+      uint8_t* const to = rec + kRecW + ((x ? tb : ta) * (kD / 32) + pair) * 2048 + lane * 16;
       *reinterpret_cast<v8h*>(to) = s.hi;
       *reinterpret_cast<v8h*>(to + 1024) = s.lo;
     }
   }
-  __syncthreads();
   // V, each column scaled by 2^e to have its largest value in [2^8, 2^9).
+  int32_t e[2];
   {
-    int32_t e[2];
+    v2f big = {0.0f, 0.0f};
+#pragma unroll
+    for (uint32_t b = 0; b < 8; ++b) {
+      const v2f x = *reinterpret_cast<const v2f*>(total + b * kD + ch);
+      big[0] = fmaxf(big[0], x[0]);
+      big[1] = fmaxf(big[1], x[1]);
+    }
     v2i top;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float big = most[ch + c];
+      top[c] = big[c] > 0.0f ? __builtin_amdgcn_frexp_expf(big[c]) : -1000;
+      e[c] = big[c] > 0.0f ? 9 - top[c] : 0;
 #pragma unroll
-      for (uint32_t b = 1; b < 4; ++b) big = fmaxf(big, most[b * kD + ch + c]);
-      top[c] = big > 0.0f ? __builtin_amdgcn_frexp_expf(big) : -1000;
-      e[c] = big > 0.0f ? 9 - top[c] : 0;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[2][i][c] = __builtin_ldexpf(y[2][i][c], e[c]);
+      for (int i = 0; i < 8; ++i) y[2][i][c] = __builtin_ldexpf(y[2][i][c], e[c]);
     }
-    put_tokens(tok, y[2], nullptr, v2f{1.0f, 1.0f});
-    if (w == 0) {
-      *reinterpret_cast<v2f*>(rec + kRecDecay + ch * 4) = tot[0] * tot[1] * tot[2] * tot[3];
-      exps[ch] = e[0];
-      exps[ch + 1] = e[1];
-      *reinterpret_cast<v2i*>(rec + kRecExps + ch * 4) = top;
-    }
+    if (w == 0) *reinterpret_cast<v2i*>(rec + kRecExps + ch * 4) = top;
+  }
+  __syncthreads();
+  int32_t* const exps = reinterpret_cast<int32_t*>(tmp);
+  put_tokens(tok, y[2], one);
+  if (w == 0) {
+    exps[ch] = e[0];
+    exps[ch + 1] = e[1];
   }
   __syncthreads();
   {
-    Terms8 v[2][2];
-#pragma unroll
-    for (uint32_t c = 0; c < 2; ++c)
-#pragma unroll
-      for (uint32_t kb = 0; kb < 2; ++kb) v[c][kb] = get_tok(w * 2 + c, kb);
-    v4f z[4][2] = {};
+    v4f z[2][2] = {};
 #pragma unroll
     for (uint32_t kb = 0; kb < 2; ++kb) {
-      Terms8 x[4];
+      Terms8 v[2];
 #pragma unroll
-      for (uint32_t ti = kb * 2; ti < 4; ++ti) x[ti] = get_t(ti, kb);
+      for (uint32_t c = 0; c < 2; ++c) v[c] = get_tok(pair * 2 + c, kb);
+      const Terms8 xa = get_t(ta, 0), xb = get_t(tb, kb);
 #pragma unroll
       for (int term = 0; term < 3; ++term)
 #pragma unroll
-        for (uint32_t ti = kb * 2; ti < 4; ++ti)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            z[ti][c] = mfma(term == 0 ? x[ti].lo : x[ti].hi,
-                            term == 1 ? v[c][kb].lo : v[c][kb].hi, z[ti][c]);
+        for (int c = 0; c < 2; ++c) {
+          const v8h right = term == 1 ? v[c].lo : v[c].hi;
+          if (kb == 0) z[0][c] = mfma(term == 0 ? xa.lo : xa.hi, right, z[0][c]);
+          z[1][c] = mfma(term == 0 ? xb.lo : xb.hi, right, z[1][c]);
+        }
     }
 #pragma unroll
     for (uint32_t c = 0; c < 2; ++c) {
-      const uint32_t tile = w * 2 + c;
-      const int32_t back = -8 - exps[tile * 16 + lr];  // T is 256 times itself
+      const uint32_t ct = pair * 2 + c;
+      const int32_t back = -8 - exps[ct * 16 + lr];  // T is 256 times itself
 #pragma unroll
-      for (uint32_t ti = 0; ti < 4; ++ti) {
+      for (uint32_t x = 0; x < 2; ++x) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) z[ti][c][n] = __builtin_ldexpf(z[ti][c][n], back);
-        *reinterpret_cast<v4f*>(rec + kRecU + (tile * 4 + ti) * 1024 + lane * 16) = z[ti][c];
+        for (int n = 0; n < 4; ++n) z[x][c][n] = __builtin_ldexpf(z[x][c][n], back);
+        *reinterpret_cast<v4f*>(rec + kRecU + (ct * 4 + (x ? tb : ta)) * 1024 + lane * 16) = z[x][c];
       }
     }
   }
   __syncthreads();
   // k D_64 (16 times itself), over T's planes too.
-  put_tokens(lds, y[1], down, after * v2f{16.0f, 16.0f});
+  put_tokens(lds, kd, after * v2f{16.0f / kUnit, 16.0f / kUnit});
   __syncthreads();
 #pragma unroll
-  for (uint32_t c = 0; c < 2; ++c)
+  for (uint32_t kb = 0; kb < 2; ++kb) {
+    const uint8_t* const from = lds + (w * 16 + lr) * kTokStride + kb * 64 + lg * 8;
+    uint8_t* const to = rec + kRecK + (w * 2 + kb) * 2048 + lane * 16;
 #pragma unroll
-    for (uint32_t kb = 0; kb < 2; ++kb) {
-      const uint32_t tile = w * 2 + c;
-      const uint8_t* const from = lds + (tile * 16 + lr) * kTokStride + kb * 64 + lg * 8;
-      uint8_t* const to = rec + kRecK + (tile * 2 + kb) * 2048 + lane * 16;
-#pragma unroll
-      for (uint32_t x = 0; x < 2; ++x) {
-        const v4h lo = *reinterpret_cast<const v4h*>(from + x * kTokPlane);
-        const v4h hi = *reinterpret_cast<const v4h*>(from + x * kTokPlane + 32);
-        *reinterpret_cast<v8h*>(to + x * 1024) = join(lo, hi);
-      }
+    for (uint32_t x = 0; x < 2; ++x) {
+      const v4h lo = *reinterpret_cast<const v4h*>(from + x * kTokPlane);
+      const v4h hi = *reinterpret_cast<const v4h*>(from + x * kTokPlane + 32);
+      *reinterpret_cast<v8h*>(to + x * 1024) = join(lo, hi);
     }
+  }
 }
 
 // A sequence's chunks in order, kCt x 16 columns of a head's state a workgroup of four
@@ -1433,7 +1479,7 @@ HKV_TOKENS_DIMS(fp32, Fp32)
       scan<T, tiles>(a, pair / a.heads, pair % a.heads, blockIdx.x / 8 % kGroups, lds);     \
   }
 #define HKV_CHUNKS(suffix, T)                                                               \
-  extern "C" __global__ __launch_bounds__(kFormThreads, 2) void hkv_kda_form_##suffix(      \
+  extern "C" __global__ __launch_bounds__(kFormThreads, 4) void hkv_kda_form_##suffix(      \
       hkv::PrefillArgs a) {                                                                 \
     __shared__ __attribute__((aligned(16))) uint8_t lds[kFormLds];                          \
     const uint32_t slot = blockIdx.x / a.heads;                                             \
