@@ -467,13 +467,9 @@ constexpr uint32_t kRecDecay = kRecU + (kD / 16) * 4 * 1024;
 constexpr uint32_t kRecExps = kRecDecay + kD * 4;
 static_assert(kRecExps + kD * 4 == hkv::kPrefillRecord, "the workspace holds a record");
 
-// Two channels of one row.
-struct __attribute__((packed, aligned(2))) Pair16 {
-  uint32_t v;
-};
-struct __attribute__((packed, aligned(4))) Pair32 {
-  float x, y;
-};
+// Two channels of one row, aligned as one.
+typedef uint32_t pair16 __attribute__((aligned(2)));
+typedef float pair32 __attribute__((ext_vector_type(2), aligned(4)));
 
 template <class E>
 __device__ __forceinline__ v2f widen(uint32_t x) {
@@ -525,15 +521,15 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
   for (int r = 0; r < 11; ++r) {
     const int32_t o = min(t0 + r - 3, len - 1);
     const int64_t row = (int64_t)ck.row + (ck.off + o < 0 ? 0 : o);
-    const E* x = static_cast<const E*>(a.x) + row * a.x_stride;
+    const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.x_stride + (uint64_t)h * kD;
 #pragma unroll
     for (int p = 0; p < 3; ++p)
-      raw[p][r] = reinterpret_cast<const Pair16*>(x + ((uint64_t)p * a.heads + h) * kD + ch)->v;
+      raw[p][r] = *(const HKV_GLOBAL pair16*)((const HKV_GLOBAL uint8_t*)(x + (uint64_t)p * a.heads * kD) + lane * 4);
     if (r >= 3) {
-      const Pair32 g = *reinterpret_cast<const Pair32*>(
-          a.log_decay + row * a.decay_stride + (uint64_t)h * kD + ch);
-      g0[r - 3] = g.x;
-      g1[r - 3] = g.y;
+      const v2f g = *(const HKV_GLOBAL pair32*)(
+          (const HKV_GLOBAL uint8_t*)(a.log_decay + row * a.decay_stride + (uint64_t)h * kD) + lane * 8);
+      g0[r - 3] = g[0];
+      g1[r - 3] = g[1];
     }
   }
   float b_t = 0.0f;  // lane i: token i's beta
@@ -1117,8 +1113,8 @@ struct ScanShared {
 // At a uniform address and a lane's offset.
 __device__ __forceinline__ Terms8 read_terms(const uint8_t* p, uint32_t at) {
   Terms8 t;
-  t.hi = *(const HKV_GLOBAL v8h*)(p + at);
-  t.lo = *(const HKV_GLOBAL v8h*)(p + 1024 + at);
+  t.hi = *(const HKV_GLOBAL v8h*)((const HKV_GLOBAL uint8_t*)p + at);
+  t.lo = *(const HKV_GLOBAL v8h*)((const HKV_GLOBAL uint8_t*)p + 1024 + at);
   return t;
 }
 
