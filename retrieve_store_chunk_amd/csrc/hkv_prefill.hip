@@ -452,9 +452,10 @@ static_assert(12 * kRowPlane <= kOffM && kFormLds <= 80 * 1024, "two workgroups 
 
 // One chunk's result in the workspace, as the scan's lanes load it (1 KiB for 64
 // lanes of 16 bytes; lane l: row or column l % 16, group g = l / 16).
-//   W, Q   [token tile][32 channels][hi, lo]: 8 channels 4 g + 0..3 and 16 + 4 g + 0..3
-//   K      [channel tile][32 tokens][hi, lo]: 8 tokens in the same order
-//   P      [tile of 16 x 32 tokens][hi, lo]
+//   W, Q   [token tile][32 channels][hi, lo]: 8 channels 4 g + 0..3 and 16 + 4 g + 0..3,
+//          where a 16x16 product leaves two tiles of the state
+//   K      [channel tile][32 tokens][hi, lo]: 8 tokens 8 g + 0..7
+//   P      [tile of 16 x 32 tokens][hi, lo]: the same
 //   U0     [channel tile][token tile]: 4 tokens 4 g + 0..3, fp32
 //   decay  [channel], fp32
 //   exps   [channel]: V's largest value is below 2^exps; -1000: V is zero
@@ -477,8 +478,6 @@ __device__ __forceinline__ v2f widen(uint32_t x) {
   return __builtin_convertvector(__builtin_bit_cast(pair, x), v2f);
 }
 
-// The scan's order of a 32-row block's rows: lane group g's eight are 4 g + 0..3 and
-// 16 + 4 g + 0..3, since that is where a 16x16 product leaves two tiles.
 __device__ __forceinline__ v8h join(v4h a, v4h b) {
   return v8h{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
@@ -781,7 +780,7 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
   }
   // The products of the other blocks' decays between a token's block and where it is
   // met: by halves of 16, 32 and 64 tokens, from the chunk's start, to its end.
-  v2f by32, by64, before, after;
+  v2f by32, by64, before;
   {
     auto of = [&](uint32_t b) { return *reinterpret_cast<const v2f*>(total + b * kD + ch); };
     v2f left = one, right = one;  // of the tiles before and behind the wave's
@@ -797,8 +796,21 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
     by32 = tile & 1 ? up : down;
     by64 = (w >= 4 ? up : down) * near;
     before = up * left;
-    after = down * right;
+    const v2f after = down * right;
     if (w == 0) *reinterpret_cast<v2f*>(rec + kRecDecay + ch * 4) = after * of(0);
+    // k D_64 (16 times itself): a lane has 8 tokens of its two channels, as the scan
+    // takes them.
+    const v2f by = after * v2f{16.0f / kUnit, 16.0f / kUnit};
+    uint8_t* const to = rec + kRecK + (lane >> 3) * 4096 + (w >> 2) * 2048 + (w & 3) * 256;
+#pragma unroll
+    for (uint32_t c = 0; c < 2; ++c) {
+      v4f z[2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i >> 2][i & 3] = kd[i][c] * by[c];
+      const Terms8 x = terms(z[0], z[1]);
+      *reinterpret_cast<v8h*>(to + ((ch + c) & 15) * 16) = x.hi;
+      *reinterpret_cast<v8h*>(to + ((ch + c) & 15) * 16 + 1024) = x.lo;
+    }
   }
   __syncthreads();
 
@@ -923,15 +935,11 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
   // P (4096 times itself): tiles (0,0) (1,0) (2,0) (2,1) (3,0) (3,1) of 16 x 32.
   if (w >= 2) {
     const uint32_t part = w - 2, ti = part < 2 ? part : 1 + (part >> 1), kb = part < 2 ? 0 : part & 1;
-    const uint32_t row = ti * 16 + lr, s0 = kb * 32 + lg * 4;
+    const uint32_t row = ti * 16 + lr, s0 = kb * 32 + lg * 8;
     v4f x[2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const uint32_t s = s0 + half * 16 + n;
-        x[half][n] = s <= row ? M[s * kMStride + row + 1] * 4096.0f : 0.0f;
-      }
+    for (int n = 0; n < 8; ++n)
+      x[n >> 2][n & 3] = s0 + n <= row ? M[(s0 + n) * kMStride + row + 1] * 4096.0f : 0.0f;
     const Terms8 z = terms(x[0], x[1]);
     uint8_t* const to = rec + kRecP + part * 2048 + lane * 16;
     *reinterpret_cast<v8h*>(to) = z.hi;
@@ -1074,21 +1082,6 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
         for (int n = 0; n < 4; ++n) z[x][c][n] = __builtin_ldexpf(z[x][c][n], back);
         *reinterpret_cast<v4f*>(rec + kRecU + (ct * 4 + (x ? tb : ta)) * 1024 + lane * 16) = z[x][c];
       }
-    }
-  }
-  __syncthreads();
-  // k D_64 (16 times itself), over T's planes too.
-  put_tokens(lds, kd, after * v2f{16.0f / kUnit, 16.0f / kUnit});
-  __syncthreads();
-#pragma unroll
-  for (uint32_t kb = 0; kb < 2; ++kb) {
-    const uint8_t* const from = lds + (w * 16 + lr) * kTokStride + kb * 64 + lg * 8;
-    uint8_t* const to = rec + kRecK + (w * 2 + kb) * 2048 + lane * 16;
-#pragma unroll
-    for (uint32_t x = 0; x < 2; ++x) {
-      const v4h lo = *reinterpret_cast<const v4h*>(from + x * kTokPlane);
-      const v4h hi = *reinterpret_cast<const v4h*>(from + x * kTokPlane + 32);
-      *reinterpret_cast<v8h*>(to + x * 1024) = join(lo, hi);
     }
   }
 }
@@ -1312,8 +1305,10 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
     for (uint32_t ct = 0; ct < kCt; ++ct) {
       u[ct] *= 1.0f / 4096.0f;
       const Terms2 x = terms(u[ct][0], u[ct][1]), y = terms(u[ct][2], u[ct][3]);
-      v4h* const hi = reinterpret_cast<v4h*>(&lds.u[ct][w >> 1][0][lane]) + (w & 1);
-      v4h* const lo = reinterpret_cast<v4h*>(&lds.u[ct][w >> 1][1][lane]) + (w & 1);
+      // tokens 16 w + 4 g + 0..3: half of the 8 that group 2 (w % 2) + g / 2 takes
+      const uint32_t to = lr + 32 * (w & 1) + 16 * (lg >> 1);
+      v4h* const hi = reinterpret_cast<v4h*>(&lds.u[ct][w >> 1][0][to]) + (lg & 1);
+      v4h* const lo = reinterpret_cast<v4h*>(&lds.u[ct][w >> 1][1][to]) + (lg & 1);
       *hi = v4h{x.hi[0], x.hi[1], y.hi[0], y.hi[1]};
       *lo = v4h{x.lo[0], x.lo[1], y.lo[0], y.lo[1]};
     }
