@@ -231,6 +231,10 @@ constexpr uint32_t kPrefillRecord = 3 * 32768 + 12288 + 32768 + 1024;  // bytes 
 // launch for them where it has chunks).
 constexpr uint32_t kPrefillShort = 8;
 
+// Up to so many sequences are looked through by every workgroup of the token-by-token
+// kernel itself: a launch less.
+constexpr uint32_t kPrefillLookThrough = 256;
+
 struct PrefillChunk {
   int32_t seq, row, len, off;  // its first token: row of the call, token of the sequence
   int32_t dst;                 // the block that its last token's state goes to, or none
@@ -258,6 +262,7 @@ struct PrefillArgs {
   float scale, eps;
   uint32_t num_blocks, block_tokens, max_blocks, n_seqs, n_tokens, max_seq_tokens;
   uint32_t heads, head_dim, taps;
+  uint32_t planned;         // a launch of its own looks the sequences through
   uint32_t chunked;         // sequences of more than short_tokens are computed in chunks
   uint32_t short_tokens;
   uint32_t max_chunks;

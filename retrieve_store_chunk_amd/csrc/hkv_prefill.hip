@@ -76,54 +76,64 @@ __device__ __forceinline__ uint32_t chunks_of(const hkv::PrefillArgs& a, const S
          (rest % a.block_tokens + kC - 1) / kC;
 }
 
-// What becomes of each sequence (hkv.h), one workgroup each.  Blocks are compared
-// with those of all sequences: entries are few (a block holds hundreds of tokens).
-__device__ __forceinline__ void plan(const hkv::PrefillArgs& a) {
-  __shared__ int32_t most;
-  __shared__ uint32_t refused, before;
-  const uint32_t s = blockIdx.x, t = threadIdx.x;
-  if (t == 0) {
-    most = INT32_MIN;
-    refused = before = 0;
+// What a thread finds against sequence s, which shares the other sequences and the
+// sequence's blocks among a workgroup's threads: 1: its rows may be another's, 2: it is
+// refused.  Blocks are compared with those of all sequences: entries are few (a block
+// holds hundreds of tokens).
+__device__ __forceinline__ uint32_t look_through(const hkv::PrefillArgs& a, uint32_t s,
+                                                 const Span& me, uint32_t t, uint32_t threads) {
+  uint32_t found = 0;
+  for (uint32_t r = t; r < s; r += threads) found |= a.starts[r] > me.row ? 1u : 0u;
+  const int32_t* own = a.table + (int64_t)s * a.table_stride;
+  if (!me.blocks || me.tokens > (int32_t)a.max_seq_tokens || outside(a.src[s], a.num_blocks))
+    return found | 2u;
+  bool bad = false;
+  for (uint32_t j = me.first + t; j <= me.last; j += threads) {
+    const int32_t id = own[j];
+    bad |= outside(id, a.num_blocks);
+    for (uint32_t i = me.first; i < j; ++i) bad |= id >= 0 && own[i] == id;
   }
+  for (uint32_t r = t; r < a.n_seqs; r += threads) {
+    if (r == s) continue;
+    const Span p = span_of(a, r);
+    if (p.tokens == 0) continue;
+    const int32_t from = a.src[r];
+    const int32_t* theirs = a.table + (int64_t)r * a.table_stride;
+    for (uint32_t j = me.first; j <= me.last; ++j) {
+      const int32_t id = own[j];
+      if (id < 0) continue;
+      bad |= id == from;
+      if (p.blocks)
+        for (uint32_t i = p.first; i <= p.last; ++i) bad |= theirs[i] == id;
+    }
+  }
+  return found | (bad ? 2u : 0u);
+}
+
+// What becomes of a sequence (hkv.h), from what its threads found.
+__device__ __forceinline__ int32_t verdict(const Span& me, uint32_t found) {
+  if (!me.known || me.tokens == 0 || (found & 1)) return hkv::kPrefillNoRows;
+  return found & 2 ? hkv::kPrefillRefused : hkv::kPrefillRuns;
+}
+
+// The verdict on each sequence and its chunks, one workgroup each.
+__device__ __forceinline__ void plan(const hkv::PrefillArgs& a) {
+  __shared__ uint32_t found, before;
+  const uint32_t s = blockIdx.x, t = threadIdx.x;
+  if (t == 0) found = before = 0;
   __syncthreads();
   const Span me = span_of(a, s);
-  int32_t top = INT32_MIN;  // starts decrease somewhere before: the rows may be another's
-  for (uint32_t r = t; r < s; r += kPlanThreads) top = max(top, a.starts[r]);
-  if (top > INT32_MIN) atomicMax(&most, top);
   const int32_t* own = a.table + (int64_t)s * a.table_stride;
-  const int32_t src = a.src[s];
-  bool bad = !me.blocks || me.tokens > (int32_t)a.max_seq_tokens || outside(src, a.num_blocks);
-  if (!bad) {
-    for (uint32_t j = me.first + t; j <= me.last; j += kPlanThreads) {
-      const int32_t id = own[j];
-      bad |= outside(id, a.num_blocks);
-      for (uint32_t i = me.first; i < j; ++i) bad |= id >= 0 && own[i] == id;
-    }
-    for (uint32_t r = t; r < a.n_seqs; r += kPlanThreads) {
-      if (r == s) continue;
-      const Span p = span_of(a, r);
-      if (p.tokens == 0) continue;
-      const int32_t from = a.src[r];
-      const int32_t* theirs = a.table + (int64_t)r * a.table_stride;
-      for (uint32_t j = me.first; j <= me.last; ++j) {
-        const int32_t id = own[j];
-        if (id < 0) continue;
-        bad |= id == from;
-        if (p.blocks)
-          for (uint32_t i = p.first; i <= p.last; ++i) bad |= theirs[i] == id;
-      }
-    }
-  }
-  if (bad) atomicOr(&refused, 1u);
+  const uint32_t mine_found = look_through(a, s, me, t, kPlanThreads);
+  if (mine_found) atomicOr(&found, mine_found);
   uint32_t mine = 0;  // chunks of the sequences before
   if (a.chunked)
     for (uint32_t r = t; r < s; r += kPlanThreads) mine += chunks_of(a, span_of(a, r));
   if (mine) atomicAdd(&before, mine);
   __syncthreads();
-  const bool rows = me.known && me.tokens > 0 && most <= me.row;
-  if (t == 0)
-    a.status[s] = !rows ? hkv::kPrefillNoRows : refused ? hkv::kPrefillRefused : hkv::kPrefillRuns;
+  const int32_t status = verdict(me, found);
+  const bool rows = status != hkv::kPrefillNoRows;
+  if (t == 0) a.status[s] = status;
   if (!a.chunked) return;
   // Starts that go backwards can give more chunks than the workspace has records
   // for: the first sequence that does not fit leaves its part of them empty.
@@ -140,7 +150,7 @@ __device__ __forceinline__ void plan(const hkv::PrefillArgs& a) {
     for (uint32_t c = first + t; c < a.max_chunks; c += kPlanThreads)
       a.chunks[c] = hkv::PrefillChunk{};
   // A chunk of a sequence that does not run is empty.
-  const bool runs = rows && !refused;
+  const bool runs = status == hkv::kPrefillRuns;
   const uint32_t lead = chunk_lead(a, me), lead_chunks = (lead + kC - 1) / kC;
   const uint32_t per = (a.block_tokens + kC - 1) / kC;
   for (uint32_t c = t; c < count; c += kPlanThreads) {
@@ -179,19 +189,16 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
   __shared__ float y[2][3][kDim];  // q, k, v after the conv
   __shared__ float decay[2][kDim];
   __shared__ v4f sums[2][kWaves][kRowThreads];
+  __shared__ uint32_t found[kWaves];
   const uint32_t h = blockIdx.x, s = blockIdx.y, t = threadIdx.x, lane = t & 63;
   const uint32_t c = t % kRowThreads, r0 = t / kRowThreads;
-  const int32_t status = a.status[s];
-  if (status == hkv::kPrefillNoRows) return;
-  const int32_t row0 = a.starts[s], n = a.starts[s + 1] - row0;
+  const int32_t row0 = a.starts[s];
+  int32_t n = a.starts[s + 1] - row0;
   if (a.chunked && n > (int32_t)a.short_tokens) return;
   E* const out = static_cast<E*>(a.out) + (int64_t)row0 * a.out_stride + (int64_t)h * kDim + c * 4;
-  if (status == hkv::kPrefillRefused) {
-    for (uint32_t i = r0; i < (uint32_t)n; i += kGroups)
-      T::store4(out + (int64_t)i * a.out_stride, v4f{NAN, NAN, NAN, NAN});
-    return;
-  }
-  const int32_t src = a.src[s], position = a.positions[s];
+  const int32_t position = a.positions[s];
+  int32_t src = a.src[s];
+  if (outside(src, a.num_blocks)) src = HKV_NULL_BLOCK;  // until the verdict below
   const int32_t* const table = a.table + (int64_t)s * a.table_stride;
   const uint64_t state_off = a.conv_bytes + (uint64_t)h * kDim * kDim * 4;
   const uint32_t state_at = r0 * kRowThreads + c;  // in units of four values
@@ -207,6 +214,27 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
       st[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
       if (src >= 0) st[i] = p[i * kGroups * kRowThreads];
     }
+  }
+  // The verdict on the sequence, while its state is under way.
+  int32_t status;
+  if (a.planned) {
+    status = a.status[s];
+  } else {
+    const Span me = span_of(a, s);
+    const uint32_t mine = look_through(a, s, me, t, kThreads);
+    const uint32_t all = (__any(mine & 1) ? 1u : 0u) | (__any(mine & 2) ? 2u : 0u);
+    if (lane == 0) found[t >> 6] = all;
+    __syncthreads();
+    uint32_t any = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kWaves; ++w) any |= found[w];
+    status = verdict(me, any);
+  }
+  if (status == hkv::kPrefillNoRows) return;
+  if (status == hkv::kPrefillRefused) {
+    for (uint32_t i = r0; i < (uint32_t)n; i += kGroups)
+      T::store4(out + (int64_t)i * a.out_stride, v4f{NAN, NAN, NAN, NAN});
+    return;
   }
   // One thread per channel: its weights, its last `keep` values (oldest first).
   E taps[kChannels][hkv::kKdaMaxKernel - 1];
@@ -226,15 +254,33 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
       taps[i][j] = j < keep && src >= 0 ? old[j] : (E)0.0f;
   }
 
-  for (int32_t m = 0; m < n; ++m) {
+  // A token's inputs are fetched while the one before is computed.
+  constexpr uint32_t kDecays = (kDim + kThreads - 1) / kThreads;
+  E x_next[kChannels];
+  float g_next[kDecays], beta_next;
+  auto fetch = [&](int32_t m) {
     const int64_t row = (int64_t)row0 + m;
-    const uint32_t b = m & 1;
 #pragma unroll
     for (uint32_t i = 0; i < kChannels; ++i) {
       const uint32_t w = t + i * kThreads;
       if (w >= 3 * kDim) break;
       const uint64_t ch = ((uint64_t)(w / kDim) * a.heads + h) * kDim + w % kDim;
-      const E x = static_cast<const E*>(a.x)[row * a.x_stride + (int64_t)ch];
+      x_next[i] = static_cast<const E*>(a.x)[row * a.x_stride + (int64_t)ch];
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kDecays; ++i)
+      if (t + i * kThreads < kDim)
+        g_next[i] = a.log_decay[row * a.decay_stride + (int64_t)h * kDim + t + i * kThreads];
+    beta_next = a.beta[row * a.beta_stride + h];
+  };
+  fetch(0);
+  for (int32_t m = 0; m < n; ++m) {
+    const uint32_t b = m & 1;
+#pragma unroll
+    for (uint32_t i = 0; i < kChannels; ++i) {
+      const uint32_t w = t + i * kThreads;
+      if (w >= 3 * kDim) break;
+      const E x = x_next[i];
       float sum = 0.0f;
 #pragma unroll
       for (uint32_t j = 0; j + 1 < hkv::kKdaMaxKernel; ++j)
@@ -249,11 +295,12 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
       }
       y[b][w / kDim][w % kDim] = sum / (1.0f + expf(-sum));
     }
-    for (uint32_t i = t; i < kDim; i += kThreads) {
-      const float g = a.log_decay[row * a.decay_stride + (int64_t)h * kDim + i];
-      decay[b][i] = expf(g > 0.0f ? 0.0f : g);
-    }
-    const float beta = a.beta[row * a.beta_stride + h];
+#pragma unroll
+    for (uint32_t i = 0; i < kDecays; ++i)
+      if (t + i * kThreads < kDim)
+        decay[b][t + i * kThreads] = expf(g_next[i] > 0.0f ? 0.0f : g_next[i]);
+    const float beta = beta_next;
+    if (m + 1 < n) fetch(m + 1);
     __syncthreads();
 
     // |q|^2, |k|^2 and q.k, by every wave for itself.
@@ -1500,8 +1547,10 @@ int launch_prefill(const PrefillArgs& a, int32_t dtype, void* stream) {
   PrefillArgs arg = a;
   void* params[] = {&arg};
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  hipError_t e = hipLaunchKernel(HKV_FN(hkv_kda_prefill_plan), dim3(a.n_seqs), dim3(kPlanThreads),
-                                 params, 0, st);
+  hipError_t e = hipSuccess;
+  if (a.planned)
+    e = hipLaunchKernel(HKV_FN(hkv_kda_prefill_plan), dim3(a.n_seqs), dim3(kPlanThreads), params, 0,
+                        st);
   if (e != hipSuccess) return (int)e;
   if (a.chunked) {
     static const void* const kForm[2] = {HKV_FN(hkv_kda_form_bf16), HKV_FN(hkv_kda_form_fp16)};

@@ -211,6 +211,7 @@ hkv_status plan_prefill(const hkv_layout* layout, const hkv_kda_prefill_args* a,
   k->short_tokens = k->n_seqs > 1 ? hkv::kPrefillShort : 0;
   k->chunked = d == (int64_t)hkv::kPrefillChunkDim && taps == 4 && es == 2 &&
                k->max_seq_tokens > hkv::kPrefillShort;
+  k->planned = k->chunked || k->n_seqs > hkv::kPrefillLookThrough;
   // A sequence's blocks are cut each on its own: the last chunk of the first, of
   // the last and of every whole block may be short.
   if (k->chunked)
