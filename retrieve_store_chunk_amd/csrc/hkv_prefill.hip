@@ -172,47 +172,72 @@ __device__ __forceinline__ void plan(const hkv::PrefillArgs& a) {
   }
 }
 
+// ---------------------------------------------------------------- lanes
+__device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+__device__ __forceinline__ float real(uint32_t x) { return __builtin_bit_cast(float, x); }
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float x) {
+  return real((uint32_t)__builtin_amdgcn_update_dpp(0, (int)bits(x), kCtrl, 0xf, 0xf, true));
+}
+
+// Sums over lanes that differ in bits 4 and 5.
+__device__ __forceinline__ float sum_rows(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
+  const uint32_t r0 = r[0], r1 = r[1];
+  x = real(r0) + real(r1);
+  const auto q = __builtin_amdgcn_permlane16_swap(bits(x), bits(x), false, false);
+  const uint32_t q0 = q[0], q1 = q[1];
+  return real(q0) + real(q1);
+}
+// Over those that differ in bits 2 to 5.
+__device__ __forceinline__ float sum_fours(float x) {
+  x += dpp<0x128>(x);  // row_ror:8
+  x += dpp<0x124>(x);  // row_ror:4
+  return sum_rows(x);
+}
+// Over all.
+__device__ __forceinline__ float sum_wave(float x) {
+  x += dpp<0xb1>(x);  // quad_perm [1,0,3,2]
+  x += dpp<0x4e>(x);  // quad_perm [2,3,0,1]
+  return sum_fours(x);
+}
+
 // ---------------------------------------------------------------- token by token
 // hkv_kda_step's arithmetic with the state and the conv's taps kept in registers
-// from token to token: one workgroup per (head, sequence).
-template <class T, uint32_t kDim, uint32_t kThreads>
+// from token to token: one workgroup per (head, sequence), a wave for 16 columns.
+// Thread t has 4 columns of kDim / 16 rows, so that the sums over rows stay within a
+// wave, and one channel of the conv or of the decays; the only thing that the waves
+// exchange is a token's q, k, v and decays: one barrier a token.
+template <class T, uint32_t kDim>
 __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
   using E = typename T::type;
-  constexpr uint32_t kRowThreads = kDim / 4;               // threads that hold a row
-  constexpr uint32_t kGroups = kThreads / kRowThreads;   // rows held at a time
-  constexpr uint32_t kRows = kDim / kGroups;               // rows per thread
-  constexpr uint32_t kWaves = kThreads / 64;
-  constexpr uint32_t kChannels = (3 * kDim + kThreads - 1) / kThreads;  // conv rows per thread
-  static_assert(kGroups * kRows == kDim && kRowThreads <= 64, "a head splits into whole rows");
+  constexpr uint32_t kThreads = kDim * 4, kWaves = kThreads / 64, kRows = kDim / 16;
   // two of each, by the token's parity: the next token's are written while slower
   // waves still read this one's
-  __shared__ float y[2][3][kDim];  // q, k, v after the conv
-  __shared__ float decay[2][kDim];
-  __shared__ v4f sums[2][kWaves][kRowThreads];
+  __shared__ __attribute__((aligned(16))) float y[2][4][kDim];  // q, k, v after the conv; decays
   __shared__ uint32_t found[kWaves];
   const uint32_t h = blockIdx.x, s = blockIdx.y, t = threadIdx.x, lane = t & 63;
-  const uint32_t c = t % kRowThreads, r0 = t / kRowThreads;
+  const uint32_t col = (t >> 6) * 16 + (lane & 3) * 4, r0 = (lane >> 2) * kRows;
   const int32_t row0 = a.starts[s];
-  int32_t n = a.starts[s + 1] - row0;
+  const int32_t n = a.starts[s + 1] - row0;
   if (a.chunked && n > (int32_t)a.short_tokens) return;
-  E* const out = static_cast<E*>(a.out) + (int64_t)row0 * a.out_stride + (int64_t)h * kDim + c * 4;
+  E* const out = static_cast<E*>(a.out) + (int64_t)row0 * a.out_stride + (int64_t)h * kDim + col;
   const int32_t position = a.positions[s];
   int32_t src = a.src[s];
   if (outside(src, a.num_blocks)) src = HKV_NULL_BLOCK;  // until the verdict below
   const int32_t* const table = a.table + (int64_t)s * a.table_stride;
-  const uint64_t state_off = a.conv_bytes + (uint64_t)h * kDim * kDim * 4;
-  const uint32_t state_at = r0 * kRowThreads + c;  // in units of four values
-  const uint32_t keep = a.taps - 1;
+  const uint64_t state_off =
+      a.conv_bytes + (((uint64_t)h * kDim + r0) * kDim + col) * 4;
 
   v4f st[kRows];
   {
-    const HKV_GLOBAL v4f* p =
-        (const HKV_GLOBAL v4f*)(a.pages + (uint64_t)(src < 0 ? 0 : src) * a.stride + state_off) +
-        state_at;
+    const HKV_GLOBAL uint8_t* p =
+        (const HKV_GLOBAL uint8_t*)(a.pages + (uint64_t)(src < 0 ? 0 : src) * a.stride + state_off);
 #pragma unroll
     for (uint32_t i = 0; i < kRows; ++i) {
       st[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      if (src >= 0) st[i] = p[i * kGroups * kRowThreads];
+      if (src >= 0) st[i] = *(const HKV_GLOBAL v4f*)(p + i * kDim * 4);
     }
   }
   // The verdict on the sequence, while its state is under way.
@@ -232,146 +257,122 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
   }
   if (status == hkv::kPrefillNoRows) return;
   if (status == hkv::kPrefillRefused) {
-    for (uint32_t i = r0; i < (uint32_t)n; i += kGroups)
+    for (uint32_t i = lane >> 2; i < (uint32_t)n; i += 16)
       T::store4(out + (int64_t)i * a.out_stride, v4f{NAN, NAN, NAN, NAN});
     return;
   }
-  // One thread per channel: its weights, its last `keep` values (oldest first).
-  E taps[kChannels][hkv::kKdaMaxKernel - 1];
-  float weight[kChannels][hkv::kKdaMaxKernel];
-#pragma unroll
-  for (uint32_t i = 0; i < kChannels; ++i) {
-    const uint32_t w = t + i * kThreads;
-    if (w >= 3 * kDim) break;
-    const uint64_t ch = ((uint64_t)(w / kDim) * a.heads + h) * kDim + w % kDim;
+  // Threads below 3 kDim: a channel's weights, its last `keep` values (oldest first).
+  // The others: a channel's decay.
+  const uint32_t keep = a.taps - 1, part = t / kDim, in_part = t % kDim;
+  const uint64_t ch = ((uint64_t)part * a.heads + h) * kDim + in_part;
+  E taps[hkv::kKdaMaxKernel - 1];
+  float weight[hkv::kKdaMaxKernel];
+  if (part < 3) {
     const E* wt = static_cast<const E*>(a.conv_weight) + ch * a.taps;
     const E* old = reinterpret_cast<const E*>(a.pages + (uint64_t)(src < 0 ? 0 : src) * a.stride) +
                    ch * keep;
 #pragma unroll
-    for (uint32_t j = 0; j < hkv::kKdaMaxKernel; ++j) weight[i][j] = j <= keep ? (float)wt[j] : 0.0f;
+    for (uint32_t j = 0; j < hkv::kKdaMaxKernel; ++j) weight[j] = j <= keep ? (float)wt[j] : 0.0f;
 #pragma unroll
     for (uint32_t j = 0; j + 1 < hkv::kKdaMaxKernel; ++j)
-      taps[i][j] = j < keep && src >= 0 ? old[j] : (E)0.0f;
+      taps[j] = j < keep && src >= 0 ? old[j] : (E)0.0f;
   }
 
   // A token's inputs are fetched while the one before is computed.
-  constexpr uint32_t kDecays = (kDim + kThreads - 1) / kThreads;
-  E x_next[kChannels];
-  float g_next[kDecays], beta_next;
+  E x_next = (E)0.0f;
+  float g_next = 0.0f, beta_next;
   auto fetch = [&](int32_t m) {
     const int64_t row = (int64_t)row0 + m;
-#pragma unroll
-    for (uint32_t i = 0; i < kChannels; ++i) {
-      const uint32_t w = t + i * kThreads;
-      if (w >= 3 * kDim) break;
-      const uint64_t ch = ((uint64_t)(w / kDim) * a.heads + h) * kDim + w % kDim;
-      x_next[i] = static_cast<const E*>(a.x)[row * a.x_stride + (int64_t)ch];
-    }
-#pragma unroll
-    for (uint32_t i = 0; i < kDecays; ++i)
-      if (t + i * kThreads < kDim)
-        g_next[i] = a.log_decay[row * a.decay_stride + (int64_t)h * kDim + t + i * kThreads];
+    if (part < 3)
+      x_next = static_cast<const E*>(a.x)[row * a.x_stride + (int64_t)ch];
+    else
+      g_next = a.log_decay[row * a.decay_stride + (int64_t)h * kDim + in_part];
     beta_next = a.beta[row * a.beta_stride + h];
   };
   fetch(0);
   for (int32_t m = 0; m < n; ++m) {
     const uint32_t b = m & 1;
-#pragma unroll
-    for (uint32_t i = 0; i < kChannels; ++i) {
-      const uint32_t w = t + i * kThreads;
-      if (w >= 3 * kDim) break;
-      const E x = x_next[i];
+    if (part < 3) {
+      const E x = x_next;
       float sum = 0.0f;
+      if (keep == 3) {
 #pragma unroll
-      for (uint32_t j = 0; j + 1 < hkv::kKdaMaxKernel; ++j)
-        if (j < keep) sum += weight[i][j] * (float)taps[i][j];
+        for (uint32_t j = 0; j < 3; ++j) sum += weight[j] * (float)taps[j];
+        sum += weight[3] * (float)x;
+        taps[0] = taps[1];
+        taps[1] = taps[2];
+        taps[2] = x;
+      } else {
 #pragma unroll
-      for (uint32_t j = 0; j < hkv::kKdaMaxKernel; ++j)
-        if (j == keep) sum += weight[i][j] * (float)x;
+        for (uint32_t j = 0; j + 1 < hkv::kKdaMaxKernel; ++j)
+          if (j < keep) sum += weight[j] * (float)taps[j];
 #pragma unroll
-      for (uint32_t j = 0; j + 1 < hkv::kKdaMaxKernel; ++j) {
-        if (j + 1 < keep) taps[i][j] = taps[i][j + 1 < hkv::kKdaMaxKernel - 1 ? j + 1 : j];
-        if (j + 1 == keep) taps[i][j] = x;
+        for (uint32_t j = 0; j < hkv::kKdaMaxKernel; ++j)
+          if (j == keep) sum += weight[j] * (float)x;
+#pragma unroll
+        for (uint32_t j = 0; j + 1 < hkv::kKdaMaxKernel; ++j) {
+          if (j + 1 < keep) taps[j] = taps[j + 1 < hkv::kKdaMaxKernel - 1 ? j + 1 : j];
+          if (j + 1 == keep) taps[j] = x;
+        }
       }
-      y[b][w / kDim][w % kDim] = sum / (1.0f + expf(-sum));
+      y[b][part][in_part] =
+          sum * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(sum * -1.44269504f));
+    } else {
+      y[b][3][in_part] = __builtin_amdgcn_exp2f((g_next > 0.0f ? 0.0f : g_next) * 1.44269504f);
     }
-#pragma unroll
-    for (uint32_t i = 0; i < kDecays; ++i)
-      if (t + i * kThreads < kDim)
-        decay[b][t + i * kThreads] = expf(g_next[i] > 0.0f ? 0.0f : g_next[i]);
     const float beta = beta_next;
     if (m + 1 < n) fetch(m + 1);
     __syncthreads();
 
     // |q|^2, |k|^2 and q.k, by every wave for itself.
     float qq = 0.0f, kk = 0.0f, qk = 0.0f;
-    for (uint32_t i = lane; i < kDim; i += 64) {
-      const float q = y[b][0][i], k = y[b][1][i];
-      qq += q * q;
-      kk += k * k;
-      qk += q * k;
-    }
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      qq += __shfl_xor(qq, d, 64);
-      kk += __shfl_xor(kk, d, 64);
-      qk += __shfl_xor(qk, d, 64);
-    }
-    const float nq = a.scale / sqrtf(qq + a.eps), nk = 1.0f / sqrtf(kk + a.eps);
+    for (uint32_t i = 0; i < (kDim + 63) / 64; ++i)
+      if (kDim >= 64 || lane < kDim) {
+        const float q = y[b][0][lane + i * 64], k = y[b][1][lane + i * 64];
+        qq += q * q;
+        kk += k * k;
+        qk += q * k;
+      }
+    qq = sum_wave(qq);
+    kk = sum_wave(kk);
+    qk = sum_wave(qk);
+    const float nq = a.scale * __builtin_amdgcn_rsqf(qq + a.eps);
+    const float nk = __builtin_amdgcn_rsqf(kk + a.eps);
 
+    float k[kRows];
     v4f sk = {0.0f, 0.0f, 0.0f, 0.0f}, sq = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (uint32_t i = 0; i < kRows; ++i) {
-      const uint32_t r = r0 + i * kGroups;
-      st[i] *= decay[b][r];
-      sk += st[i] * (y[b][1][r] * nk);
-      sq += st[i] * (y[b][0][r] * nq);
+      k[i] = y[b][1][r0 + i] * nk;
+      st[i] *= y[b][3][r0 + i];
+      sk += st[i] * k[i];
+      sq += st[i] * (y[b][0][r0 + i] * nq);
     }
-#pragma unroll
-    for (uint32_t d = kRowThreads; d < 64; d <<= 1)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sk[i] += __shfl_xor(sk[i], (int)d, 64);
-        sq[i] += __shfl_xor(sq[i], (int)d, 64);
-      }
-    if (kWaves > 1) {
-      if (lane < kRowThreads) {
-        sums[0][t >> 6][c] = sk;
-        sums[1][t >> 6][c] = sq;
-      }
-      __syncthreads();
-      sk = sums[0][0][c];
-      sq = sums[1][0][c];
-#pragma unroll
-      for (uint32_t w = 1; w < kWaves; ++w) {
-        sk += sums[0][w][c];
-        sq += sums[1][w][c];
-      }
-    }
+    const v4f v = *reinterpret_cast<const v4f*>(&y[b][2][col]);
     v4f u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = beta * (y[b][2][c * 4 + i] - sk[i]);
-    if (r0 == 0) T::store4(out + (int64_t)m * a.out_stride, sq + u * (qk * nq * nk));
+    for (int i = 0; i < 4; ++i) {
+      u[i] = beta * (v[i] - sum_fours(sk[i]));
+      sq[i] = sum_fours(sq[i]) + u[i] * (qk * nq * nk);
+    }
+    if (lane < 4) T::store4(out + (int64_t)m * a.out_stride, sq);
 #pragma unroll
-    for (uint32_t i = 0; i < kRows; ++i) st[i] += u * (y[b][1][r0 + i * kGroups] * nk);
+    for (uint32_t i = 0; i < kRows; ++i) st[i] += u * k[i];
 
     const uint32_t at = (uint32_t)(position + m);
-    if ((at + 1) % a.block_tokens != 0 && m != n - 1) continue;
+    if (m != n - 1 && (at + 1) % a.block_tokens != 0) continue;
     const int32_t dst = table[at / a.block_tokens];
     if (dst < 0) continue;
-    HKV_GLOBAL v4f* p =
-        (HKV_GLOBAL v4f*)(a.pages + (uint64_t)dst * a.stride + state_off) + state_at;
+    HKV_GLOBAL uint8_t* p =
+        (HKV_GLOBAL uint8_t*)(a.pages + (uint64_t)dst * a.stride + state_off);
 #pragma unroll
-    for (uint32_t i = 0; i < kRows; ++i) p[i * kGroups * kRowThreads] = st[i];
-#pragma unroll
-    for (uint32_t i = 0; i < kChannels; ++i) {
-      const uint32_t w = t + i * kThreads;
-      if (w >= 3 * kDim) break;
-      const uint64_t ch = ((uint64_t)(w / kDim) * a.heads + h) * kDim + w % kDim;
+    for (uint32_t i = 0; i < kRows; ++i) *(HKV_GLOBAL v4f*)(p + i * kDim * 4) = st[i];
+    if (part < 3) {
       E* to = reinterpret_cast<E*>(a.pages + (uint64_t)dst * a.stride) + ch * keep;
 #pragma unroll
       for (uint32_t j = 0; j + 1 < hkv::kKdaMaxKernel; ++j)
-        if (j < keep) to[j] = taps[i][j];
+        if (j < keep) to[j] = taps[j];
     }
   }
 }
@@ -401,9 +402,6 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef int32_t v2i __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
-__device__ __forceinline__ float real(uint32_t x) { return __builtin_bit_cast(float, x); }
 
 // x = hi + lo, to 2^-22 of x.
 struct Terms2 {
@@ -439,11 +437,6 @@ __device__ __forceinline__ void mfma3(const Terms8& a, const Terms8& b, v4f (&c)
   c[0] = mfma(a.lo, b.hi, c[0]);
   c[1] = mfma(a.hi, b.lo, c[1]);
   c[2] = mfma(a.hi, b.hi, c[2]);
-}
-
-template <int kCtrl>
-__device__ __forceinline__ float dpp(float x) {
-  return real((uint32_t)__builtin_amdgcn_update_dpp(0, (int)bits(x), kCtrl, 0xf, 0xf, true));
 }
 
 // Sums 16 values over the wave: lane l gets the sum of value l / 4.
@@ -1483,18 +1476,17 @@ extern "C" __global__ __launch_bounds__(kPlanThreads) void hkv_kda_prefill_plan(
   plan(a);
 }
 
-// Threads by head dim, as in the step's kernels.
-#define HKV_TOKENS(name, T, d, threads)                                     \
-  extern "C" __global__ __launch_bounds__(threads, 4) void name(            \
-      hkv::PrefillArgs a) {                                                 \
-    tokens<T, d, threads>(a);                                               \
+#define HKV_TOKENS(name, T, d)                                                     \
+  extern "C" __global__ __launch_bounds__(d * 4, d <= 128 ? 4 : 1) void name(      \
+      hkv::PrefillArgs a) {                                                        \
+    tokens<T, d>(a);                                                               \
   }
-#define HKV_TOKENS_DIMS(suffix, T)                        \
-  HKV_TOKENS(hkv_kda_tokens_##suffix##_d16, T, 16, 64)    \
-  HKV_TOKENS(hkv_kda_tokens_##suffix##_d32, T, 32, 64)    \
-  HKV_TOKENS(hkv_kda_tokens_##suffix##_d64, T, 64, 256)   \
-  HKV_TOKENS(hkv_kda_tokens_##suffix##_d128, T, 128, 512) \
-  HKV_TOKENS(hkv_kda_tokens_##suffix##_d256, T, 256, 1024)
+#define HKV_TOKENS_DIMS(suffix, T)                 \
+  HKV_TOKENS(hkv_kda_tokens_##suffix##_d16, T, 16)    \
+  HKV_TOKENS(hkv_kda_tokens_##suffix##_d32, T, 32)    \
+  HKV_TOKENS(hkv_kda_tokens_##suffix##_d64, T, 64)    \
+  HKV_TOKENS(hkv_kda_tokens_##suffix##_d128, T, 128)  \
+  HKV_TOKENS(hkv_kda_tokens_##suffix##_d256, T, 256)
 HKV_TOKENS_DIMS(bf16, Bf16)
 HKV_TOKENS_DIMS(fp16, Fp16)
 HKV_TOKENS_DIMS(fp32, Fp32)
@@ -1541,7 +1533,6 @@ int launch_prefill(const PrefillArgs& a, int32_t dtype, void* stream) {
    HKV_FN(hkv_kda_tokens_##suffix##_d256)}
   static const void* const kTokens[3][5] = {HKV_DIMS(bf16), HKV_DIMS(fp16), HKV_DIMS(fp32)};
 #undef HKV_DIMS
-  static const uint32_t kThreads[5] = {64, 64, 256, 512, 1024};
   uint32_t i = 0;
   while (i < 4 && (16u << i) != a.head_dim) ++i;
   PrefillArgs arg = a;
@@ -1566,8 +1557,8 @@ int launch_prefill(const PrefillArgs& a, int32_t dtype, void* stream) {
                         dim3(kScanThreads), params, 0, st);
     if (e != hipSuccess || a.short_tokens == 0) return (int)e;
   }
-  return (int)hipLaunchKernel(kTokens[dtype][i], dim3(a.heads, a.n_seqs), dim3(kThreads[i]),
-                              params, 0, st);
+  return (int)hipLaunchKernel(kTokens[dtype][i], dim3(a.heads, a.n_seqs), dim3(64u << i), params,
+                              0, st);
 #undef HKV_FN
 }
 
