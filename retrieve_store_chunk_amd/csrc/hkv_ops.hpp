@@ -227,9 +227,13 @@ constexpr uint32_t kPrefillChunk = 64;       // tokens
 constexpr uint32_t kPrefillChunkDim = 128;   // the head dim that is computed in chunks
 constexpr uint32_t kPrefillRecord = 3 * 32768 + 12288 + 32768 + 1024;  // bytes of a chunk and head
 
-// Runs of up to so many tokens go token by token (a call of one sequence has no
-// launch for them where it has chunks).
-constexpr uint32_t kPrefillShort = 8;
+// Calls whose longest run has up to so many tokens go token by token; in others,
+// runs of up to kPrefillShort (a call of one sequence has no launch for them).
+constexpr uint32_t kPrefillTokens = 24, kPrefillTokensOne = 16;
+constexpr uint32_t kPrefillShort = 2;
+// Calls of at most so many (sequence, head) pairs whose longest run has at least so many
+// tokens cut their sequences' chunks into parts.
+constexpr uint32_t kPrefillPartPairs = 16, kPrefillPartTokens = 1200;
 
 // Up to so many sequences are looked through by every workgroup of the token-by-token
 // kernel itself: a launch less.
@@ -266,11 +270,14 @@ struct PrefillArgs {
   uint32_t chunked;         // sequences of more than short_tokens are computed in chunks
   uint32_t short_tokens;
   uint32_t max_chunks;
+  uint32_t column_tiles;    // of 16 columns a scanning workgroup, 1 or 2
+  uint32_t parts;           // that a sequence's chunks are cut into, 1 or at least 3
   // workspace
   int32_t* status;          // [n_seqs]: kPrefill* below
   int32_t* first_chunk;     // [2][n_seqs], [1]: each sequence's first, how many; all of them
   PrefillChunk* chunks;     // [max_chunks]
   uint8_t* records;         // [max_chunks][heads][kPrefillRecord]
+  float* made;              // [n_seqs][heads][parts - 1][2][128][128], where there are parts
 };
 
 // What becomes of a sequence.
@@ -279,14 +286,17 @@ constexpr int32_t kPrefillRefused = 1;  // NaN in its rows, no page
 constexpr int32_t kPrefillNoRows = 2;   // nothing to do, or its rows are not known
 
 struct PrefillWorkspace {
-  uint64_t status, first_chunk, chunks, records, total;
+  uint64_t status, first_chunk, chunks, records, made, total;
 };
-inline PrefillWorkspace prefill_workspace(uint64_t n_seqs, uint64_t max_chunks, uint64_t heads) {
+inline PrefillWorkspace prefill_workspace(uint64_t n_seqs, uint64_t max_chunks, uint64_t heads,
+                                          uint64_t parts) {
   PrefillWorkspace w{};
   w.first_chunk = w.status + align256(n_seqs * 4);
   w.chunks = w.first_chunk + (max_chunks ? align256((2 * n_seqs + 1) * 4) : 0);
   w.records = w.chunks + align256(max_chunks * sizeof(PrefillChunk));
-  w.total = w.records + max_chunks * heads * kPrefillRecord;
+  w.made = w.records + max_chunks * heads * kPrefillRecord;
+  w.total = w.made + n_seqs * heads * (parts > 1 ? (parts - 1) * 2 : 0) * kPrefillChunkDim *
+                         kPrefillChunkDim * 4;
   return w;
 }
 

@@ -1151,42 +1151,63 @@ __device__ __forceinline__ Terms8 read_terms(const uint8_t* p, uint32_t at) {
   return t;
 }
 
-template <class T, uint32_t kCt>
+// The part of a sequence that a workgroup goes through: chunks c0 .. c1 - 1 from
+//   kSource    the source page's state,
+//   kIdentity  the unit matrix, without V, and kNothing, zeros: what the part makes of any
+//              state S before it, M S + B, goes to `end`,
+//   kJoined    the state before it, joined from what `parts` parts made.
+enum Start { kSource, kIdentity, kNothing, kJoined };
+struct Part {
+  Start start;
+  uint32_t c0, c1;
+  float* end;         // [kD][kD] the state behind the part, or nullptr
+  const float* made;  // [parts][2][kD][kD]: B and M of each part before
+  uint32_t parts;
+};
+
+template <class T, uint32_t kCt, bool kOut>
 __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint32_t h,
-                                     uint32_t group, ScanShared<kCt>& lds) {
+                                     uint32_t group, const Part& part, ScanShared<kCt>& lds) {
   using E = typename T::type;
   const uint32_t w = wave_index(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
-  const int32_t status = a.status[s];
-  if (status == hkv::kPrefillNoRows) return;
   const int32_t row0 = a.starts[s], n = a.starts[s + 1] - row0;
-  if (n <= (int32_t)a.short_tokens) return;
   const uint32_t col0 = group * kCt * 16;
   E* const out = static_cast<E*>(a.out) + (int64_t)h * kD + col0 + lg * 4;
-  if (status == hkv::kPrefillRefused) {
-    for (int32_t i = (int32_t)(lr + w * 16); i < n; i += 64)
+  if (a.status[s] == hkv::kPrefillRefused) {
+    if (kOut)
+      for (int32_t i = (int32_t)(lr + w * 16); i < n; i += 64)
 #pragma unroll
-      for (uint32_t ct = 0; ct < kCt; ++ct)
-        T::store4(out + (int64_t)(row0 + i) * a.out_stride + ct * 16, v4f{NAN, NAN, NAN, NAN});
+        for (uint32_t ct = 0; ct < kCt; ++ct)
+          T::store4(out + (int64_t)(row0 + i) * a.out_stride + ct * 16, v4f{NAN, NAN, NAN, NAN});
     return;
   }
   const int32_t src = a.src[s];
-  const uint32_t slot0 = (uint32_t)a.first_chunk[s], count = (uint32_t)a.first_chunk[s + a.n_seqs];
-  const uint8_t* rec = a.records + ((uint64_t)slot0 * a.heads + h) * hkv::kPrefillRecord;
+  const uint32_t slot0 = (uint32_t)a.first_chunk[s];
+  const uint8_t* rec =
+      a.records + ((uint64_t)(slot0 + part.c0) * a.heads + h) * hkv::kPrefillRecord;
   const uint64_t step = (uint64_t)a.heads * hkv::kPrefillRecord;
-  const uint64_t state_off =
-      a.conv_bytes + (((uint64_t)h * kD + w * 32 + lg * 4) * kD + col0 + lr) * 4;
+  const uint32_t state_at = (w * 32 + lg * 4) * kD + col0 + lr;  // of a head's [kD][kD]
+  const uint64_t state_off = a.conv_bytes + ((uint64_t)h * kD * kD + state_at) * 4;
   v4f st[2][kCt];
+  {
+    const HKV_GLOBAL float* from = nullptr;
+    if (part.start == kJoined)
+      from = (const HKV_GLOBAL float*)(part.made + state_at);
+    else if (part.start == kSource && src >= 0)
+      from = (const HKV_GLOBAL float*)(a.pages + (uint64_t)src * a.stride + state_off);
 #pragma unroll
-  for (uint32_t i = 0; i < 2; ++i)
+    for (uint32_t i = 0; i < 2; ++i)
 #pragma unroll
-    for (uint32_t ct = 0; ct < kCt; ++ct) {
-      st[i][ct] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      if (src < 0) continue;
-      const HKV_GLOBAL float* p =
-          (const HKV_GLOBAL float*)(a.pages + (uint64_t)src * a.stride + state_off);
+      for (uint32_t ct = 0; ct < kCt; ++ct)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) st[i][ct][j] = p[(i * 16 + j) * kD + ct * 16];
-    }
+        for (int j = 0; j < 4; ++j) {
+          const bool one = part.start == kIdentity &&
+                           w * 32 + i * 16 + lg * 4 + j == col0 + ct * 16 + lr;
+          st[i][ct][j] = one ? 1.0f : 0.0f;
+          if (from) st[i][ct][j] = from[(i * 16 + j) * kD + ct * 16];
+        }
+  }
+
   // A chunk's operands of this wave.
   Terms8 wf[kD / 32], qf[kD / 32], pf[2], kf[2][2];
   v4f u0[kCt], decay[2];
@@ -1195,12 +1216,15 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
   const uint32_t at = lane * 16;
   auto fetch_wq = [&](const uint8_t* r, uint32_t kb) {
     wf[kb] = read_terms(r + kRecW + (w * (kD / 32) + kb) * 2048, at);
-    qf[kb] = read_terms(r + kRecQ + (w * (kD / 32) + kb) * 2048, at);
+    if (kOut) qf[kb] = read_terms(r + kRecQ + (w * (kD / 32) + kb) * 2048, at);
   };
   auto fetch_u = [&](const uint8_t* r) {
 #pragma unroll
     for (uint32_t ct = 0; ct < kCt; ++ct)
-      u0[ct] = *(const HKV_GLOBAL v4f*)(r + kRecU + ((group * kCt + ct) * 4 + w) * 1024 + at);
+      if (!kOut && part.start == kIdentity)
+        u0[ct] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      else
+        u0[ct] = *(const HKV_GLOBAL v4f*)(r + kRecU + ((group * kCt + ct) * 4 + w) * 1024 + at);
   };
   auto fetch_k = [&](const uint8_t* r, uint32_t i, uint32_t kb) {
     kf[i][kb] = read_terms(r + kRecK + ((w * 2 + i) * 2 + kb) * 2048, at);
@@ -1217,7 +1241,9 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
   auto fetch_e = [&](const uint8_t* r) {
 #pragma unroll
     for (uint32_t ct = 0; ct < kCt; ++ct)
-      ve[ct] = *(const HKV_GLOBAL int32_t*)(r + kRecExps + (col0 + ct * 16) * 4 + lr * 4);
+      ve[ct] = !kOut && part.start == kIdentity
+                   ? -1000
+                   : *(const HKV_GLOBAL int32_t*)(r + kRecExps + (col0 + ct * 16) * 4 + lr * 4);
   };
 
   // Columns are held 2^e times themselves.  The state's terms for the products of the
@@ -1277,6 +1303,49 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
       lds.s[ct][w][1][lane] = x.lo;
     }
   };
+  v4f none[kCt];
+#pragma unroll
+  for (uint32_t ct = 0; ct < kCt; ++ct) none[ct] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  // The state before the part: S <- M S + B for each of the parts between the first and
+  // this one.  M's rows lie in memory as they are; a lane takes those of its 8 columns.
+  if (kOut && part.start == kJoined)
+    for (uint32_t x = 1; x < part.parts; ++x) {
+      const float* const b = part.made + (uint64_t)x * 2 * kD * kD;
+#pragma unroll
+      for (uint32_t ct = 0; ct < kCt; ++ct) ve[ct] = -1000;
+      put_most(none, 0.0f);
+      __syncthreads();
+      get_most();
+      put_state();
+      __syncthreads();
+      v4f z[2][kCt] = {};
+#pragma unroll
+      for (uint32_t kb = 0; kb < kD / 32; ++kb)
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i) {
+          const HKV_GLOBAL float* const m = (const HKV_GLOBAL float*)(b + kD * kD) +
+                                            (w * 32 + i * 16 + lr) * kD + kb * 32 + lg * 4;
+          const Terms8 mf = terms(*(const HKV_GLOBAL v4f*)m * kUnit,
+                                  *(const HKV_GLOBAL v4f*)(m + 16) * kUnit);
+#pragma unroll
+          for (uint32_t ct = 0; ct < kCt; ++ct) {
+            const v8h hi = lds.s[ct][kb][0][lane], lo = lds.s[ct][kb][1][lane];
+            z[i][ct] = mfma(mf.lo, hi, z[i][ct]);
+            z[i][ct] = mfma(mf.hi, lo, z[i][ct]);
+            z[i][ct] = mfma(mf.hi, hi, z[i][ct]);
+          }
+        }
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i)
+#pragma unroll
+        for (uint32_t ct = 0; ct < kCt; ++ct)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            st[i][ct][j] =
+                z[i][ct][j] * (1.0f / kUnit) +
+                __builtin_ldexpf(((const HKV_GLOBAL float*)(b + state_at))[(i * 16 + j) * kD + ct * 16],
+                                 e[ct]);
+    }
   fetch_e(rec);
   fetch_u(rec);
 #pragma unroll
@@ -1284,22 +1353,18 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
   fetch_d(rec);
 #pragma unroll
   for (uint32_t x = 0; x < 4; ++x) fetch_k(rec, x & 1, x >> 1);
-  fetch_p(rec);
-  {
-    v4f none[kCt];
-#pragma unroll
-    for (uint32_t ct = 0; ct < kCt; ++ct) none[ct] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    put_most(none, 0.0f);
-  }
+  if (kOut) fetch_p(rec);
+  put_most(none, 0.0f);
   __syncthreads();
   get_most();
   put_state();
   __syncthreads();
-  hkv::PrefillChunk ck = read_chunk(a, slot0);
-  for (uint32_t c = 0; c < count; ++c) {
-    const hkv::PrefillChunk ck_next = read_chunk(a, slot0 + (c + 1 < count ? c + 1 : c));
+  hkv::PrefillChunk ck = read_chunk(a, slot0 + part.c0);
+  for (uint32_t c = part.c0; c < part.c1; ++c) {
+    const bool more = c + 1 < part.c1;
+    const hkv::PrefillChunk ck_next = read_chunk(a, slot0 + (more ? c + 1 : c));
     // the last chunk's operands are fetched once more instead of none
-    const uint8_t* const next = c + 1 < count ? rec + step : rec;
+    const uint8_t* const next = more ? rec + step : rec;
     fetch_e(next);
     Terms8 sf[2][kCt];
     auto get_state = [&](uint32_t kb) {
@@ -1332,7 +1397,7 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
         for (uint32_t ct = 0; ct < kCt; ++ct) {
           const v8h x = term == 1 ? sf[kb & 1][ct].lo : sf[kb & 1][ct].hi;
           u[ct] = mfma(term == 0 ? wf[kb].lo : wf[kb].hi, x, u[ct]);
-          o[ct] = mfma(x, term == 0 ? qf[kb].lo : qf[kb].hi, o[ct]);
+          if (kOut) o[ct] = mfma(x, term == 0 ? qf[kb].lo : qf[kb].hi, o[ct]);
         }
       // operands of the next chunk as their registers become free: a CU takes 64
       // bytes a cycle, so that all of them in a row would hold up the products
@@ -1389,7 +1454,7 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
       fetch_k(next, 1, kb);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (ck.dst >= 0) {
+    if (kOut && ck.dst >= 0) {
       HKV_GLOBAL float* p = (HKV_GLOBAL float*)(a.pages + (uint64_t)ck.dst * a.stride + state_off);
 #pragma unroll
       for (uint32_t i = 0; i < 2; ++i)
@@ -1400,33 +1465,109 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
             p[(i * 16 + j) * kD + ct * 16] = __builtin_ldexpf(st[i][ct][j], -e[ct]);
     }
     put_state();
-    // O's part from U.
-#pragma unroll
-    for (int term = 0; term < 3; ++term)
-#pragma unroll
-      for (uint32_t ct = 0; ct < kCt; ++ct)
-        o[ct] = mfma(term == 1 ? uf[ct][0].lo : uf[ct][0].hi,
-                     term == 0 ? pf[0].lo : pf[0].hi, o[ct]);
-    if (w >= 2)
+    if constexpr (kOut) {
+      // O's part from U.
 #pragma unroll
       for (int term = 0; term < 3; ++term)
 #pragma unroll
         for (uint32_t ct = 0; ct < kCt; ++ct)
-          o[ct] = mfma(term == 1 ? uf[ct][1].lo : uf[ct][1].hi,
-                       term == 0 ? pf[1].lo : pf[1].hi, o[ct]);
-    fetch_p(next);
-    const int32_t i = (int32_t)(w * 16 + lr);
+          o[ct] = mfma(term == 1 ? uf[ct][0].lo : uf[ct][0].hi,
+                       term == 0 ? pf[0].lo : pf[0].hi, o[ct]);
+      if (w >= 2)
 #pragma unroll
-    for (uint32_t ct = 0; ct < kCt; ++ct) {
-      v4f x;
+        for (int term = 0; term < 3; ++term)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = __builtin_ldexpf(o[ct][j], back[ct][j]) * a.scale;
-      if (i < ck.len) T::store4(out + (int64_t)(ck.row + i) * a.out_stride + ct * 16, x);
+          for (uint32_t ct = 0; ct < kCt; ++ct)
+            o[ct] = mfma(term == 1 ? uf[ct][1].lo : uf[ct][1].hi,
+                         term == 0 ? pf[1].lo : pf[1].hi, o[ct]);
+      fetch_p(next);
+      const int32_t i = (int32_t)(w * 16 + lr);
+#pragma unroll
+      for (uint32_t ct = 0; ct < kCt; ++ct) {
+        v4f x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __builtin_ldexpf(o[ct][j], back[ct][j]) * a.scale;
+        if (i < ck.len) T::store4(out + (int64_t)(ck.row + i) * a.out_stride + ct * 16, x);
+      }
     }
     rec = next;
     ck = ck_next;
     __syncthreads();
   }
+  if (part.end) {
+    HKV_GLOBAL float* const p = (HKV_GLOBAL float*)(part.end + state_at);
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i)
+#pragma unroll
+      for (uint32_t ct = 0; ct < kCt; ++ct)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          p[(i * 16 + j) * kD + ct * 16] = __builtin_ldexpf(st[i][ct][j], -e[ct]);
+  }
+}
+
+// Whether a sequence has chunks, or rows that are refused.
+__device__ __forceinline__ bool scanned(const hkv::PrefillArgs& a, uint32_t s) {
+  return a.status[s] != hkv::kPrefillNoRows &&
+         a.starts[s + 1] - a.starts[s] > (int32_t)a.short_tokens;
+}
+
+template <class T, uint32_t kCt>
+__device__ __forceinline__ void scan_all(const hkv::PrefillArgs& a, uint32_t s, uint32_t h,
+                                         uint32_t group, ScanShared<kCt>& lds) {
+  if (!scanned(a, s)) return;
+  const Part part = {kSource, 0, (uint32_t)a.first_chunk[s + a.n_seqs], nullptr, nullptr, 0};
+  scan<T, kCt, true>(a, s, h, group, part, lds);
+}
+
+// Few heads and long sequences: a sequence's chunks in a.parts parts.  First the first
+// part is gone through, and at the same time the others but the last make M and B; then
+// every other part joins the state before it and is gone through.
+constexpr uint32_t kLeastPart = 6;  // chunks
+__device__ __forceinline__ uint32_t part_chunks(const hkv::PrefillArgs& a, uint32_t count) {
+  return max((count + a.parts - 1) / a.parts, kLeastPart);
+}
+__device__ __forceinline__ float* made_by(const hkv::PrefillArgs& a, uint32_t s, uint32_t h,
+                                          uint32_t part) {
+  return a.made + (((uint64_t)s * a.heads + h) * (a.parts - 1) + part) * 2 * kD * kD;
+}
+// unit: 8 column groups of the first part, then for each other but the last those of B and
+// of M.
+template <class T>
+__device__ __forceinline__ void scan_first(const hkv::PrefillArgs& a, uint32_t s, uint32_t h,
+                                           uint32_t unit, ScanShared<1>& lds) {
+  if (!scanned(a, s)) return;
+  const uint32_t group = unit % 8, x = unit / 8, which = (x + 1) / 2;
+  const uint32_t count = (uint32_t)a.first_chunk[s + a.n_seqs], each = part_chunks(a, count);
+  Part part = {};
+  part.c0 = which * each;
+  part.c1 = min(part.c0 + each, count);
+  if (which == 0) {
+    part.start = kSource;
+    if (part.c1 < count) part.end = made_by(a, s, h, 0);
+    scan<T, 1, true>(a, s, h, group, part, lds);
+    return;
+  }
+  if (part.c1 >= count) return;  // no part behind this one
+  const bool is_m = x % 2 == 0;
+  part.start = is_m ? kIdentity : kNothing;
+  part.end = made_by(a, s, h, which) + (is_m ? kD * kD : 0);
+  scan<T, 1, false>(a, s, h, group, part, lds);
+}
+template <class T>
+__device__ __forceinline__ void scan_rest(const hkv::PrefillArgs& a, uint32_t s, uint32_t h,
+                                          uint32_t unit, ScanShared<1>& lds) {
+  if (!scanned(a, s) || a.status[s] != hkv::kPrefillRuns) return;
+  const uint32_t group = unit % 8, which = unit / 8 + 1;
+  const uint32_t count = (uint32_t)a.first_chunk[s + a.n_seqs], each = part_chunks(a, count);
+  Part part = {};
+  part.c0 = which * each;
+  part.c1 = min(part.c0 + each, count);
+  if (part.c0 >= count) return;
+  part.start = kJoined;
+  part.made = made_by(a, s, h, 0);
+  part.parts = which;
+  scan<T, 1, true>(a, s, h, group, part, lds);
 }
 
 // The conv states of a sequence's blocks, a head's channels by one workgroup: it reads the
@@ -1493,20 +1634,20 @@ HKV_TOKENS_DIMS(fp32, Fp32)
 #undef HKV_TOKENS
 #undef HKV_TOKENS_DIMS
 
-#define HKV_SCAN(name, T, tiles)                                                            \
+// Workgroups of a (sequence, head) pair, `units` of them, lie 8 apart: on one XCD, which
+// reads the pair's records once.  The conv states' workgroups come last.
+#define HKV_SCAN(name, tiles, units, convs, call)                                           \
   extern "C" __global__ __launch_bounds__(kScanThreads, 2) void name(hkv::PrefillArgs a) {  \
     __shared__ ScanShared<tiles> lds;                                                       \
-    /* a head's column groups on one XCD, which reads its records once */                   \
-    constexpr uint32_t kGroups = kD / 16 / tiles;                                           \
-    const uint32_t pairs = a.n_seqs * a.heads, scans = (pairs + 7) / 8 * 8 * kGroups;       \
-    if (blockIdx.x >= scans) {                                                              \
+    const uint32_t n_units = units, pairs = a.n_seqs * a.heads;                             \
+    const uint32_t scans = (pairs + 7) / 8 * 8 * n_units;                                   \
+    if (convs && blockIdx.x >= scans) {                                                     \
       const uint32_t pair = blockIdx.x - scans;                                             \
       conv_states(a, pair / a.heads, pair % a.heads);                                       \
       return;                                                                               \
     }                                                                                       \
-    const uint32_t pair = blockIdx.x / (8 * kGroups) * 8 + blockIdx.x % 8;                  \
-    if (pair < pairs)                                                                       \
-      scan<T, tiles>(a, pair / a.heads, pair % a.heads, blockIdx.x / 8 % kGroups, lds);     \
+    const uint32_t pair = blockIdx.x / (8 * n_units) * 8 + blockIdx.x % 8;                  \
+    if (pair < pairs) call(a, pair / a.heads, pair % a.heads, blockIdx.x / 8 % n_units, lds); \
   }
 #define HKV_CHUNKS(suffix, T)                                                               \
   extern "C" __global__ __launch_bounds__(kFormThreads, 4) void hkv_kda_form_##suffix(      \
@@ -1516,8 +1657,10 @@ HKV_TOKENS_DIMS(fp32, Fp32)
     if (slot >= (uint32_t)a.first_chunk[2 * a.n_seqs] || a.chunks[slot].len == 0) return;   \
     form<T>(a, slot, blockIdx.x % a.heads, lds);                                            \
   }                                                                                         \
-  HKV_SCAN(hkv_kda_scan_##suffix##_16, T, 1)                                                \
-  HKV_SCAN(hkv_kda_scan_##suffix##_32, T, 2)
+  HKV_SCAN(hkv_kda_scan_##suffix##_16, 1, 8, true, scan_all<T>)                             \
+  HKV_SCAN(hkv_kda_scan_##suffix##_32, 2, 4, true, scan_all<T>)                             \
+  HKV_SCAN(hkv_kda_scan_first_##suffix, 1, 8 * (2 * a.parts - 3), true, scan_first<T>)      \
+  HKV_SCAN(hkv_kda_scan_rest_##suffix, 1, 8 * (a.parts - 1), false, scan_rest<T>)
 HKV_CHUNKS(bf16, Bf16)
 HKV_CHUNKS(fp16, Fp16)
 #undef HKV_CHUNKS
@@ -1548,13 +1691,25 @@ int launch_prefill(const PrefillArgs& a, int32_t dtype, void* stream) {
     static const void* const kScan[2][2] = {
         {HKV_FN(hkv_kda_scan_bf16_16), HKV_FN(hkv_kda_scan_bf16_32)},
         {HKV_FN(hkv_kda_scan_fp16_16), HKV_FN(hkv_kda_scan_fp16_32)}};
-    const uint32_t tiles = a.n_seqs * a.heads * (kD / 16) > 256 ? 2 : 1;
-    const uint32_t pairs = a.n_seqs * a.heads;
+    static const void* const kFirst[2] = {HKV_FN(hkv_kda_scan_first_bf16),
+                                          HKV_FN(hkv_kda_scan_first_fp16)};
+    static const void* const kRest[2] = {HKV_FN(hkv_kda_scan_rest_bf16),
+                                         HKV_FN(hkv_kda_scan_rest_fp16)};
+    const uint32_t pairs = a.n_seqs * a.heads, pairs8 = (pairs + 7) / 8 * 8;
     e = hipLaunchKernel(kForm[dtype], dim3(a.max_chunks * a.heads), dim3(kFormThreads), params, 0,
                         st);
     if (e != hipSuccess) return (int)e;
-    e = hipLaunchKernel(kScan[dtype][tiles - 1], dim3((pairs + 7) / 8 * 8 * (kD / 16 / tiles) + pairs),
-                        dim3(kScanThreads), params, 0, st);
+    if (a.parts > 1) {
+      e = hipLaunchKernel(kFirst[dtype], dim3(pairs8 * 8 * (2 * a.parts - 3) + pairs),
+                          dim3(kScanThreads), params, 0, st);
+      if (e != hipSuccess) return (int)e;
+      e = hipLaunchKernel(kRest[dtype], dim3(pairs8 * 8 * (a.parts - 1)), dim3(kScanThreads),
+                          params, 0, st);
+    } else {
+      const uint32_t tiles = a.column_tiles;
+      e = hipLaunchKernel(kScan[dtype][tiles - 1], dim3(pairs8 * (8 / tiles) + pairs),
+                          dim3(kScanThreads), params, 0, st);
+    }
     if (e != hipSuccess || a.short_tokens == 0) return (int)e;
   }
   return (int)hipLaunchKernel(kTokens[dtype][i], dim3(a.heads, a.n_seqs), dim3(64u << i), params,

@@ -210,13 +210,20 @@ hkv_status plan_prefill(const hkv_layout* layout, const hkv_kda_prefill_args* a,
   // In chunks where that pays (and is built): not for runs of a few tokens.
   k->short_tokens = k->n_seqs > 1 ? hkv::kPrefillShort : 0;
   k->chunked = d == (int64_t)hkv::kPrefillChunkDim && taps == 4 && es == 2 &&
-               k->max_seq_tokens > hkv::kPrefillShort;
+               k->max_seq_tokens > (k->n_seqs > 1 ? hkv::kPrefillTokens
+                                                  : hkv::kPrefillTokensOne);
   k->planned = k->chunked || k->n_seqs > hkv::kPrefillLookThrough;
   // A sequence's blocks are cut each on its own: the last chunk of the first, of
   // the last and of every whole block may be short.
   if (k->chunked)
     k->max_chunks = k->n_tokens / hkv::kPrefillChunk + k->n_tokens / k->block_tokens + 2 * k->n_seqs;
-  *w = hkv::prefill_workspace(k->n_seqs, k->max_chunks, k->heads);
+  const uint32_t pairs = k->n_seqs * k->heads;
+  k->column_tiles = pairs * 8 > 256 ? 2 : 1;
+  k->parts = 1;
+  if (k->chunked && pairs <= hkv::kPrefillPartPairs &&
+      k->max_seq_tokens >= hkv::kPrefillPartTokens)
+    k->parts = std::min<uint32_t>(8, std::max<uint32_t>(3, 48 / pairs));
+  *w = hkv::prefill_workspace(k->n_seqs, k->max_chunks, k->heads, k->parts);
   return HKV_OK;
 }
 
@@ -305,6 +312,7 @@ hkv_status prefill(const hkv_layout* layout, void* pool, const hkv_kda_prefill_a
   k.first_chunk = reinterpret_cast<int32_t*>(wsb + w.first_chunk);
   k.chunks = reinterpret_cast<hkv::PrefillChunk*>(wsb + w.chunks);
   k.records = wsb + w.records;
+  k.made = reinterpret_cast<float*>(wsb + w.made);
   int dev = 0;
   st = stream_device(reinterpret_cast<hipStream_t>(stream), &dev);
   if (st != HKV_OK) return st;

@@ -353,3 +353,70 @@ def test_many_sequences():
     new = [(i * 5) % 4 for i in range(150)]
     new[10], new[77], new[149] = 90, 130, 66
     Case(new, src=[None if i % 4 == 0 else "other" for i in range(150)], heads=1, d=64, seed=36, block_size=96).run()
+
+
+@pytest.mark.parametrize("heads", [1, 3, 16])
+def test_long_runs_in_parts(heads):
+    """Few heads and long runs: what parts of a run make of a state is joined."""
+    Case([1300], heads=heads, seed=37, block_size=960 if heads == 16 else 480, at=[100], src=["own"]).run()
+
+
+def test_parts_beside_short_runs():
+    Case([1250, 0, 700, 3, 90, 1], at=[0, 5, 300, 0, 200, 7], src=["other", "other", None, "own", "own", None],
+         heads=2, seed=38, block_size=320, null=[(0, 1), (2, 2)], lead=1, tail=9).run()
+
+
+def test_parts_with_strong_and_no_decays():
+    for decay, beta in ((0.0, (0.0, 2.0)), (40.0, (0.0, 1.0)), (0.0, (2.0, 2.0))):
+        Case([1400], heads=1, seed=39, decay=decay, beta=beta).run()
+    c = Case([1400], heads=1, seed=40, decay=0.05)
+    c.log_decay[500] = -math.inf
+    c.run()
+
+
+def test_parts_of_refused_runs():
+    c = Case([1300, 1250, 600, 40], heads=1, block_size=320, seed=41)
+    c.src[0] = c.pool.blocks
+    c.table[2, 1] = c.table[3, 0]
+    c.refused = {0, 2, 3}
+    c.upload()
+    c.run()
+
+
+def test_parts_keep_infinities_in_their_column():
+    c = Case([1300], heads=2, seed=42)
+    c.rec()[int(c.src[0]), 0, 3, 5] = math.inf
+    c.enqueue()
+    torch.cuda.synchronize()
+    out = c.out.float().cpu().view(1300, 2, 128)
+    assert not out[:, 0, 5].isfinite().any()
+    out[:, 0, 5] = 0
+    assert out.isfinite().all()
+
+
+def test_many_pairs():
+    """Enough heads that a workgroup scans two column tiles."""
+    Case([70, 5, 130, 64], heads=12, seed=43, lead=2, tail=3).run()
+
+
+def test_parts_captured_and_replayed():
+    """A captured call whose lengths change: parts that were full are empty, and back."""
+    c = Case([1300, 60], at=[0, 30], heads=1, seed=44, block_size=320, tail=200)
+    for a in (c.x, c.log_decay, c.beta):
+        a[1360:] = a[:200]
+    before = c.pool.bytes.clone()
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    c.enqueue()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        c.enqueue()
+    for new in ([1300, 60], [30, 100], [700, 10], [1300, 200]):
+        c.pool.bytes.copy_(before)
+        c.new = list(new)
+        c.starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        c.d_starts.copy_(torch.from_numpy(c.starts))
+        c.out.fill_(7.0)
+        torch.cuda.synchronize()
+        want = c.expect()
+        g.replay()
+        c.compare(want)
