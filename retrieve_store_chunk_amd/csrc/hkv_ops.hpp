@@ -231,9 +231,7 @@ constexpr uint32_t kPrefillRecord = 3 * 32768 + 12288 + 32768 + 1024;  // bytes 
 // runs of up to kPrefillShort (a call of one sequence has no launch for them).
 constexpr uint32_t kPrefillTokens = 24, kPrefillTokensOne = 16;
 constexpr uint32_t kPrefillShort = 2;
-// Calls of at most so many (sequence, head) pairs whose longest run has at least so many
-// tokens cut their sequences' chunks into parts.
-constexpr uint32_t kPrefillPartPairs = 16, kPrefillPartTokens = 1200;
+constexpr uint32_t kPrefillPartTokens = 1200;  // of the longest run, from which on it is cut
 
 // Up to so many sequences are looked through by every workgroup of the token-by-token
 // kernel itself: a launch less.

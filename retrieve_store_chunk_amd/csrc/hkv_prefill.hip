@@ -1152,15 +1152,16 @@ __device__ __forceinline__ Terms8 read_terms(const uint8_t* p, uint32_t at) {
 }
 
 // The part of a sequence that a workgroup goes through: chunks c0 .. c1 - 1 from
-//   kSource    the source page's state,
-//   kIdentity  the unit matrix, without V, and kNothing, zeros: what the part makes of any
-//              state S before it, M S + B, goes to `end`,
-//   kJoined    the state before it, joined from what `parts` parts made.
-enum Start { kSource, kIdentity, kNothing, kJoined };
+//   kSource  the source page's state, or
+//   kJoined  the state before it, joined from what `parts` parts made.
+// Without outputs (two column tiles, both of the same columns): what the part makes of any
+// state S before it, M S + B, where B's tile starts from zeros and M's from the unit
+// matrix, without V.
+enum Start { kSource, kJoined, kNothing };
 struct Part {
   Start start;
   uint32_t c0, c1;
-  float* end;         // [kD][kD] the state behind the part, or nullptr
+  float* end;         // [kCt][kD][kD] the state behind the part (B and M), or nullptr
   const float* made;  // [parts][2][kD][kD]: B and M of each part before
   uint32_t parts;
 };
@@ -1171,7 +1172,7 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
   using E = typename T::type;
   const uint32_t w = wave_index(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int32_t row0 = a.starts[s], n = a.starts[s + 1] - row0;
-  const uint32_t col0 = group * kCt * 16;
+  const uint32_t col0 = group * (kOut ? kCt : 1) * 16;
   E* const out = static_cast<E*>(a.out) + (int64_t)h * kD + col0 + lg * 4;
   if (a.status[s] == hkv::kPrefillRefused) {
     if (kOut)
@@ -1201,8 +1202,7 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
       for (uint32_t ct = 0; ct < kCt; ++ct)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bool one = part.start == kIdentity &&
-                           w * 32 + i * 16 + lg * 4 + j == col0 + ct * 16 + lr;
+          const bool one = !kOut && ct == 1 && w * 32 + i * 16 + lg * 4 + j == col0 + lr;
           st[i][ct][j] = one ? 1.0f : 0.0f;
           if (from) st[i][ct][j] = from[(i * 16 + j) * kD + ct * 16];
         }
@@ -1221,10 +1221,10 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
   auto fetch_u = [&](const uint8_t* r) {
 #pragma unroll
     for (uint32_t ct = 0; ct < kCt; ++ct)
-      if (!kOut && part.start == kIdentity)
+      if (!kOut && ct == 1)
         u0[ct] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
       else
-        u0[ct] = *(const HKV_GLOBAL v4f*)(r + kRecU + ((group * kCt + ct) * 4 + w) * 1024 + at);
+        u0[ct] = *(const HKV_GLOBAL v4f*)(r + kRecU + ((col0 / 16 + ct) * 4 + w) * 1024 + at);
   };
   auto fetch_k = [&](const uint8_t* r, uint32_t i, uint32_t kb) {
     kf[i][kb] = read_terms(r + kRecK + ((w * 2 + i) * 2 + kb) * 2048, at);
@@ -1241,7 +1241,7 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
   auto fetch_e = [&](const uint8_t* r) {
 #pragma unroll
     for (uint32_t ct = 0; ct < kCt; ++ct)
-      ve[ct] = !kOut && part.start == kIdentity
+      ve[ct] = !kOut && ct == 1
                    ? -1000
                    : *(const HKV_GLOBAL int32_t*)(r + kRecExps + (col0 + ct * 16) * 4 + lr * 4);
   };
@@ -1502,7 +1502,8 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
       for (uint32_t ct = 0; ct < kCt; ++ct)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          p[(i * 16 + j) * kD + ct * 16] = __builtin_ldexpf(st[i][ct][j], -e[ct]);
+          p[(kOut ? ct * 16 : ct * kD * kD) + (i * 16 + j) * kD] =
+              __builtin_ldexpf(st[i][ct][j], -e[ct]);
   }
 }
 
@@ -1514,7 +1515,7 @@ __device__ __forceinline__ bool scanned(const hkv::PrefillArgs& a, uint32_t s) {
 
 template <class T, uint32_t kCt>
 __device__ __forceinline__ void scan_all(const hkv::PrefillArgs& a, uint32_t s, uint32_t h,
-                                         uint32_t group, ScanShared<kCt>& lds) {
+                                         uint32_t, uint32_t group, ScanShared<kCt>& lds) {
   if (!scanned(a, s)) return;
   const Part part = {kSource, 0, (uint32_t)a.first_chunk[s + a.n_seqs], nullptr, nullptr, 0};
   scan<T, kCt, true>(a, s, h, group, part, lds);
@@ -1531,34 +1532,28 @@ __device__ __forceinline__ float* made_by(const hkv::PrefillArgs& a, uint32_t s,
                                           uint32_t part) {
   return a.made + (((uint64_t)s * a.heads + h) * (a.parts - 1) + part) * 2 * kD * kD;
 }
-// unit: 8 column groups of the first part, then for each other but the last those of B and
-// of M.
 template <class T>
 __device__ __forceinline__ void scan_first(const hkv::PrefillArgs& a, uint32_t s, uint32_t h,
-                                           uint32_t unit, ScanShared<1>& lds) {
+                                           uint32_t which, uint32_t group, ScanShared<2>& lds) {
   if (!scanned(a, s)) return;
-  const uint32_t group = unit % 8, x = unit / 8, which = (x + 1) / 2;
   const uint32_t count = (uint32_t)a.first_chunk[s + a.n_seqs], each = part_chunks(a, count);
   Part part = {};
   part.c0 = which * each;
   part.c1 = min(part.c0 + each, count);
+  if (part.c1 < count) part.end = made_by(a, s, h, which);
   if (which == 0) {
     part.start = kSource;
-    if (part.c1 < count) part.end = made_by(a, s, h, 0);
-    scan<T, 1, true>(a, s, h, group, part, lds);
-    return;
+    scan<T, 1, true>(a, s, h, group, part, reinterpret_cast<ScanShared<1>&>(lds));
+  } else if (part.c1 < count) {
+    part.start = kNothing;
+    scan<T, 2, false>(a, s, h, group, part, lds);
   }
-  if (part.c1 >= count) return;  // no part behind this one
-  const bool is_m = x % 2 == 0;
-  part.start = is_m ? kIdentity : kNothing;
-  part.end = made_by(a, s, h, which) + (is_m ? kD * kD : 0);
-  scan<T, 1, false>(a, s, h, group, part, lds);
 }
 template <class T>
 __device__ __forceinline__ void scan_rest(const hkv::PrefillArgs& a, uint32_t s, uint32_t h,
-                                          uint32_t unit, ScanShared<1>& lds) {
+                                          uint32_t set, uint32_t group, ScanShared<1>& lds) {
   if (!scanned(a, s) || a.status[s] != hkv::kPrefillRuns) return;
-  const uint32_t group = unit % 8, which = unit / 8 + 1;
+  const uint32_t which = set + 1;
   const uint32_t count = (uint32_t)a.first_chunk[s + a.n_seqs], each = part_chunks(a, count);
   Part part = {};
   part.c0 = which * each;
@@ -1573,9 +1568,10 @@ __device__ __forceinline__ void scan_rest(const hkv::PrefillArgs& a, uint32_t s,
 // The conv states of a sequence's blocks, a head's channels by one workgroup: it reads the
 // source's before it writes any, since the source may be one of the blocks.
 __device__ __forceinline__ void conv_states(const hkv::PrefillArgs& a, uint32_t s, uint32_t h) {
-  if (a.status[s] != hkv::kPrefillRuns) return;
+  if (a.status[s] != hkv::kPrefillRuns || !scanned(a, s)) return;
   const int32_t src = a.src[s], row0 = a.starts[s];
-  const uint32_t slot0 = (uint32_t)a.first_chunk[s], count = (uint32_t)a.first_chunk[s + a.n_seqs];
+  const Span me = span_of(a, s);
+  const int32_t* const own = a.table + (int64_t)s * a.table_stride;
   constexpr uint32_t kEach = (3 * kD + kScanThreads - 1) / kScanThreads;
   uint16_t old[kEach][3];
 #pragma unroll
@@ -1588,16 +1584,18 @@ __device__ __forceinline__ void conv_states(const hkv::PrefillArgs& a, uint32_t 
                       ? 0
                       : reinterpret_cast<const uint16_t*>(a.pages + (uint64_t)src * a.stride)[ch * 3 + j];
   }
-  for (uint32_t c = 0; c < count; ++c) {
-    const hkv::PrefillChunk ck = read_chunk(a, slot0 + c);
-    if (ck.dst < 0) continue;
-    const int32_t done = ck.off + ck.len;
+  for (uint32_t b = me.first; b <= me.last; ++b) {
+    const int32_t dst = own[b];
+    if (dst < 0) continue;
+    // tokens up to the block's end, or the last
+    const int32_t done =
+        b < me.last ? (int32_t)((b + 1) * a.block_tokens) - me.position : me.tokens;
 #pragma unroll
     for (uint32_t i = 0; i < kEach; ++i) {
       const uint32_t m = threadIdx.x + i * kScanThreads;
       if (m >= 3 * kD) break;
       const uint64_t ch = ((uint64_t)(m / kD) * a.heads + h) * kD + m % kD;
-      uint16_t* const to = reinterpret_cast<uint16_t*>(a.pages + (uint64_t)ck.dst * a.stride) + ch * 3;
+      uint16_t* const to = reinterpret_cast<uint16_t*>(a.pages + (uint64_t)dst * a.stride) + ch * 3;
 #pragma unroll
       for (int j = 0; j < 3; ++j) {
         const int32_t k = done - 3 + j;  // of the sequence's tokens
@@ -1634,20 +1632,23 @@ HKV_TOKENS_DIMS(fp32, Fp32)
 #undef HKV_TOKENS
 #undef HKV_TOKENS_DIMS
 
-// Workgroups of a (sequence, head) pair, `units` of them, lie 8 apart: on one XCD, which
-// reads the pair's records once.  The conv states' workgroups come last.
-#define HKV_SCAN(name, tiles, units, convs, call)                                           \
+// The column groups of one part of a (sequence, head) pair lie 8 workgroups apart: on one
+// XCD, which reads the part's records once.  The conv states' workgroups come last.
+#define HKV_SCAN(name, tiles, columns, sets, convs, call)                                   \
   extern "C" __global__ __launch_bounds__(kScanThreads, 2) void name(hkv::PrefillArgs a) {  \
     __shared__ ScanShared<tiles> lds;                                                       \
-    const uint32_t n_units = units, pairs = a.n_seqs * a.heads;                             \
-    const uint32_t scans = (pairs + 7) / 8 * 8 * n_units;                                   \
+    constexpr uint32_t kGroups = kD / (columns);                                            \
+    const uint32_t n_sets = sets, pairs = a.n_seqs * a.heads, items = pairs * n_sets;       \
+    const uint32_t scans = (items + 7) / 8 * 8 * kGroups;                                   \
     if (convs && blockIdx.x >= scans) {                                                     \
       const uint32_t pair = blockIdx.x - scans;                                             \
       conv_states(a, pair / a.heads, pair % a.heads);                                       \
       return;                                                                               \
     }                                                                                       \
-    const uint32_t pair = blockIdx.x / (8 * n_units) * 8 + blockIdx.x % 8;                  \
-    if (pair < pairs) call(a, pair / a.heads, pair % a.heads, blockIdx.x / 8 % n_units, lds); \
+    const uint32_t item = blockIdx.x / (8 * kGroups) * 8 + blockIdx.x % 8;                  \
+    const uint32_t pair = item / n_sets, set = item % n_sets;                               \
+    if (item < items)                                                                       \
+      call(a, pair / a.heads, pair % a.heads, set, blockIdx.x / 8 % kGroups, lds);          \
   }
 #define HKV_CHUNKS(suffix, T)                                                               \
   extern "C" __global__ __launch_bounds__(kFormThreads, 4) void hkv_kda_form_##suffix(      \
@@ -1657,10 +1658,10 @@ HKV_TOKENS_DIMS(fp32, Fp32)
     if (slot >= (uint32_t)a.first_chunk[2 * a.n_seqs] || a.chunks[slot].len == 0) return;   \
     form<T>(a, slot, blockIdx.x % a.heads, lds);                                            \
   }                                                                                         \
-  HKV_SCAN(hkv_kda_scan_##suffix##_16, 1, 8, true, scan_all<T>)                             \
-  HKV_SCAN(hkv_kda_scan_##suffix##_32, 2, 4, true, scan_all<T>)                             \
-  HKV_SCAN(hkv_kda_scan_first_##suffix, 1, 8 * (2 * a.parts - 3), true, scan_first<T>)      \
-  HKV_SCAN(hkv_kda_scan_rest_##suffix, 1, 8 * (a.parts - 1), false, scan_rest<T>)
+  HKV_SCAN(hkv_kda_scan_##suffix##_16, 1, 16, 1, true, scan_all<T>)                         \
+  HKV_SCAN(hkv_kda_scan_##suffix##_32, 2, 32, 1, true, scan_all<T>)                         \
+  HKV_SCAN(hkv_kda_scan_first_##suffix, 2, 16, a.parts - 1, true, scan_first<T>)            \
+  HKV_SCAN(hkv_kda_scan_rest_##suffix, 1, 16, a.parts - 1, false, scan_rest<T>)
 HKV_CHUNKS(bf16, Bf16)
 HKV_CHUNKS(fp16, Fp16)
 #undef HKV_CHUNKS
@@ -1695,19 +1696,22 @@ int launch_prefill(const PrefillArgs& a, int32_t dtype, void* stream) {
                                           HKV_FN(hkv_kda_scan_first_fp16)};
     static const void* const kRest[2] = {HKV_FN(hkv_kda_scan_rest_bf16),
                                          HKV_FN(hkv_kda_scan_rest_fp16)};
-    const uint32_t pairs = a.n_seqs * a.heads, pairs8 = (pairs + 7) / 8 * 8;
+    const uint32_t pairs = a.n_seqs * a.heads;
+    auto groups = [&](uint32_t sets, uint32_t tiles) {
+      return (pairs * sets + 7) / 8 * 8 * (kD / 16 / tiles);
+    };
     e = hipLaunchKernel(kForm[dtype], dim3(a.max_chunks * a.heads), dim3(kFormThreads), params, 0,
                         st);
     if (e != hipSuccess) return (int)e;
     if (a.parts > 1) {
-      e = hipLaunchKernel(kFirst[dtype], dim3(pairs8 * 8 * (2 * a.parts - 3) + pairs),
+      e = hipLaunchKernel(kFirst[dtype], dim3(groups(a.parts - 1, 1) + pairs),
                           dim3(kScanThreads), params, 0, st);
       if (e != hipSuccess) return (int)e;
-      e = hipLaunchKernel(kRest[dtype], dim3(pairs8 * 8 * (a.parts - 1)), dim3(kScanThreads),
+      e = hipLaunchKernel(kRest[dtype], dim3(groups(a.parts - 1, 1)), dim3(kScanThreads),
                           params, 0, st);
     } else {
       const uint32_t tiles = a.column_tiles;
-      e = hipLaunchKernel(kScan[dtype][tiles - 1], dim3(pairs8 * (8 / tiles) + pairs),
+      e = hipLaunchKernel(kScan[dtype][tiles - 1], dim3(groups(1, tiles) + pairs),
                           dim3(kScanThreads), params, 0, st);
     }
     if (e != hipSuccess || a.short_tokens == 0) return (int)e;

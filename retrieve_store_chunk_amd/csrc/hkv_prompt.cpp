@@ -217,12 +217,17 @@ hkv_status plan_prefill(const hkv_layout* layout, const hkv_kda_prefill_args* a,
   // the last and of every whole block may be short.
   if (k->chunked)
     k->max_chunks = k->n_tokens / hkv::kPrefillChunk + k->n_tokens / k->block_tokens + 2 * k->n_seqs;
+  // A launch has at most 2^32 threads: 512 for a chunk and head, 8 x 256 for a sequence
+  // and head.
+  if ((uint64_t)k->max_chunks * k->heads > (1u << 23) - 1 ||
+      (uint64_t)k->n_seqs * k->heads > (1u << 20))
+    return set_error(HKV_E_ARG, "too many heads for so many tokens or sequences; split the batch");
   const uint32_t pairs = k->n_seqs * k->heads;
   k->column_tiles = pairs * 8 > 256 ? 2 : 1;
   k->parts = 1;
-  if (k->chunked && pairs <= hkv::kPrefillPartPairs &&
-      k->max_seq_tokens >= hkv::kPrefillPartTokens)
-    k->parts = std::min<uint32_t>(8, std::max<uint32_t>(3, 48 / pairs));
+  const uint32_t fit = 256 / (pairs * 8 > 0 ? pairs * 8 : 1) + 1;  // one workgroup a CU
+  if (k->chunked && fit >= 4 && k->max_seq_tokens >= hkv::kPrefillPartTokens)
+    k->parts = std::min<uint32_t>(fit, 8);
   *w = hkv::prefill_workspace(k->n_seqs, k->max_chunks, k->heads, k->parts);
   return HKV_OK;
 }

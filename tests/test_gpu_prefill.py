@@ -420,3 +420,68 @@ def test_parts_captured_and_replayed():
         want = c.expect()
         g.replay()
         c.compare(want)
+
+
+def test_strides_of_chunks():
+    """Rows at odd elements, one row for all, padded outputs, where runs go in chunks."""
+    c = Case([90, 9], heads=2, seed=45)
+    hd, tokens = 256, 99
+    x = torch.full((tokens, 3 * hd + 5), 9.0, dtype=c.dt, device="cuda")
+    x[:, 3:3 * hd + 3] = c.x
+    c.x = x[:, 3:3 * hd + 3]
+    g = torch.full((tokens, hd + 3), 9.0, device="cuda")
+    g[:, 1:hd + 1] = c.log_decay
+    c.log_decay = g[:, 1:hd + 1]
+    c.beta = torch.cat([c.beta, c.beta], 1)[:, :2]
+    out = torch.full((tokens, hd + 12), 7.0, dtype=c.dt, device="cuda")
+    c.out = out[:, :hd]
+    table = torch.full((2, 5), 0x7FFFFFFF, dtype=torch.int32, device="cuda")
+    table[:, :c.columns] = c.d_table
+    c.d_table = table
+    c.run()
+    assert (out[:, hd:] == 7.0).all()
+
+
+def test_records_past_4_gib():
+    """One call whose workspace passes 2^32 bytes against two calls that follow each
+    other, cut where a block ends, so that both have the same chunks."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GiB")
+    heads, n = 32, 1888
+    first, second = 17 * n, 18 * n
+    c = Case([8], heads=heads, seed=46, block_size=n, spare=3)
+    hd, tokens = heads * 128, first + second
+    gen = torch.Generator(device="cuda").manual_seed(46)
+    c.x = torch.randn(tokens, 3 * hd, device="cuda", generator=gen, dtype=c.dt)
+    c.log_decay = -torch.rand(tokens, hd, device="cuda", generator=gen) ** 3
+    c.beta = torch.rand(tokens, heads, device="cuda", generator=gen)
+    c.out = torch.zeros(tokens, hd, dtype=c.dt, device="cuda")
+    c.columns = 35
+    end, cut = int(c.table[0, 0]), [b for b in range(c.pool.blocks) if b not in (c.table[0, 0], c.src[0])][0]
+    c.table = np.full((1, 35), -1, np.int32)   # only two snapshots are kept
+    c.table[0, 16], c.table[0, 34] = cut, end
+    before = c.pool.bytes.clone()
+
+    def call(at, rows, src):
+        c.at, c.src, c.starts, c.most = [at], np.array([src]), np.array(rows), rows[1] - rows[0]
+        c.new = [c.most]
+        c.upload()
+        c.enqueue()
+        torch.cuda.synchronize()
+
+    src = int(c.src[0])
+    call(0, [0, tokens], src)
+    assert c.workspace.numel() > 1 << 32
+    out, pool = c.out.clone(), c.pool.bytes.clone()
+    c.pool.bytes.copy_(before)
+    c.out.zero_()
+    call(0, [0, first], src)
+    call(first, [first, tokens], cut)
+    mine, c.pool.bytes = c.pool.bytes, pool
+    states = [c.rec()[b].double() for b in (cut, end)]
+    c.pool.bytes = mine
+    for want, b in zip(states, (cut, end)):
+        got = c.rec()[b].double()
+        assert float((got - want).norm() / want.norm()) < 2e-6, b   # two states' 2^-20 each
+    off = (c.out.double() - out.double()).norm() / out.double().norm()
+    assert float(off) < 2.0 ** -9

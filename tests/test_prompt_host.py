@@ -7,6 +7,7 @@ import re
 import pytest
 
 import retrieve_store_chunk_amd as hkv
+import workloads as W
 from tests.test_ops_host import POOL, WS, layout, needs_no_gpu
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -143,6 +144,16 @@ def test_workspaces_follow_the_call():
     assert lay.kda_prefill_workspace(prefill_args(n_seqs=4096, n_tokens=1 << 20, max_seq_tokens=1 << 20)) >= size
     for bad in (dict(n_seqs=-1), dict(n_tokens=-1), dict(max_blocks=0)):
         assert hkv.status_of(lay.kda_prefill_workspace, prefill_args(**bad)) == hkv.HKV_E_ARG
+
+
+def test_heads_that_no_launch_holds_are_refused():
+    heads = 1024
+    desc = W._desc([0, 1], heads, 128, 3 * heads * 128, 2, 0, 1 << 40)
+    lay = hkv.Layout(desc)
+    args = dict(n_tokens=1 << 20, max_seq_tokens=1 << 20, max_blocks=1)
+    assert hkv.status_of(lay.kda_prefill_workspace, prefill_args(n_seqs=1, **args)) == hkv.HKV_E_ARG
+    assert hkv.status_of(lay.kda_prefill_workspace, prefill_args(n_seqs=4096, n_tokens=9, max_seq_tokens=9)) == hkv.HKV_E_ARG
+    assert lay.kda_prefill_workspace(prefill_args(n_seqs=8, n_tokens=5000, max_seq_tokens=900)) > 1 << 33
 
 
 def test_the_header_declares_them():
