@@ -671,11 +671,12 @@ hkv_status hkv_mla_append(const hkv_layout* layout, void* pool, const hkv_mla_ap
  * HKV_NULL_BLOCK is not written (snapshots that are not kept).  The source may
  * be one of the sequence's own blocks.  A sequence without new tokens reads and
  * writes nothing.
- * Sums, norms, decays and states are fp32.  Long runs are computed in chunks of
- * up to 64 tokens whose products take each operand as two fp16 terms (22 bits),
- * so a state differs from the token-by-token one by about 1e-6 of its column's
- * size; there, a NaN or an infinity may also reach outputs of its head up to 63
- * rows before it. */
+ * Sums, norms, decays and states are fp32.  Longer runs of heads of 128 with
+ * conv_kernel 4 in bf16 or fp16 are computed in chunks of up to 64 tokens, whose
+ * products take each operand as two fp16 terms (22 bits): a column of the state
+ * is off from the token-by-token one by about 1e-6 of the largest value that it, or
+ * the values v that it takes in, had in the chunk and the one before.  There, a
+ * NaN or an infinity may also reach outputs of its head up to 63 rows before it. */
 typedef struct hkv_kda_prefill_args {
   int32_t layer;             /* a KDA layer */
   int32_t n_seqs;            /* 0..4096; 0 is a no-op */
@@ -703,8 +704,12 @@ typedef struct hkv_kda_prefill_args {
   int64_t out_stride;        /* elements, a multiple of 4, >= heads x d */
 } hkv_kda_prefill_args;
 
-/* Device workspace bytes of a call with these shapes (n_seqs, n_tokens,
- * max_seq_tokens, dtype; pointers are not read).  Errors: HKV_E_ARG. */
+/* Device workspace bytes of a call with these shapes (n_seqs, max_blocks,
+ * table_stride, n_tokens, max_seq_tokens, dtype; pointers are not read).  In chunks
+ * it is mostly 141 KiB for each head of each of the C = n_tokens / 64 + n_tokens / N +
+ * 2 n_seqs chunks that there may be (N: tokens of a block), about 2.2 KB a token and
+ * head for long runs.  Errors: HKV_E_ARG (also where C x heads is over 2^23 - 1 in
+ * chunks, or n_seqs x heads over 2^20). */
 hkv_status hkv_kda_prefill_workspace(const hkv_layout* layout, const hkv_kda_prefill_args* args,
                                      size_t* bytes);
 

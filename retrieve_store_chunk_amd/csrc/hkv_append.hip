@@ -8,7 +8,10 @@
 // queries' rotary parts are independent 16-byte pieces, four a thread, in
 // workgroups behind those of the rows.
 //
-// Bound: reading and writing each row and query once, a launch where they are few.
+// Bound: reading and writing each row and query once, a launch where they are few (us of
+// the kernel): 15813 tokens, 32 heads, bf16 (170 MB) 35, 4.8 TB/s, the rate of a large
+// copy; 5491 tokens, 64 heads, e4m3 (101 MB) 21; 255 sequences of one token, 16 heads 5.5; one
+// 3.1.
 #include <hip/hip_runtime.h>
 
 #include "hkv.h"

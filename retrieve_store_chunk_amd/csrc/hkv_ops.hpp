@@ -227,14 +227,22 @@ constexpr uint32_t kPrefillChunk = 64;       // tokens
 constexpr uint32_t kPrefillChunkDim = 128;   // the head dim that is computed in chunks
 constexpr uint32_t kPrefillRecord = 3 * 32768 + 12288 + 32768 + 1024;  // bytes of a chunk and head
 
-// Calls whose longest run has up to so many tokens go token by token; in others,
-// runs of up to kPrefillShort (a call of one sequence has no launch for them).
+// Calls whose longest run has up to so many tokens go token by token (us, token by token
+// and in chunks: 61 runs of up to 16 tokens, 6 heads 43, 66; 24 60, 72; 32 76, 73; one run
+// of 12 20, 27; 16 25, 26; 20 31, 27).  In others, runs of up to kPrefillShort do, in a
+// launch of their own (24 runs of one token beside 4 prompts of up to 1400, 32 heads: 256
+// us; 331 with all in chunks; 61 runs of up to 12, all in chunks but those: 73 with 2, 74 with
+// 4, 65 with 8; of up to 16 66, 72 and 69; of up to 32 73, 72 and 83).  A call of one sequence has no such launch.
 constexpr uint32_t kPrefillTokens = 24, kPrefillTokensOne = 16;
 constexpr uint32_t kPrefillShort = 2;
-constexpr uint32_t kPrefillPartTokens = 1200;  // of the longest run, from which on it is cut
+// Runs are cut into parts where that makes at least 4 with one workgroup a CU, from so many
+// tokens of the longest on (us in all, one part and cut: 1500 tokens, 6 heads 64, 60; 16384
+// 488, 279 to 291; with 16 heads, which leave room for 3 parts, 1887 tokens 83, 80, and 90 in 4).  8 at most.
+constexpr uint32_t kPrefillPartTokens = 1200;
 
 // Up to so many sequences are looked through by every workgroup of the token-by-token
-// kernel itself: a launch less.
+// kernel itself, a launch less (us with and without: 61 of one token, 6 heads 12.8, 16.5;
+// 256 42.4, 43.0; 256 of 16 heads 128.6, 125.7; 512 of 16 heads 240, 232; 1000 of 6 196, 183).
 constexpr uint32_t kPrefillLookThrough = 256;
 
 struct PrefillChunk {

@@ -1,5 +1,17 @@
 // The KDA layers' prompt form: many tokens of each sequence, from the state
 // page of one block to the pages of the sequence's blocks (gfx950).
+//
+// Short runs go token by token (`tokens`), heads of 128 in longer runs by chunks of up
+// to 64 tokens (`form`, then `scan`); other head dims, conv kernels but 4 and fp32
+// inputs always go token by token.  `plan` looks the sequences through.
+//
+// Bound: the inputs, outputs and pages for short runs (61 runs of up to 5 tokens, 6 heads:
+// 20 us for 50 MB; a longer run takes 1.2 to 1.4 us a token, its chain); for chunks
+// `form`'s arithmetic and, where a sequence has few heads, `scan`'s chain from chunk to
+// chunk.  Measured (us, form + scan): 1500 tokens, 6 heads 24 + 31; 1887 tokens, 16 heads
+// 34 + 45; 16384 tokens, 6 heads 88 + 202 (in parts); 20011 tokens, 32 heads 532 to 592
+// + 705; 16 runs of up to 2000, 32 heads 487 to 583 + 446, for 1.0 GB each, of which a copy
+// at 4.7 TB/s would take 0.21 ms.
 #include <hip/hip_runtime.h>
 
 #include "hkv.h"
@@ -208,7 +220,8 @@ __device__ __forceinline__ float sum_wave(float x) {
 // from token to token: one workgroup per (head, sequence), a wave for 16 columns.
 // Thread t has 4 columns of kDim / 16 rows, so that the sums over rows stay within a
 // wave, and one channel of the conv or of the decays; the only thing that the waves
-// exchange is a token's q, k, v and decays: one barrier a token.
+// exchange is a token's q, k, v and decays: one barrier a token (61 runs of up to
+// 5 tokens, 6 heads: 20 us; the form before, without this split, 28).
 template <class T, uint32_t kDim>
 __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
   using E = typename T::type;
@@ -392,7 +405,14 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
 // summed one by one in fp32.  Products of matrices run in fp16 with each operand as two terms, hi +
 // lo (22 bits), and three products (lo lo is below 2^-22); what is scaled by a
 // power of two to lie well inside fp16's range says so.  V's and S's columns never
-// mix, so each has a power of two of its own.
+// mix, so each has a power of two of its own.  (Two bf16 terms would have
+// 16 bits.)
+//
+// `form`: one workgroup of eight waves a chunk and head, a wave 8 tokens, a lane two
+// channels.  With 20011 tokens of 32 heads a wave has 2290 vector instructions and waits 37%
+// of its cycles, LDS is active in 37% of a CU's (37% of that are conflicts), the matrix
+// units in 11%.  Four waves of 16 tokens, with the halves of 16 tokens pair by pair, took
+// 569 us there where this split first took 554.  Two workgroups a CU: 80 KB of LDS, 128 registers.
 constexpr uint32_t kD = hkv::kPrefillChunkDim;
 constexpr uint32_t kFormThreads = 512;
 constexpr float kUnit = 64.0f;  // scale of k and q operands (each at most 1 in size)
@@ -1133,6 +1153,12 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
 // goes straight to that wave's registers, a chunk ahead.  What the waves need of each
 // other, the state's and U's terms, goes through LDS, in the order in which
 // products take them: two barriers a chunk.
+//
+// A chunk takes 1.45 us (16 columns), of which 0.75 are the 116 KB that a CU takes in at
+// 64 bytes a cycle; 2.2 us with 256 workgroups at once, which the caches bound.  Before:
+// one wave of 16 columns a workgroup, its operands as they were needed, 13 to 20 us; two
+// waves computing and two staging through LDS 3.4 us.  Operands two chunks ahead were no
+// faster (20011 tokens, 32 heads in all: 1191 us for 1166).
 constexpr uint32_t kScanThreads = 256;
 
 // The state's terms by 32 rows, U's by 32 tokens, the columns' largest values by wave.
@@ -1521,7 +1547,9 @@ __device__ __forceinline__ void scan_all(const hkv::PrefillArgs& a, uint32_t s, 
   scan<T, kCt, true>(a, s, h, group, part, lds);
 }
 
-// Few heads and long sequences: a sequence's chunks in a.parts parts.  First the first
+// Few heads and long sequences: a sequence's chunks in a.parts parts (16384 tokens, 6 heads,
+// in all: 279 to 291 us in 6 parts, 488 in one, 331 in 4, 308 in 8, where workgroups share
+// CUs).  First the first
 // part is gone through, and at the same time the others but the last make M and B; then
 // every other part joins the state before it and is gone through.
 constexpr uint32_t kLeastPart = 6;  // chunks
