@@ -653,7 +653,7 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
   }
 
   // q and k over their norms (16 sums at once, each lane's root goes to all), times
-  // kUnit.
+  // kUnit.  Blanked tokens get a factor of 0: without an eps theirs would be infinite.
   {
     float v[16];
 #pragma unroll
@@ -661,7 +661,8 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
       v[i] = y[0][i][0] * y[0][i][0] + y[0][i][1] * y[0][i][1];
       v[8 + i] = y[1][i][0] * y[1][i][0] + y[1][i][1] * y[1][i][1];
     }
-    const float by = kUnit / sqrtf(sum16(v, lane) + a.eps);
+    const float sum = sum16(v, lane);  // of token lane / 4 % 8
+    const float by = t0 + (int32_t)(lane >> 2 & 7) < len ? kUnit / sqrtf(sum + a.eps) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float nq = real((uint32_t)__builtin_amdgcn_readlane((int)bits(by), 4 * i));
