@@ -1334,45 +1334,47 @@ __device__ __forceinline__ void scan(const hkv::PrefillArgs& a, uint32_t s, uint
 #pragma unroll
   for (uint32_t ct = 0; ct < kCt; ++ct) none[ct] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   // The state before the part: S <- M S + B for each of the parts between the first and
-  // this one.  M's rows lie in memory as they are; a lane takes those of its 8 columns.
-  if (kOut && part.start == kJoined)
-    for (uint32_t x = 1; x < part.parts; ++x) {
-      const float* const b = part.made + (uint64_t)x * 2 * kD * kD;
+  // this one.  In fp32, since a part may be hundreds of chunks long: M's rows, S and B can
+  // lie many powers of two apart, which no exponent of a column covers, and a small row
+  // that stays counts as much as a large one that fades.  The columns of S go through LDS,
+  // four rows 80 floats apart, so that the four lane groups read different banks.
+  if constexpr (kOut) {
+    if (part.start == kJoined) {
+      float* const shared = reinterpret_cast<float*>(&lds);
+      constexpr uint32_t kFour = 80, kTile = kD / 4 * kFour;
+      static_assert(kCt * kTile * sizeof(float) <= sizeof(lds), "a state fits the scan's LDS");
+      for (uint32_t x = 1; x < part.parts; ++x) {
+        const HKV_GLOBAL float* const b =
+            (const HKV_GLOBAL float*)(part.made + (uint64_t)x * 2 * kD * kD);
+        const HKV_GLOBAL float* const m = b + kD * kD + (w * 32 + lr) * kD + lg * 4;
 #pragma unroll
-      for (uint32_t ct = 0; ct < kCt; ++ct) ve[ct] = -1000;
-      put_most(none, 0.0f);
-      __syncthreads();
-      get_most();
-      put_state();
-      __syncthreads();
-      v4f z[2][kCt] = {};
+        for (uint32_t i = 0; i < 2; ++i)
 #pragma unroll
-      for (uint32_t kb = 0; kb < kD / 32; ++kb)
+          for (uint32_t ct = 0; ct < kCt; ++ct)
 #pragma unroll
-        for (uint32_t i = 0; i < 2; ++i) {
-          const HKV_GLOBAL float* const m = (const HKV_GLOBAL float*)(b + kD * kD) +
-                                            (w * 32 + i * 16 + lr) * kD + kb * 32 + lg * 4;
-          const Terms8 mf = terms(*(const HKV_GLOBAL v4f*)m * kUnit,
-                                  *(const HKV_GLOBAL v4f*)(m + 16) * kUnit);
+            for (int j = 0; j < 4; ++j) {
+              shared[ct * kTile + (w * 8 + i * 4 + lg) * kFour + j * 16 + lr] = st[i][ct][j];
+              st[i][ct][j] = b[state_at + (i * 16 + j) * kD + ct * 16];
+            }
+        __syncthreads();
 #pragma unroll
-          for (uint32_t ct = 0; ct < kCt; ++ct) {
-            const v8h hi = lds.s[ct][kb][0][lane], lo = lds.s[ct][kb][1][lane];
-            z[i][ct] = mfma(mf.lo, hi, z[i][ct]);
-            z[i][ct] = mfma(mf.hi, lo, z[i][ct]);
-            z[i][ct] = mfma(mf.hi, hi, z[i][ct]);
-          }
+        for (uint32_t kb = 0; kb < kD / 16; ++kb) {
+          const v4f row[2] = {*(const HKV_GLOBAL v4f*)(m + kb * 16),
+                              *(const HKV_GLOBAL v4f*)(m + 16 * kD + kb * 16)};
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (uint32_t ct = 0; ct < kCt; ++ct) {
+              const float s = shared[ct * kTile + (kb * 4 + lg) * kFour + n * 16 + lr];
+#pragma unroll
+              for (uint32_t i = 0; i < 2; ++i)
+                st[i][ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[i][n], s, st[i][ct], 0, 0, 0);
+            }
         }
-#pragma unroll
-      for (uint32_t i = 0; i < 2; ++i)
-#pragma unroll
-        for (uint32_t ct = 0; ct < kCt; ++ct)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            st[i][ct][j] =
-                z[i][ct][j] * (1.0f / kUnit) +
-                __builtin_ldexpf(((const HKV_GLOBAL float*)(b + state_at))[(i * 16 + j) * kD + ct * 16],
-                                 e[ct]);
+        __syncthreads();
+      }
     }
+  }
   fetch_e(rec);
   fetch_u(rec);
 #pragma unroll
