@@ -215,6 +215,13 @@ __device__ __forceinline__ float sum_wave(float x) {
   return sum_fours(x);
 }
 
+// 1 / sqrt(x).  The instruction takes numbers below 2^-126, where sums of squares without
+// an eps may lie, for 0.
+__device__ __forceinline__ float inverse_root(float x) {
+  const bool tiny = x < 0x1p-126f;
+  return __builtin_amdgcn_rsqf(tiny ? x * 0x1p64f : x) * (tiny ? 0x1p32f : 1.0f);
+}
+
 // ---------------------------------------------------------------- token by token
 // hkv_kda_step's arithmetic with the state and the conv's taps kept in registers
 // from token to token: one workgroup per (head, sequence), a wave for 16 columns.
@@ -350,8 +357,8 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
     qq = sum_wave(qq);
     kk = sum_wave(kk);
     qk = sum_wave(qk);
-    const float nq = a.scale * __builtin_amdgcn_rsqf(qq + a.eps);
-    const float nk = __builtin_amdgcn_rsqf(kk + a.eps);
+    const float nq = a.scale * inverse_root(qq + a.eps);
+    const float nk = inverse_root(kk + a.eps);
 
     float k[kRows];
     v4f sk = {0.0f, 0.0f, 0.0f, 0.0f}, sq = {0.0f, 0.0f, 0.0f, 0.0f};
