@@ -708,14 +708,16 @@ typedef struct hkv_kda_prefill_args {
  * table_stride, n_tokens, max_seq_tokens, dtype; pointers are not read).  In chunks
  * it is mostly 141 KiB for each head of each of the C = n_tokens / 64 + n_tokens / N +
  * 2 n_seqs chunks that there may be (N: tokens of a block), about 2.2 KB a token and
- * head for long runs.  Errors: HKV_E_ARG (also where C x heads is over 2^23 - 1 in
+ * head for long runs; 8 bytes for each of the pool's blocks where n_tokens / N is over 24.
+ * Errors: HKV_E_ARG (also where C x heads is over 2^23 - 1 in
  * chunks, or n_seqs x heads over 2^20). */
 hkv_status hkv_kda_prefill_workspace(const hkv_layout* layout, const hkv_kda_prefill_args* args,
                                      size_t* bytes);
 
 /* Enqueues the prefill (see above).  Needs of the layout what hkv_kda_step
  * needs; pool, out and workspace are 16-byte aligned, the other arrays by their
- * element.  The result of a call depends on its inputs alone (no atomics).
+ * element.  The result of a call depends on its inputs alone (atomics
+ * only count, in integers).
  * A sequence whose position is negative, that has more tokens than
  * max_seq_tokens or than its table's max_blocks x N - positions[s], that names
  * a block id which is neither HKV_NULL_BLOCK nor in [0, num_blocks), or a block

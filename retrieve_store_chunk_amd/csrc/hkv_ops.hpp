@@ -245,6 +245,13 @@ constexpr uint32_t kPrefillPartTokens = 1200;
 // 256 42.4, 43.0; 256 of 16 heads 128.6, 125.7; 512 of 16 heads 240, 232; 1000 of 6 196, 183).
 constexpr uint32_t kPrefillLookThrough = 256;
 
+// Block ids are compared pair by pair up to so many whole blocks in the call's rows
+// (n_tokens / N), by counting in the workspace beyond: two launches more, but pairs grow
+// with the square, up to 2^30 for one thread (us in all, N = 16, one head of 128, counted and
+// compared: 2 runs of 8 blocks each 44, 46; of 16 59, 77; of 128 313, 1632; 8 runs of 2 36,
+// 32; of 4 41, 36; of 8 49, 49; one of 16 54, 51; of 64 148, 149).
+constexpr uint32_t kPrefillPairBlocks = 24;
+
 struct PrefillChunk {
   int32_t seq, row, len, off;  // its first token: row of the call, token of the sequence
   int32_t dst;                 // the block that its last token's state goes to, or none
@@ -272,6 +279,7 @@ struct PrefillArgs {
   float scale, eps;
   uint32_t num_blocks, block_tokens, max_blocks, n_seqs, n_tokens, max_seq_tokens;
   uint32_t heads, head_dim, taps;
+  uint32_t counted;         // the uses of blocks are counted, not compared
   uint32_t planned;         // a launch of its own looks the sequences through
   uint32_t chunked;         // sequences of more than short_tokens are computed in chunks
   uint32_t short_tokens;
@@ -280,6 +288,7 @@ struct PrefillArgs {
   uint32_t parts;           // that a sequence's chunks are cut into, 1 or at least 3
   // workspace
   int32_t* status;          // [n_seqs]: kPrefill* below
+  uint32_t* uses;           // [num_blocks][2]: entries and sources that name a block, if counted
   int32_t* first_chunk;     // [2][n_seqs], [1]: each sequence's first, how many; all of them
   PrefillChunk* chunks;     // [max_chunks]
   uint8_t* records;         // [max_chunks][heads][kPrefillRecord]
@@ -292,12 +301,14 @@ constexpr int32_t kPrefillRefused = 1;  // NaN in its rows, no page
 constexpr int32_t kPrefillNoRows = 2;   // nothing to do, or its rows are not known
 
 struct PrefillWorkspace {
-  uint64_t status, first_chunk, chunks, records, made, total;
+  uint64_t status, uses, first_chunk, chunks, records, made, total;
 };
+// `counted_blocks`: the pool's, where their uses are counted, else 0.
 inline PrefillWorkspace prefill_workspace(uint64_t n_seqs, uint64_t max_chunks, uint64_t heads,
-                                          uint64_t parts) {
+                                          uint64_t parts, uint64_t counted_blocks) {
   PrefillWorkspace w{};
-  w.first_chunk = w.status + align256(n_seqs * 4);
+  w.uses = w.status + align256(n_seqs * 4);
+  w.first_chunk = w.uses + align256(counted_blocks * 8);
   w.chunks = w.first_chunk + (max_chunks ? align256((2 * n_seqs + 1) * 4) : 0);
   w.records = w.chunks + align256(max_chunks * sizeof(PrefillChunk));
   w.made = w.records + max_chunks * heads * kPrefillRecord;

@@ -90,8 +90,9 @@ __device__ __forceinline__ uint32_t chunks_of(const hkv::PrefillArgs& a, const S
 
 // What a thread finds against sequence s, which shares the other sequences and the
 // sequence's blocks among a workgroup's threads: 1: its rows may be another's, 2: it is
-// refused.  Blocks are compared with those of all sequences: entries are few (a block
-// holds hundreds of tokens).
+// refused.  Blocks are compared with those of all sequences where the call has few, as
+// blocks of hundreds of tokens make it (at worst 26 entries with 26, on one thread);
+// otherwise they were counted.
 __device__ __forceinline__ uint32_t look_through(const hkv::PrefillArgs& a, uint32_t s,
                                                  const Span& me, uint32_t t, uint32_t threads) {
   uint32_t found = 0;
@@ -100,6 +101,17 @@ __device__ __forceinline__ uint32_t look_through(const hkv::PrefillArgs& a, uint
   if (!me.blocks || me.tokens > (int32_t)a.max_seq_tokens || outside(a.src[s], a.num_blocks))
     return found | 2u;
   bool bad = false;
+  if (a.counted) {
+    const int32_t from = a.src[s];
+    for (uint32_t j = me.first + t; j <= me.last; j += threads) {
+      const int32_t id = own[j];
+      bad |= outside(id, a.num_blocks);
+      if (id < 0 || (uint32_t)id >= a.num_blocks) continue;
+      const uint32_t* const uses = a.uses + (uint64_t)id * 2;
+      bad |= uses[0] > 1 || uses[1] > (id == from ? 1u : 0u);
+    }
+    return found | (bad ? 2u : 0u);
+  }
   for (uint32_t j = me.first + t; j <= me.last; j += threads) {
     const int32_t id = own[j];
     bad |= outside(id, a.num_blocks);
@@ -120,6 +132,27 @@ __device__ __forceinline__ uint32_t look_through(const hkv::PrefillArgs& a, uint
     }
   }
   return found | (bad ? 2u : 0u);
+}
+
+// How many entries and how many sources of the call's sequences name a block, one
+// workgroup a sequence: first the counts of the blocks that it names are cleared, then, in
+// a launch of its own, they are counted (integers: their order does not matter).
+__device__ __forceinline__ void count_uses(const hkv::PrefillArgs& a, bool clear) {
+  const uint32_t s = blockIdx.x, t = threadIdx.x;
+  const Span me = span_of(a, s);
+  if (me.tokens == 0) return;
+  auto use = [&](int32_t id, uint32_t which) {
+    if (id < 0 || (uint32_t)id >= a.num_blocks) return;
+    uint32_t* const uses = a.uses + (uint64_t)id * 2;
+    if (clear)
+      uses[0] = uses[1] = 0;
+    else
+      atomicAdd(uses + which, 1u);
+  };
+  if (t == 0) use(a.src[s], 1);
+  if (!me.blocks) return;
+  const int32_t* const own = a.table + (int64_t)s * a.table_stride;
+  for (uint32_t j = me.first + t; j <= me.last; j += kPlanThreads) use(own[j], 0);
 }
 
 // What becomes of a sequence (hkv.h), from what its threads found.
@@ -1648,6 +1681,14 @@ __device__ __forceinline__ void conv_states(const hkv::PrefillArgs& a, uint32_t 
 
 }  // namespace
 
+extern "C" __global__ __launch_bounds__(kPlanThreads) void hkv_kda_prefill_clear(
+    hkv::PrefillArgs a) {
+  count_uses(a, true);
+}
+extern "C" __global__ __launch_bounds__(kPlanThreads) void hkv_kda_prefill_count(
+    hkv::PrefillArgs a) {
+  count_uses(a, false);
+}
 extern "C" __global__ __launch_bounds__(kPlanThreads) void hkv_kda_prefill_plan(
     hkv::PrefillArgs a) {
   plan(a);
@@ -1721,9 +1762,15 @@ int launch_prefill(const PrefillArgs& a, int32_t dtype, void* stream) {
   void* params[] = {&arg};
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t e = hipSuccess;
-  if (a.planned)
-    e = hipLaunchKernel(HKV_FN(hkv_kda_prefill_plan), dim3(a.n_seqs), dim3(kPlanThreads), params, 0,
-                        st);
+  auto by_sequence = [&](const void* kernel) {
+    if (e == hipSuccess)
+      e = hipLaunchKernel(kernel, dim3(a.n_seqs), dim3(kPlanThreads), params, 0, st);
+  };
+  if (a.counted) {
+    by_sequence(HKV_FN(hkv_kda_prefill_clear));
+    by_sequence(HKV_FN(hkv_kda_prefill_count));
+  }
+  if (a.planned) by_sequence(HKV_FN(hkv_kda_prefill_plan));
   if (e != hipSuccess) return (int)e;
   if (a.chunked) {
     static const void* const kForm[2] = {HKV_FN(hkv_kda_form_bf16), HKV_FN(hkv_kda_form_fp16)};

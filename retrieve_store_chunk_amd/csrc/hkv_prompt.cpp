@@ -212,7 +212,8 @@ hkv_status plan_prefill(const hkv_layout* layout, const hkv_kda_prefill_args* a,
   k->chunked = d == (int64_t)hkv::kPrefillChunkDim && taps == 4 && es == 2 &&
                k->max_seq_tokens > (k->n_seqs > 1 ? hkv::kPrefillTokens
                                                   : hkv::kPrefillTokensOne);
-  k->planned = k->chunked || k->n_seqs > hkv::kPrefillLookThrough;
+  k->counted = k->n_tokens / k->block_tokens > hkv::kPrefillPairBlocks;
+  k->planned = k->chunked || k->counted || k->n_seqs > hkv::kPrefillLookThrough;
   // A sequence's blocks are cut each on its own: the last chunk of the first, of
   // the last and of every whole block may be short.
   if (k->chunked)
@@ -232,7 +233,8 @@ hkv_status plan_prefill(const hkv_layout* layout, const hkv_kda_prefill_args* a,
   const uint32_t fit = 256 / (pairs * 8 > 0 ? pairs * 8 : 1) + 1;  // one workgroup a CU
   if (k->chunked && fit >= 4 && k->max_seq_tokens >= hkv::kPrefillPartTokens)
     k->parts = std::min<uint32_t>(fit, 8);
-  *w = hkv::prefill_workspace(k->n_seqs, k->max_chunks, k->heads, k->parts);
+  *w = hkv::prefill_workspace(k->n_seqs, k->max_chunks, k->heads, k->parts,
+                              k->counted ? k->num_blocks : 0);
   return HKV_OK;
 }
 
@@ -318,6 +320,7 @@ hkv_status prefill(const hkv_layout* layout, void* pool, const hkv_kda_prefill_a
   k.eps = a->eps;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   k.status = reinterpret_cast<int32_t*>(wsb + w.status);
+  k.uses = reinterpret_cast<uint32_t*>(wsb + w.uses);
   k.first_chunk = reinterpret_cast<int32_t*>(wsb + w.first_chunk);
   k.chunks = reinterpret_cast<hkv::PrefillChunk*>(wsb + w.chunks);
   k.records = wsb + w.records;
