@@ -671,12 +671,16 @@ hkv_status hkv_mla_append(const hkv_layout* layout, void* pool, const hkv_mla_ap
  * HKV_NULL_BLOCK is not written (snapshots that are not kept).  The source may
  * be one of the sequence's own blocks.  A sequence without new tokens reads and
  * writes nothing.
- * Sums, norms, decays and states are fp32.  Longer runs of heads of 128 with
- * conv_kernel 4 in bf16 or fp16 are computed in chunks of up to 64 tokens, whose
- * products take each operand as two fp16 terms (22 bits): a column of the state
- * is off from the token-by-token one by about 1e-6 of the largest value that it, or
- * the values v that it takes in, had in the chunk and the one before.  There, a
- * NaN or an infinity may also reach outputs of its head up to 63 rows before it. */
+ * Sums, norms, decays and states are fp32, with the hardware's exponential and
+ * reciprocals in SiLU, decays and norms: a decay of e^-x is off by up to about
+ * 6e-8 (1 + x) of itself.  Longer runs of heads of 128 with conv_kernel 4 in bf16
+ * or fp16 are computed in chunks of up to 64 tokens, whose products take each
+ * operand as two fp16 terms (22 bits): a chunk adds to a column of the state an
+ * error of up to about 1e-6 of the largest value that it, or the values v that it
+ * takes in, had in the chunk and the one before, which fades as the state does.
+ * The bound is the column's: rows far below its largest value (those of key
+ * channels near zero) keep fewer bits of their own.  In chunks a NaN or an
+ * infinity may also reach outputs of its head up to 63 rows before it. */
 typedef struct hkv_kda_prefill_args {
   int32_t layer;             /* a KDA layer */
   int32_t n_seqs;            /* 0..4096; 0 is a no-op */
@@ -709,15 +713,15 @@ typedef struct hkv_kda_prefill_args {
  * it is mostly 141 KiB for each head of each of the C = n_tokens / 64 + n_tokens / N +
  * 2 n_seqs chunks that there may be (N: tokens of a block), about 2.2 KB a token and
  * head for long runs; 8 bytes for each of the pool's blocks where n_tokens / N is over 24.
- * Errors: HKV_E_ARG (also where C x heads is over 2^23 - 1 in
- * chunks, or n_seqs x heads over 2^20). */
+ * Errors: HKV_E_ARG (also where C x heads is over 2^23 - 1 in chunks, or n_seqs x heads
+ * over 2^20). */
 hkv_status hkv_kda_prefill_workspace(const hkv_layout* layout, const hkv_kda_prefill_args* args,
                                      size_t* bytes);
 
 /* Enqueues the prefill (see above).  Needs of the layout what hkv_kda_step
  * needs; pool, out and workspace are 16-byte aligned, the other arrays by their
- * element.  The result of a call depends on its inputs alone (atomics
- * only count, in integers).
+ * element.  The result of a call depends on its inputs alone (no atomics but
+ * on integers, whose order does not matter).
  * A sequence whose position is negative, that has more tokens than
  * max_seq_tokens or than its table's max_blocks x N - positions[s], that names
  * a block id which is neither HKV_NULL_BLOCK nor in [0, num_blocks), or a block

@@ -228,8 +228,10 @@ constexpr uint32_t kPrefillChunkDim = 128;   // the head dim that is computed in
 constexpr uint32_t kPrefillRecord = 3 * 32768 + 12288 + 32768 + 1024;  // bytes of a chunk and head
 
 // Calls whose longest run has up to so many tokens go token by token (us, token by token
-// and in chunks: 61 runs of up to 16 tokens, 6 heads 43, 66; 24 60, 72; 32 76, 73; one run
-// of 12 20, 27; 16 25, 26; 20 31, 27).  In others, runs of up to kPrefillShort do, in a
+// and in chunks: 61 runs of up to 16 tokens, 6 heads 45, 67; 24 62, 68; 32 79, 73; 61 runs
+// of 32 heads, which fill the card either way, 24 167, 290; 48 305, 297; 16 runs of 6 heads
+// 24 38, 38; 32 49, 38; of 32 heads 24 58, 71; 32 73, 72; 4 runs, 6 or 32 heads 16 27, 30
+// and 38; 24 37, 30 and 38; one run of 12 21, 27; 16 26, 26; 24 37, 27).  In others, runs of up to kPrefillShort do, in a
 // launch of their own (24 runs of one token beside 4 prompts of up to 1400, 32 heads: 256
 // us; 331 with all in chunks; 61 runs of up to 12, all in chunks but those: 73 with 2, 74 with
 // 4, 65 with 8; of up to 16 66, 72 and 69; of up to 32 73, 72 and 83).  A call of one sequence has no such launch.
@@ -238,6 +240,9 @@ constexpr uint32_t kPrefillShort = 2;
 // Runs are cut into parts where that makes at least 4 with one workgroup a CU, from so many
 // tokens of the longest on (us in all, one part and cut: 1500 tokens, 6 heads 64, 60; 16384
 // 488, 279 to 291; with 16 heads, which leave room for 3 parts, 1887 tokens 83, 80, and 90 in 4).  8 at most.
+// The room counts all sequences of the call, short ones too, since the host does not know
+// which are: beside single tokens a long run is not cut (16384 tokens, 6 heads 285 alone,
+// 504 beside one token, 638 beside 8, 648 beside 30).
 constexpr uint32_t kPrefillPartTokens = 1200;
 
 // Up to so many sequences are looked through by every workgroup of the token-by-token
@@ -285,7 +290,7 @@ struct PrefillArgs {
   uint32_t short_tokens;
   uint32_t max_chunks;
   uint32_t column_tiles;    // of 16 columns a scanning workgroup, 1 or 2
-  uint32_t parts;           // that a sequence's chunks are cut into, 1 or at least 3
+  uint32_t parts;           // that a sequence's chunks are cut into: 1, or 4 to 8
   // workspace
   int32_t* status;          // [n_seqs]: kPrefill* below
   uint32_t* uses;           // [num_blocks][2]: entries and sources that name a block, if counted

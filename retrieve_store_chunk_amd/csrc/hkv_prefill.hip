@@ -6,12 +6,13 @@
 // inputs always go token by token.  `plan` looks the sequences through.
 //
 // Bound: the inputs, outputs and pages for short runs (61 runs of up to 5 tokens, 6 heads:
-// 20 us for 50 MB; a longer run takes 1.2 to 1.4 us a token, its chain); for chunks
+// 20 us for 50 MB) and a token's chain for longer ones (1500 tokens, us a token: heads of
+// 16 to 64 0.7 to 0.9, of 128 1.4 to 1.5, of 256 2.9 to 3.1, which spill); for chunks
 // `form`'s arithmetic and, where a sequence has few heads, `scan`'s chain from chunk to
-// chunk.  Measured (us, form + scan): 1500 tokens, 6 heads 24 + 31; 1887 tokens, 16 heads
-// 34 + 45; 16384 tokens, 6 heads 88 + 202 (in parts); 20011 tokens, 32 heads 532 to 592
-// + 705; 16 runs of up to 2000, 32 heads 487 to 583 + 446, for 1.0 GB each, of which a copy
-// at 4.7 TB/s would take 0.21 ms.
+// chunk.  Measured (us, form + scan): 1500 tokens, 6 heads 24 + 30; 1887 tokens, 16 heads
+// 34 + 45; 16384 tokens, 6 heads 88 + 200 (in parts); 20011 tokens, 32 heads 528 to 597
+// + 685 to 724; 16 runs of up to 2000, 32 heads 487 to 583 + 422 to 463, for 1.0 GB each, of
+// which a copy at 4.7 TB/s would take 0.21 ms.
 #include <hip/hip_runtime.h>
 
 #include "hkv.h"
@@ -256,12 +257,15 @@ __device__ __forceinline__ float inverse_root(float x) {
 }
 
 // ---------------------------------------------------------------- token by token
-// hkv_kda_step's arithmetic with the state and the conv's taps kept in registers
-// from token to token: one workgroup per (head, sequence), a wave for 16 columns.
-// Thread t has 4 columns of kDim / 16 rows, so that the sums over rows stay within a
+// hkv_kda_step's recurrence with the state and the conv's taps kept in registers
+// from token to token, and the hardware's exp2, rcp and rsq where the step has expf, a
+// division and sqrtf, since they lie on a token's chain (x log2 e is rounded to fp32: a
+// decay of e^-x is off by up to 6e-8 (1 + x) of itself).  One workgroup per (head,
+// sequence), a wave for 16 columns.  Thread t has 4 columns of kDim / 16 rows, so that the sums over rows stay within a
 // wave, and one channel of the conv or of the decays; the only thing that the waves
 // exchange is a token's q, k, v and decays: one barrier a token (61 runs of up to
-// 5 tokens, 6 heads: 20 us; the form before, without this split, 28).
+// 5 tokens, 6 heads: 20 us; the form before, without this split, 28).  Heads of 256 have
+// 1024 threads and so 128 registers, of which 20 (bf16, fp16) or 22 (fp32) are spilled.
 template <class T, uint32_t kDim>
 __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
   using E = typename T::type;
@@ -446,10 +450,12 @@ __device__ __forceinline__ void tokens(const hkv::PrefillArgs& a) {
 // lo (22 bits), and three products (lo lo is below 2^-22); what is scaled by a
 // power of two to lie well inside fp16's range says so.  V's and S's columns never
 // mix, so each has a power of two of its own.  (Two bf16 terms would have
-// 16 bits.)
+// 16 bits.)  The low term is a multiple of 2^-24 like all of fp16, so what is far below its
+// scale has fewer bits: 2^-25 of 16 k in K, say, is 2^-29 of the longest key, far below
+// the column's own rounding, but all that a channel of 1e-6 of a key has for its row.
 //
 // `form`: one workgroup of eight waves a chunk and head, a wave 8 tokens, a lane two
-// channels.  With 20011 tokens of 32 heads a wave has 2290 vector instructions and waits 37%
+// channels.  With 20011 tokens of 32 heads a wave has 2290 vector instructions and waits 36%
 // of its cycles, LDS is active in 37% of a CU's (37% of that are conflicts), the matrix
 // units in 11%.  Four waves of 16 tokens, with the halves of 16 tokens pair by pair, took
 // 569 us there where this split first took 554.  Two workgroups a CU: 80 KB of LDS, 128 registers.
@@ -1196,7 +1202,7 @@ __device__ __forceinline__ void form(const hkv::PrefillArgs& a, uint32_t slot, u
 // products take them: two barriers a chunk.
 //
 // A chunk takes 1.45 us (16 columns), of which 0.75 are the 116 KB that a CU takes in at
-// 64 bytes a cycle; 2.2 us with 256 workgroups at once, which the caches bound.  Before:
+// 64 bytes a cycle; 2.2 us with 256 workgroups at once whose records come from HBM.  Before:
 // one wave of 16 columns a workgroup, its operands as they were needed, 13 to 20 us; two
 // waves computing and two staging through LDS 3.4 us.  Operands two chunks ahead were no
 // faster (20011 tokens, 32 heads in all: 1191 us for 1166).

@@ -227,7 +227,8 @@ hkv_status plan_prefill(const hkv_layout* layout, const hkv_kda_prefill_args* a,
   // 16 columns a scanning workgroup while each has a CU to itself, else 32, which read a
   // record half as often (us in all, 16 and 32 columns: 1887 tokens, 16 heads 83, 102; 20011
   // tokens, 32 heads 1167, 1266; 4 prompts and 24 single tokens, 32 heads 308, 262; 16
-  // prompts, 32 heads 1055, 901).
+  // prompts, 32 heads 1055, 901).  All sequences count, short ones too: 20011 tokens beside
+  // one single token, 32 heads, go by 32 columns, 1274 for 1159 alone.
   k->column_tiles = pairs * 8 > 256 ? 2 : 1;
   k->parts = 1;
   const uint32_t fit = 256 / (pairs * 8 > 0 ? pairs * 8 : 1) + 1;  // one workgroup a CU
