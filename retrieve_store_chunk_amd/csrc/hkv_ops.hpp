@@ -231,8 +231,8 @@ constexpr uint32_t kPrefillRecord = 3 * 32768 + 12288 + 32768 + 1024;  // bytes 
 // and in chunks: 61 runs of up to 16 tokens, 6 heads 45, 67; 24 62, 68; 32 79, 73; 61 runs
 // of 32 heads, which fill the card either way, 24 167, 290; 48 305, 297; 16 runs of 6 heads
 // 24 38, 38; 32 49, 38; of 32 heads 24 58, 71; 32 73, 72; 4 runs, 6 or 32 heads 16 27, 30
-// and 38; 24 37, 30 and 38; one run of 12 21, 27; 16 26, 26; 24 37, 27).  In others, runs of up to kPrefillShort do, in a
-// launch of their own (24 runs of one token beside 4 prompts of up to 1400, 32 heads: 256
+// and 38; 24 37, 30 and 38; one run of 12 21, 27; 16 26, 26; 24 37, 27).  In others, runs
+// of up to kPrefillShort do, in a launch of their own (24 runs of one token beside 4 prompts of up to 1400, 32 heads: 256
 // us; 331 with all in chunks; 61 runs of up to 12, all in chunks but those: 73 with 2, 74 with
 // 4, 65 with 8; of up to 16 66, 72 and 69; of up to 32 73, 72 and 83).  A call of one sequence has no such launch.
 constexpr uint32_t kPrefillTokens = 24, kPrefillTokensOne = 16;

@@ -261,8 +261,8 @@ __device__ __forceinline__ float inverse_root(float x) {
 // from token to token, and the hardware's exp2, rcp and rsq where the step has expf, a
 // division and sqrtf, since they lie on a token's chain (x log2 e is rounded to fp32: a
 // decay of e^-x is off by up to 6e-8 (1 + x) of itself).  One workgroup per (head,
-// sequence), a wave for 16 columns.  Thread t has 4 columns of kDim / 16 rows, so that the sums over rows stay within a
-// wave, and one channel of the conv or of the decays; the only thing that the waves
+// sequence), a wave for 16 columns.  Thread t has 4 columns of kDim / 16 rows, so that the
+// sums over rows stay within a wave, and one channel of the conv or of the decays; the only thing that the waves
 // exchange is a token's q, k, v and decays: one barrier a token (61 runs of up to
 // 5 tokens, 6 heads: 20 us; the form before, without this split, 28).  Heads of 256 have
 // 1024 threads and so 128 registers, of which 20 (bf16, fp16) or 22 (fp32) are spilled.
